@@ -163,19 +163,19 @@ def _run_own(s):
     op = s["op"]
     if op == "roundtrip":
         r, k = s["R"], s["K"]
-        q = tg.quant_mxfp4(s["x"], s["dims"])
+        q = tg.mxfp4_quant(s["x"], s["dims"])
         if s["dims"] == "rows":
-            return tg.dequant_mxfp4(q[0], q[1], k)
+            return tg.mxfp4_dequant(q[0], q[1], k)
         if s["dims"] == "cols":
-            return tg.dequant_mxfp4(q[0], q[1], r)
-        return tg.dequant_mxfp4(q[0], q[1], k), tg.dequant_mxfp4(q[2], q[3], r)
+            return tg.mxfp4_dequant(q[0], q[1], r)
+        return tg.mxfp4_dequant(q[0], q[1], k), tg.mxfp4_dequant(q[2], q[3], r)
     if op == "mxfp4":
-        return tg.gemm_mxfp4(s["a"], s["sa"], s["b"], s["sb"], relu=s["relu"])
+        return tg.mxfp4_gemm(s["a"], s["sa"], s["b"], s["sb"], relu=s["relu"])
     if op == "train":
         y = tg.Mxfp4LinearFunction.apply(s["x"], s["w"])
         return (y.detach(), *torch.autograd.grad(y, (s["x"], s["w"]), s["dy"]))
     if op == "weight":
-        return tg.gemm_f16_mxfp4(s["x"], s["q"], s["s"], relu=s["relu"])
+        return tg.mxfp4_gemm_f16(s["x"], s["q"], s["s"], relu=s["relu"])
     if op == "tune":
         y = tg.Mxfp4WeightFunction.apply(s["x"], s["q"], s["s"])
         return (y.detach(), *torch.autograd.grad(y, (s["x"],), s["dy"]))
