@@ -18,7 +18,14 @@ the fp8 (E4M3) block-scaled path: ``gemm_fp8_block`` (``gemm_fp8_block_cfg`` as
 ``tgemm_fp8_select_config``, and ``fp8_block_scaled_linear`` (quantize x per 1 x 128
 block, then the block-scaled GEMM against an fp8 weight). ``matmul`` takes row- or
 column-major operand views and picks the layout; ``GemmFunction`` is the autograd wrapper (backward: dA = dC B^T, dB = A^T dC
-through gemm_f16_ex). The tooling
+through gemm_f16_ex).
+
+The operators of ``include/tgemm_ops.h``: MXFP4 (4-bit microscaled) matrices in
+``mxfp4.py`` (``mxfp4_quant``, ``mxfp4_dequant``, ``mxfp4_gemm``, ``mxfp4_gemm_f16``,
+``mxfp4_linear``, and the autograd forms ``Mxfp4LinearFunction`` and
+``Mxfp4WeightFunction``).
+
+The tooling
 twin ``libtgemm_stamps.so`` (``stamps_lib()``, measurement tools only) compiles every config
 row (the sweep-only variants too; ``built`` in a config description says whether the
 library at hand has the row) and adds ``tgemm_stamps_capacity``, ``tgemm_stamps_read``,
@@ -163,6 +170,8 @@ def _load(path: str, stamps: bool) -> ctypes.CDLL:
     L.tgemm_fp8_config_desc.argtypes = [i32, ctypes.POINTER(ConfigInfo)]
     L.tgemm_fp8_select_config.restype = i32
     L.tgemm_fp8_select_config.argtypes = [i64, i64, i64, p, i64, p, i64, p, i64]
+    for name, (restype, argtypes) in OPS_SIGNATURES.items():
+        getattr(L, name).restype, getattr(L, name).argtypes = restype, argtypes
     if stamps:
         L.tgemm_stamps_capacity.restype = i32
         L.tgemm_stamps_capacity.argtypes = [ctypes.POINTER(i32), ctypes.POINTER(i32)]
@@ -660,6 +669,9 @@ def __getattr__(name):
         fn = _autograd_function()
         globals()["GemmFunction"] = fn
         return fn
+    if name in ("Mxfp4LinearFunction", "Mxfp4WeightFunction"):
+        globals().update(mxfp4.autograd_functions())
+        return globals()[name]
     raise AttributeError(name)
 
 
@@ -796,3 +808,14 @@ def fp8_block_scaled_linear(x, w_fp8, scale_w, block: int = 128, relu: bool = Fa
         raise ValueError(f"only block = {FP8_BLOCK} is supported")
     xq, sx = quant_fp8_block(x, 1, stream=stream)
     return gemm_fp8_block(xq, sx, w_fp8, scale_w, c=out, relu=relu, stream=stream)
+
+
+# ---------------------------------------------------------------- the operators of tgemm_ops.h
+from . import mxfp4  # noqa: E402
+from .mxfp4 import (MX_128, MX_256, MX_BLOCK, MX_BLOCK_BYTES, MX_GENERIC, MX_MAX_DIM, MX_SKINNY,  # noqa: E402,F401
+                    MX_SKINNY_ROWS, mxfp4_dequant, mxfp4_empty, mxfp4_gemm, mxfp4_gemm_f16, mxfp4_linear, mxfp4_quant,
+                    mxfp4_select_config)
+
+OPS_SIGNATURES = {**mxfp4.SIGNATURES}
+# Every symbol include/tgemm_ops.h declares.
+OPS_EXPORTS = tuple(OPS_SIGNATURES)

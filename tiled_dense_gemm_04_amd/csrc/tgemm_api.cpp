@@ -367,6 +367,11 @@ int fp8_run(int cfg, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda
 
 }  // namespace
 
+namespace tgemm {
+int current_device(int* device);  // declared in tgemm_mx.h and tgemm_orth.h
+int current_device(int* device) { return check_device(device); }
+}  // namespace tgemm
+
 extern "C" {
 
 int gemm_fp8_block(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const float* scale_a,

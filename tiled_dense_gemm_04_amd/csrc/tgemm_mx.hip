@@ -1,0 +1,761 @@
+// tgemm_mx.hip -- gfx950 kernels of the MXFP4 operators: the quantiser and its inverse, the
+// product of two MXFP4 matrices, and the product of a binary16 matrix with an MXFP4 weight.
+//
+// An MXFP4 matrix holds E2M1 codes (0, .5, 1, 1.5, 2, 3, 4, 6 and a sign) in blocks of 32
+// along k, each with one E8M0 scale 2^(s - 127). Rows hold whole blocks (16 bytes each), zero
+// codes past K:
+//   quantiser:  s = floor(log2 max|x|) - 2 + 127, code = E2M1(x 2^(127 - s)), to nearest even,
+//               saturated at 6 (7 < x 2^.. < 8 rounds past the grid);
+//   products:   C[i,j] = ReLU?( sum_kb 2^(sa + sb - 254) sum_{k in kb} a[i,k] b[j,k] ), or with
+//               binary16 A and the weight decoded to binary16, sum_k a[i,k] half(2^(sb - 127)
+//               b[j,k]), both summed in float32 and rounded to binary16 once.
+#include "tgemm_mx.h"
+#include "tgemm_pingpong.h"
+
+#include <atomic>
+
+namespace tgemm {
+namespace {
+
+typedef int int8v __attribute__((ext_vector_type(8)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef unsigned short ushort2v __attribute__((ext_vector_type(2)));
+typedef unsigned int uint2v __attribute__((ext_vector_type(2)));
+typedef unsigned int uint4v __attribute__((ext_vector_type(4)));
+
+// Loads and stores of any alignment (gfx950 serves them; the compiler emits one wide access).
+template <typename V>
+__device__ __forceinline__ V load_any(const void* p) {
+  V v;
+  __builtin_memcpy(&v, p, sizeof(V));
+  return v;
+}
+template <typename V>
+__device__ __forceinline__ void store_any(void* p, const V& v) {
+  __builtin_memcpy(p, &v, sizeof(V));
+}
+
+// 2^(s - 127) as float32; s = 0 is a subnormal, 255 a NaN.
+__device__ __forceinline__ float scale_f32(uint32_t s) {
+  return __uint_as_float(s == 255 ? 0x7FC00000u : s == 0 ? 0x00400000u : s << 23);
+}
+
+// Lane permutations inside groups of four lanes.
+__device__ __forceinline__ uint32_t quad_xor1(uint32_t x) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0xB1, 0xF, 0xF, true); }
+__device__ __forceinline__ uint32_t quad_xor2(uint32_t x) { return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, 0x4E, 0xF, 0xF, true); }
+
+// Magnitudes of binary16 values order like their bit patterns, infinities and NaN at the top.
+__device__ __forceinline__ uint32_t pk_max(uint32_t a, uint32_t b) {
+  const ushort2v x = __builtin_bit_cast(ushort2v, a), y = __builtin_bit_cast(ushort2v, b);
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(x, y));
+}
+constexpr uint32_t kAbs2 = 0x7FFF7FFFu;
+
+// The scale byte of a block whose largest magnitude has binary16 bits h: the exponent of that
+// magnitude minus 2 (E2M1's largest exponent), 127 (a scale of one) for a block of zeros, 255
+// where the block holds an infinity or a NaN. Every nonzero magnitude (at least 2^-24) is a
+// normal float32, so its exponent field is the logarithm.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t h) {
+  const float f = (float)__builtin_bit_cast(_Float16, (unsigned short)h);
+  const uint32_t e = (__float_as_uint(f) >> 23) - 2;
+  return h == 0 ? 127u : h >= 0x7C00u ? 255u : e;
+}
+
+// Two binary16 values to two E2M1 codes in byte B of a word: x / scale to nearest even,
+// saturated at 6 (gfx950's conversion; checked code by code against the definition).
+template <int B>
+__device__ __forceinline__ uint32_t fp4_pack(uint32_t old, uint32_t x, float scale) {
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(old, __builtin_bit_cast(half2v, x), scale, B);
+}
+// Eight binary16 values (four words) to eight codes; a block with scale byte 255 gets zeros.
+__device__ __forceinline__ uint32_t fp4_pack8(const uint4v& x, uint32_t sb) {
+  const float s = __uint_as_float(sb << 23);
+  uint32_t w = 0;
+  w = fp4_pack<0>(w, x[0], s);
+  w = fp4_pack<1>(w, x[1], s);
+  w = fp4_pack<2>(w, x[2], s);
+  w = fp4_pack<3>(w, x[3], s);
+  return sb == 255 ? 0u : w;
+}
+
+// Eight consecutive binary16 values from p, those at or past `n` zero.
+__device__ __forceinline__ uint4v load8(const _Float16* p, int n) {
+  uint4v v = {0, 0, 0, 0};
+  if (n >= 8) {
+    v = load_any<uint4v>(p);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (e < n) v[e / 2] |= (uint32_t)__builtin_bit_cast(unsigned short, p[e]) << (16 * (e % 2));
+  }
+  return v;
+}
+
+// ------------------------------------------------------------------------------------
+// Quantiser along the rows. Four lanes per block, eight values (16 bytes) each, NB blocks per
+// group of lanes with all loads issued first; block b of the matrix is block b % KB of row
+// b / KB, so consecutive groups of lanes read consecutive memory. Bound by memory: 2 bytes
+// read and 17/32 written per value.
+template <int NB>
+__global__ __launch_bounds__(256) void quant_mxfp4_rows(MxQuantArgs q) {
+  const uint32_t KB = (uint32_t)((q.K - 1) / kMxBlock + 1);
+  const uint64_t nblk = (uint64_t)q.R * KB;
+  const int sub = threadIdx.x & 3;
+  const uint64_t first = (uint64_t)blockIdx.x * (64 * NB) + (threadIdx.x >> 2);
+  uint4v x[NB];
+  uint32_t row[NB], kb[NB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const uint64_t b = first + 64 * i;  // the host keeps the number of blocks below 2^32
+    row[i] = (uint32_t)b / KB;
+    kb[i] = (uint32_t)b - row[i] * KB;
+    x[i] = (uint4v){0, 0, 0, 0};
+    if (b < nblk) x[i] = load8(q.X + (int64_t)row[i] * q.ldx + kb[i] * kMxBlock + 8 * sub, q.K - (int)(kb[i] * kMxBlock + 8 * sub));
+  }
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    uint32_t m = pk_max(pk_max(x[i][0] & kAbs2, x[i][1] & kAbs2), pk_max(x[i][2] & kAbs2, x[i][3] & kAbs2));
+    m = pk_max(m, quad_xor1(m));
+    m = pk_max(m, quad_xor2(m));
+    const uint32_t sb = scale_byte(m >> 16 > (m & 0xFFFF) ? m >> 16 : m & 0xFFFF);
+    if (first + 64 * i >= nblk) continue;
+    store_any(q.Q + (int64_t)row[i] * q.ldq + kb[i] * kMxBlockBytes + 4 * sub, fp4_pack8(x[i], sb));
+    if (sub == 0) q.S[(int64_t)row[i] * q.lds + kb[i]] = (uint8_t)sb;
+  }
+}
+
+// ------------------------------------------------------------------------------------
+// Quantiser along the columns (blocks of 32 rows, codes of X^T), and with ROWS along the rows
+// in the same pass over X. A workgroup takes 256 rows x 128 columns. Wave w takes row blocks
+// w and w + 4; a lane holds 8 rows x 8 columns of a block (lane % 16: columns, lane / 16:
+// rows), so a row of the tile is one 256-byte load, a column's maximum is one over the lane's
+// rows and two lane swaps, and a row block's one over four neighbouring lanes. The codes of
+// X^T cross the workgroup through LDS ([128 columns][8 blocks of 16 bytes], block j of column
+// c at place j ^ (c / 8) % 8, which spreads the sixteen columns groups written at once over
+// the banks) and leave as 128 contiguous bytes per column.
+template <bool ROWS>
+__global__ __launch_bounds__(256) void quant_mxfp4_cols(MxQuantArgs q) {
+  __shared__ __attribute__((aligned(16))) uint8_t codes[128 * 128];
+  __shared__ __attribute__((aligned(8))) uint8_t scales[128 * 8];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int cg = lane & 15, sub = lane >> 4;
+  const uint32_t tiles_c = (uint32_t)((q.K + 127) / 128);
+  const int r0 = (int)(blockIdx.x / tiles_c) * 256, c0 = (int)(blockIdx.x % tiles_c) * 128;
+  const int RB = (q.R - 1) / kMxBlock + 1, rb0 = r0 / kMxBlock;
+  const int col = c0 + 8 * cg;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int j = wave + 4 * h;
+    const int row = r0 + j * kMxBlock + 8 * sub;
+    uint4v x[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      x[r] = (uint4v){0, 0, 0, 0};
+      if (row + r < q.R && col < q.K) x[r] = load8(q.X + (int64_t)(row + r) * q.ldx + col, q.K - col);
+    }
+    if (ROWS) {
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        uint32_t m = pk_max(pk_max(x[r][0] & kAbs2, x[r][1] & kAbs2), pk_max(x[r][2] & kAbs2, x[r][3] & kAbs2));
+        m = pk_max(m, quad_xor1(m));
+        m = pk_max(m, quad_xor2(m));
+        const uint32_t sb = scale_byte(m >> 16 > (m & 0xFFFF) ? m >> 16 : m & 0xFFFF);
+        // a block that starts inside the row is written whole, zero codes past K
+        if (row + r < q.R && (col & ~(kMxBlock - 1)) < q.K) {
+          store_any(q.Q + (int64_t)(row + r) * q.ldq + col / 2, fp4_pack8(x[r], sb));
+          if ((cg & 3) == 0) q.S[(int64_t)(row + r) * q.lds + col / kMxBlock] = (uint8_t)sb;
+        }
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {  // columns 2p and 2p + 1
+      uint32_t m = 0;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) m = pk_max(m, x[r][p] & kAbs2);
+      m = pk_max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+      m = pk_max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+      const uint32_t sb0 = scale_byte(m & 0xFFFF), sb1 = scale_byte(m >> 16);
+      uint4v lo, hi;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        lo[r] = __builtin_amdgcn_perm(x[2 * r + 1][p], x[2 * r][p], 0x05040100);
+        hi[r] = __builtin_amdgcn_perm(x[2 * r + 1][p], x[2 * r][p], 0x07060302);
+      }
+      const int at = 8 * cg + 2 * p, place = ((j ^ (cg & 7)) << 4) + 4 * sub;
+      *(TG_LDS uint32_t*)(codes + at * 128 + place) = fp4_pack8(lo, sb0);
+      *(TG_LDS uint32_t*)(codes + (at + 1) * 128 + place) = fp4_pack8(hi, sb1);
+      if (sub == 0) {
+        *(TG_LDS uint8_t*)(scales + at * 8 + j) = (uint8_t)sb0;
+        *(TG_LDS uint8_t*)(scales + (at + 1) * 8 + j) = (uint8_t)sb1;
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int u = i * 256 + threadIdx.x, c = u >> 3, j = u & 7;
+    const uint4v v = *(const TG_LDS uint4v*)(codes + c * 128 + ((j ^ ((c >> 3) & 7)) << 4));
+    if (c0 + c < q.K && rb0 + j < RB) {
+      store_any(q.QT + (int64_t)(c0 + c) * q.ldqt + (int64_t)(rb0 + j) * kMxBlockBytes, v);
+      q.ST[(int64_t)(c0 + c) * q.ldst + rb0 + j] = *(const TG_LDS uint8_t*)(scales + c * 8 + j);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------
+// Codes and scales to binary16 values, each rounded to nearest even (only scales outside
+// 2^-23 .. 2^13 make values that binary16 does not hold; those past its range become
+// infinite, a scale byte of 255 gives NaN). Four lanes per block, eight values (16 bytes
+// written) each, NB blocks per group of lanes. Bound by memory.
+__device__ __forceinline__ half8 decode8(uint32_t w, uint32_t sb) {
+  const float s = scale_f32(sb);
+  const half2v a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1);
+  const half2v c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 3);
+  return (half8){a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+template <int NB>
+__global__ __launch_bounds__(256) void dequant_mxfp4_rows(MxDequantArgs q) {
+  const uint32_t KB = (uint32_t)((q.K - 1) / kMxBlock + 1);
+  const uint64_t nblk = (uint64_t)q.R * KB;
+  const int sub = threadIdx.x & 3;
+  const uint64_t first = (uint64_t)blockIdx.x * (64 * NB) + (threadIdx.x >> 2);
+  uint32_t w[NB], sb[NB], row[NB], kb[NB];
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    const uint64_t b = first + 64 * i;
+    row[i] = (uint32_t)b / KB;
+    kb[i] = (uint32_t)b - row[i] * KB;
+    if (b < nblk) {
+      w[i] = load_any<uint32_t>(q.Q + (int64_t)row[i] * q.ldq + kb[i] * kMxBlockBytes + 4 * sub);
+      sb[i] = q.S[(int64_t)row[i] * q.lds + kb[i]];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NB; ++i) {
+    if (first + 64 * i >= nblk) continue;
+    const int k = (int)(kb[i] * kMxBlock) + 8 * sub;
+    _Float16* const p = q.X + (int64_t)row[i] * q.ldx + k;
+    const half8 v = decode8(w[i], sb[i]);
+    if (k + 8 <= q.K) {
+      store_any(p, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (k + e < q.K) p[e] = v[e];
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------
+// Product of two MXFP4 matrices, ping-pong kernel. One v_mfma_scale_f32_16x16x128_f8f6f4
+// multiplies 16 x 128 by 128 x 16 codes and applies both operands' block scales itself: lane
+// l's 16 bytes of an operand are one whole block (row l % 16, block l / 16 of the four) and
+// its scale byte sits in a register beside it, so nothing is folded outside the MFMA.
+// A k-tile of 128 codes is 64 bytes a row, the bytes of a binary16 k-tile of 32: operand
+// copies, range-checked edges, swizzle and the four-slot ring are the binary16 ping-pong's
+// (PpOperand on code rows seen as halves).
+// Scales come in groups of four k-tiles, 16 bytes a row and one 16-byte copy per row, in a
+// ring of two groups: group s goes with tile 4 s, when the last read of group s - 2 (tile
+// 4 s - 5) lies a barrier back. In the last group bytes past KB are whatever the padding
+// holds: a lane whose block lies past KB takes the last block's scale instead, and its codes
+// are zeros (out-of-range copies).
+// Requirements (host): A, B, SA, SB 16-byte aligned, their row strides multiples of 16.
+struct MxScaleRing {
+  static constexpr int GROUP = 4;  // k-tiles per group
+};
+
+template <int BM, int BN, int WM, int WN, int STAGES>
+constexpr int mx_lds_bytes() {
+  return STAGES * (BM + BN) * 64 + 2 * (BM + BN) * 16;
+}
+
+template <int BM, int BN, int WM, int WN, int STAGES, int PANEL>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_mxfp4_pp(MxGemmArgs g) {
+  constexpr int NW = WM * WN, WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
+  using OpA = PpOperand<BM, 32, 16, true, NW>;
+  using OpB = PpOperand<BN, 32, 16, true, NW>;
+  constexpr int A_BYTES = OpA::BYTES, B_BYTES = OpB::BYTES, PT = OpA::LD + OpB::LD;
+  constexpr int SG_BYTES = (BM + BN) * 16;  // one scale group: A's rows, then B's
+  constexpr int SC_A = BM / 64, SC_B = BN / 64;
+  static_assert(NW == 8 && OpA::REM == 0 && OpB::REM == 0 && (SC_A + SC_B == 4 || SC_A + SC_B == 8) && STAGES <= 4, "copies");
+
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  char* const a_lds = smem;
+  char* const b_lds = smem + STAGES * A_BYTES;
+  char* const s_lds = b_lds + STAGES * B_BYTES;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int64_t tm, tn;
+  tile_of(blockIdx.x, g.tiles_m, g.tiles_n, PANEL, 1, &tm, &tn);
+  const int row0 = (int)tm * BM, col0 = (int)tn * BN;
+  const int mvalid = min(BM, g.M - row0), nvalid = min(BN, g.N - col0);
+  const int nk = (g.KB + 3) / 4;
+  const int kin_last = (g.KB - (nk - 1) * 4) * (kMxBlockBytes / 2);  // in halves
+
+  OpA opa;
+  OpB opb;
+  opa.init_copies((const _Float16*)g.A, g.lda / 2, row0, mvalid, kin_last, wave, lane);
+  opb.init_copies((const _Float16*)g.B, g.ldb / 2, col0, nvalid, kin_last, wave, lane);
+  const uint32_t a_lds0 = lds_addr(a_lds) + wave * 1024, b_lds0 = lds_addr(b_lds) + wave * 1024;
+
+  // The scale copies (64 rows of A or B each) are group 1's: the group that runs no tile ahead
+  // has the registers for them. Its wave w takes copies w - 4 and, if there are more than four,
+  // w.
+  auto copy_scales = [&](int sg, int part) __attribute__((always_inline)) {
+    const bool is_a = part < SC_A;
+    const int r = (is_a ? part : part - SC_A) * 64;
+    const int64_t ld = is_a ? g.ldsa : g.ldsb;
+    const uint8_t* const base = is_a ? g.SA + (int64_t)(row0 + r) * ld : g.SB + (int64_t)(col0 + r) * ld;
+    const int left = (is_a ? mvalid : nvalid) - r;
+    dma_to_lds(make_rsrc(base + (int64_t)sg * 16, kMaxRange), lds_addr(s_lds) + (sg & 1) * SG_BYTES + part * 1024,
+               lane < left ? (uint32_t)lane * (uint32_t)ld : kOob);
+  };
+  auto copy_tile = [&](int t, auto group) __attribute__((always_inline)) {
+    if (decltype(group)::value == 1 && t % MxScaleRing::GROUP == 0 && t < nk) {
+      copy_scales(t / MxScaleRing::GROUP, wave - 4);
+      if (SC_A + SC_B > 4) copy_scales(t / MxScaleRing::GROUP, wave);
+    }
+    const int4v ra = opa.rsrc(t, nk, nk), rb = opb.rsrc(t, nk, nk);
+    const int slot = t % STAGES;
+    const bool last = t == nk - 1;
+#pragma unroll
+    for (int j = 0; j < OpA::LD; ++j)
+      dma_to_lds(ra, a_lds0 + slot * A_BYTES + j * NW * 1024, last ? opa.off_last[j] : opa.off[j]);
+#pragma unroll
+    for (int j = 0; j < OpB::LD; ++j)
+      dma_to_lds(rb, b_lds0 + slot * B_BYTES + j * NW * 1024, last ? opb.off_last[j] : opb.off[j]);
+  };
+
+  const int wm = wave / WN, wn = wave % WN, lrow = lane & 15, lblk = lane >> 4;
+  opa.init_frags(wm * WTM, lane);
+  opb.init_frags(wn * WTN, lane);
+  const char* const sa_lds = s_lds + (wm * WTM + lrow) * 16;
+  const char* const sb_lds = s_lds + (BM + wn * WTN + lrow) * 16;
+
+  half8 fa[FM], fb[FN];
+  int sa[FM], sb[FN];
+  auto read_tile = [&](int t) __attribute__((always_inline)) {
+    const char* const As = a_lds + (t % STAGES) * A_BYTES;
+    const char* const Bs = b_lds + (t % STAGES) * B_BYTES;
+    const int off = ((t / MxScaleRing::GROUP) & 1) * SG_BYTES + 4 * (t % MxScaleRing::GROUP) + max(min(lblk, g.KB - 1 - 4 * t), 0);
+#pragma unroll
+    for (int fn = 0; fn < FN; ++fn) {
+      fb[fn] = opb.frag(Bs, fn, 0);
+      sb[fn] = *(const TG_LDS uint8_t*)(sb_lds + off + fn * 256);
+    }
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) {
+      fa[fm] = opa.frag(As, fm, 0);
+      sa[fm] = *(const TG_LDS uint8_t*)(sa_lds + off + fm * 256);
+    }
+  };
+
+  float4v acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
+  auto wide = [](const half8& h) {
+    const int4v v = __builtin_bit_cast(int4v, h);
+    return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
+  };
+  // Operands go in as (B fragment, A fragment), so a lane holds four consecutive columns.
+  auto mma_tile = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn)
+        acc[fm][fn] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(fb[fn]), wide(fa[fm]), acc[fm][fn], 4, 4, 0, sb[fn], 0, sa[fm]);
+  };
+  pingpong_schedule<STAGES, PT, PT, (BM == 256 && BN == 256)>(wave / 4, nk, copy_tile, read_tile, mma_tile);
+
+  using ST = StagedTile<WTM, WTN>;
+  static_assert(NW * ST::BYTES <= mx_lds_bytes<BM, BN, WM, WN, STAGES>(), "staged tile fits in the ring");
+  __syncthreads();
+  char* const stage = smem + wave * ST::BYTES;
+  if (g.relu != 0)
+    ST::template stage<true>(stage, acc, lane);
+  else
+    ST::template stage<false>(stage, acc, lane);
+  ST::wave_fence();
+  store_staged<ST, WTM>(stage, lane, g.C + (int64_t)(row0 + wm * WTM) * g.ldc + col0 + wn * WTN, g.ldc,
+                        mvalid - wm * WTM, nvalid - wn * WTN, g.vec_c);
+}
+
+// ------------------------------------------------------------------------------------
+// Product of binary16 A with an MXFP4 weight, ping-pong kernel on k-tiles of 32 (one block):
+// A's tile as in the binary16 kernel (64-byte rows), B's 16 bytes a row. Lane l of a 16 x 16
+// x 32 MFMA needs k 8 (l / 16) .. + 7 of weight row l % 16: one 4-byte LDS read (16 rows of
+// 16 bytes: every bank once) and four conversions with the block's scale, done in the phase
+// in which the other group's MFMAs keep the matrix pipe busy. Scales as in gemm_mxfp4_pp,
+// 16 bytes a row covering 16 k-tiles.
+// Requirements (host): A, B, SB 16-byte aligned, lda and K multiples of 8, ldb, ldsb of 16.
+template <int BM, int BN, int WM, int WN, int STAGES>
+constexpr int wq_lds_bytes() {
+  return STAGES * (BM * 64 + BN * 16) + 2 * BN * 16;
+}
+
+template <int BM, int BN, int WM, int WN, int STAGES, int PANEL>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_f16_mxfp4_pp(MxGemmArgs g) {
+  constexpr int NW = WM * WN, WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
+  using OpA = PpOperand<BM, 32, 16, true, NW>;
+  constexpr int A_BYTES = OpA::BYTES, B_BYTES = BN * 16;
+  constexpr int GROUP = 16, SG_BYTES = BN * 16;
+  constexpr int BW = BN / 64;  // waves that copy a tile of B (64 rows each), from wave 0 on
+  static_assert(NW == 8 && OpA::REM == 0 && BW <= 4 && STAGES <= 4, "copies");
+
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  char* const a_lds = smem;
+  char* const b_lds = smem + STAGES * A_BYTES;
+  char* const s_lds = b_lds + STAGES * B_BYTES;
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int64_t tm, tn;
+  tile_of(blockIdx.x, g.tiles_m, g.tiles_n, PANEL, 1, &tm, &tn);
+  const int row0 = (int)tm * BM, col0 = (int)tn * BN;
+  const int mvalid = min(BM, g.M - row0), nvalid = min(BN, g.N - col0);
+  const int nk = g.KB;
+  const int kin_last = g.K - (nk - 1) * kMxBlock;
+
+  OpA opa;
+  opa.init_copies((const _Float16*)g.A, g.lda, row0, mvalid, kin_last, wave, lane);
+  const uint32_t a_lds0 = lds_addr(a_lds) + wave * 1024;
+  // Waves 0 .. BW-1 copy 64 rows of B's codes per k-tile, waves 4 .. 4+BW-1 (the other group,
+  // which copies less) 64 rows of scales every 16 k-tiles.
+  const int part = wave & 3;
+  const bool has_b = part < BW;
+  const char* const b_base = (const char*)(g.B + (int64_t)(col0 + part * 64) * g.ldb);
+  const char* const s_base = (const char*)(g.SB + (int64_t)(col0 + part * 64) * g.ldsb);
+  const uint32_t b_off = lane < nvalid - part * 64 ? (uint32_t)(lane * g.ldb) : kOob;
+  const uint32_t s_off = lane < nvalid - part * 64 ? (uint32_t)(lane * g.ldsb) : kOob;
+  const uint32_t b_dst = lds_addr(b_lds) + part * 1024, s_dst = lds_addr(s_lds) + part * 1024;
+
+  auto copy_tile = [&](int t, auto group) __attribute__((always_inline)) {
+    constexpr int G = decltype(group)::value;
+    const int slot = t % STAGES;
+    const int4v ra = opa.rsrc(t, nk, nk);
+    const bool last = t == nk - 1;
+    if (G == 1 && t % GROUP == 0 && t < nk && has_b)
+      dma_to_lds(make_rsrc(s_base + t, kMaxRange), s_dst + ((t / GROUP) & 1) * SG_BYTES, s_off);
+#pragma unroll
+    for (int j = 0; j < OpA::LD; ++j)
+      dma_to_lds(ra, a_lds0 + slot * A_BYTES + j * NW * 1024, last ? opa.off_last[j] : opa.off[j]);
+    if (G == 0 && has_b)
+      dma_to_lds(make_rsrc(b_base + (int64_t)min(t, nk - 1) * kMxBlockBytes, t < nk ? kMaxRange : 0u), b_dst + slot * B_BYTES, b_off);
+  };
+
+  const int wm = wave / WN, wn = wave % WN, lrow = lane & 15, lkg = lane >> 4;
+  opa.init_frags(wm * WTM, lane);
+  const char* const b_rd = b_lds + (wn * WTN + lrow) * 16 + 4 * lkg;
+  const char* const s_rd = s_lds + (wn * WTN + lrow) * 16;
+
+  half8 fa[FM], fb[FN];
+  auto read_tile = [&](int t) __attribute__((always_inline)) {
+    const char* const As = a_lds + (t % STAGES) * A_BYTES;
+    uint32_t w[FN], s[FN];
+    const int so = ((t / GROUP) & 1) * SG_BYTES + t % GROUP;
+#pragma unroll
+    for (int fn = 0; fn < FN; ++fn) {
+      w[fn] = *(const TG_LDS uint32_t*)(b_rd + (t % STAGES) * B_BYTES + fn * 256);
+      s[fn] = *(const TG_LDS uint8_t*)(s_rd + so + fn * 256);
+    }
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) fa[fm] = opa.frag(As, fm, 0);
+#pragma unroll
+    for (int fn = 0; fn < FN; ++fn) fb[fn] = decode8(w[fn], s[fn]);
+  };
+
+  float4v acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
+  auto mma_tile = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn)
+        acc[fm][fn] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[fn], fa[fm], acc[fm][fn], 0, 0, 0);
+  };
+  // every wave copies at least A's share of a tile (waves 0 .. BW-1 one more)
+  constexpr int PT = OpA::LD;
+  pingpong_schedule<STAGES, PT, PT, (BM == 256 && BN == 256)>(wave / 4, nk, copy_tile, read_tile, mma_tile);
+
+  using ST = StagedTile<WTM, WTN>;
+  static_assert(NW * ST::BYTES <= 160 * 1024, "staged tile");
+  __syncthreads();
+  char* const stage = smem + wave * ST::BYTES;
+  if (g.relu != 0)
+    ST::template stage<true>(stage, acc, lane);
+  else
+    ST::template stage<false>(stage, acc, lane);
+  ST::wave_fence();
+  store_staged<ST, WTM>(stage, lane, g.C + (int64_t)(row0 + wm * WTM) * g.ldc + col0 + wn * WTN, g.ldc,
+                        mvalid - wm * WTM, nvalid - wn * WTN, g.vec_c);
+}
+
+// ------------------------------------------------------------------------------------
+// Few rows (M <= 64: single tokens and small batches): bound by reading the weight once. A
+// workgroup owns 16 rows of the weight and splits K over its waves in runs of 512 (16 blocks:
+// one 16-byte load of scales per row, four loads of codes), so all of a wave's loads of a run
+// are in flight at once and nothing passes through LDS but the waves' partial sums, added in
+// wave order. Lane l of the weight's fragment holds block l / 16 (of four) of row l % 16, 32
+// codes. The binary16 product uses them in four MFMAs of 8 k per lane: step j takes k 32 (l /
+// 16) + 8 j .. + 7 on both sides (any order of k will do that both operands share), which is
+// one 16-byte load of A.
+constexpr int kSkinnyWaves = 8;
+
+template <int MT, bool F16A>
+__global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_mxfp4_skinny(MxGemmArgs g) {
+  __shared__ __attribute__((aligned(16))) float4v part[kSkinnyWaves][MT][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lrow = lane & 15, lblk = lane >> 4;
+  const int n0 = (int)blockIdx.x * 16;
+  const int n = min(n0 + lrow, g.N - 1);  // rows past N read the last one, their sums are dropped
+  const uint8_t* const brow = g.B + (int64_t)n * g.ldb + lblk * kMxBlockBytes;
+  const uint8_t* const srow = g.SB + (int64_t)n * g.ldsb;
+  const int runs = (g.KB + 15) / 16;
+  float4v acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
+
+  for (int r = wave; r < runs; r += kSkinnyWaves) {
+    const int kb0 = r * 16;
+    uint4v w[4];
+    const uint4v sv = load_any<uint4v>(srow + kb0);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      w[c] = (uint4v){0, 0, 0, 0};
+      if (kb0 + 4 * c + lblk < g.KB) w[c] = load_any<uint4v>(brow + (int64_t)(kb0 + 4 * c) * kMxBlockBytes);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int kb = kb0 + 4 * c;
+      // blocks past KB: zero codes, and a finite scale whatever the padding holds
+      const uint32_t sb = kb + lblk < g.KB ? (sv[c] >> (8 * lblk)) & 255u : 127u;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int m = 16 * i + lrow;
+        if constexpr (F16A) {
+          const _Float16* const arow = (const _Float16*)g.A + (int64_t)m * g.lda;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int k = (kb + lblk) * kMxBlock + 8 * j;
+            half8 a = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (m < g.M && k < g.K) a = *(const half8*)(arow + k);
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(decode8(w[c][j], sb), a, acc[i], 0, 0, 0);
+          }
+        } else {
+          int4v a = {0, 0, 0, 0};
+          int sa = 127;
+          if (m < g.M && kb + lblk < g.KB) {
+            a = *(const int4v*)((const uint8_t*)g.A + (int64_t)m * g.lda + (int64_t)(kb + lblk) * kMxBlockBytes);
+            sa = g.SA[(int64_t)m * g.ldsa + kb + lblk];
+          }
+          const int4v b = __builtin_bit_cast(int4v, w[c]);
+          acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1), __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1),
+              acc[i], 4, 4, 0, (int)sb, 0, sa);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+  __syncthreads();
+  for (int i = wave; i < MT; i += kSkinnyWaves) {
+    float4v s = part[0][i][lane];
+#pragma unroll
+    for (int w = 1; w < kSkinnyWaves; ++w) s += part[w][i][lane];
+    const int m = 16 * i + lrow, c = n0 + 4 * lblk;
+    if (m >= g.M) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (c + e < g.N) g.C[(int64_t)m * g.ldc + c + e] = (_Float16)(g.relu ? relu_f(s[e]) : s[e]);
+  }
+}
+
+// ------------------------------------------------------------------------------------
+// Any alignment, stride and K: 128 x 128 tiles, four waves of 64 x 64, one block of 32 k at a
+// time through a double-buffered LDS tile filled through registers (unaligned loads). Codes of
+// A are decoded without their scale, which multiplies the block's product in float32 together
+// with B's (E8M0 scales leave binary16's range); a binary16 A meets the decoded weight.
+template <bool F16A>
+__global__ __launch_bounds__(256) void gemm_mxfp4_generic(MxGemmArgs g) {
+  constexpr int ROW = 40;  // halves per LDS row: 16-byte aligned, rows spread over the banks
+  __shared__ __attribute__((aligned(16))) _Float16 at[2][128 * ROW], bt[2][128 * ROW];
+  __shared__ int as[2][128], bs[2][128];  // scale exponents
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int row0 = (int)(blockIdx.x / g.tiles_n) * 128, col0 = (int)(blockIdx.x % g.tiles_n) * 128;
+  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64, lrow = lane & 15, lkg = lane >> 4;
+  // thread t stages half (t & 1) of row t / 2 of both tiles: 16 values of A, 16 codes of B
+  const int sr = tid >> 1, sh = tid & 1;
+  const bool a_in = row0 + sr < g.M, b_in = col0 + sr < g.N;
+  const int64_t ar = a_in ? row0 + sr : 0, br = b_in ? col0 + sr : 0;
+  uint4v av[2];
+  uint2v bv;
+  uint32_t sav = 127, sbv = 127;
+  auto fetch = [&](int kb) {
+    if constexpr (F16A) {
+      const int k = kb * kMxBlock + 16 * sh;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) av[h] = load8((const _Float16*)g.A + ar * g.lda + k + 8 * h, a_in ? g.K - k - 8 * h : 0);
+    } else {
+      const uint2v c = load_any<uint2v>((const uint8_t*)g.A + ar * g.lda + (int64_t)kb * kMxBlockBytes + 8 * sh);
+      av[0] = (uint4v){c[0], c[1], 0, 0};
+      sav = g.SA[ar * g.ldsa + kb];
+    }
+    bv = load_any<uint2v>(g.B + br * g.ldb + (int64_t)kb * kMxBlockBytes + 8 * sh);
+    sbv = g.SB[br * g.ldsb + kb];
+  };
+  auto put = [&](int buf) {
+    half8 a0, a1;
+    if constexpr (F16A) {
+      a0 = __builtin_bit_cast(half8, av[0]);
+      a1 = __builtin_bit_cast(half8, av[1]);
+    } else {
+      a0 = decode8(av[0][0], sav == 255 ? 255 : 127);  // a NaN scale makes NaN values
+      a1 = decode8(av[0][1], sav == 255 ? 255 : 127);
+      if (sh == 0) {
+        as[buf][sr] = (int)sav - 127;
+        bs[buf][sr] = (int)sbv - 127;
+      }
+    }
+    *(half8*)&at[buf][sr * ROW + 16 * sh] = a0;
+    *(half8*)&at[buf][sr * ROW + 16 * sh + 8] = a1;
+    *(half8*)&bt[buf][sr * ROW + 16 * sh] = decode8(bv[0], F16A || sbv == 255 ? sbv : 127);
+    *(half8*)&bt[buf][sr * ROW + 16 * sh + 8] = decode8(bv[1], F16A || sbv == 255 ? sbv : 127);
+  };
+  float4v acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
+  fetch(0);
+  put(0);
+  __syncthreads();
+  for (int kb = 0; kb < g.KB; ++kb) {
+    const int buf = kb & 1;
+    if (kb + 1 < g.KB) fetch(kb + 1);
+    half8 fa[4], fb[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      fa[f] = *(const half8*)&at[buf][(wm + 16 * f + lrow) * ROW + 8 * lkg];
+      fb[f] = *(const half8*)&bt[buf][(wn + 16 * f + lrow) * ROW + 8 * lkg];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (F16A) {
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+        } else {
+          const float4v zero = {0.0f, 0.0f, 0.0f, 0.0f};
+          const float4v p = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[j], fa[i], zero, 0, 0, 0);
+          // the exponents are added first: either scale alone may leave float32's range
+          const int sa = as[buf][wm + 16 * i + lrow];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[i][j][e] += __builtin_amdgcn_ldexpf(p[e], sa + bs[buf][wn + 16 * j + 4 * lkg + e]);
+        }
+      }
+    if (kb + 1 < g.KB) put(buf ^ 1);
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int m = row0 + wm + 16 * i + lrow;
+    if (m >= g.M) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = col0 + wn + 16 * j + 4 * lkg + e;
+        if (c < g.N) g.C[(int64_t)m * g.ldc + c] = (_Float16)(g.relu ? relu_f(acc[i][j][e]) : acc[i][j][e]);
+      }
+  }
+}
+
+// Launch of a kernel with more than the default dynamic LDS: the limit is raised once per
+// kernel and device.
+template <typename K>
+hipError_t launch_big(K kern, int lds, std::atomic<uint64_t>& ready, const MxGemmArgs& g, hipStream_t s, int device) {
+  const uint64_t bit = 1ull << (device & 63);
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n)), dim3(512), lds, s, g);
+  return hipGetLastError();
+}
+
+template <int BM, int BN, int STAGES>
+hipError_t launch_mx_pp(bool f16_a, const MxGemmArgs& g, hipStream_t s, int device) {
+  static std::atomic<uint64_t> ready[2];
+  if (f16_a) {
+    constexpr int ring = wq_lds_bytes<BM, BN, 2, 4, STAGES>(), st = 8 * StagedTile<BM / 2, BN / 4>::BYTES;
+    return launch_big(gemm_f16_mxfp4_pp<BM, BN, 2, 4, STAGES, 4>, ring > st ? ring : st, ready[1], g, s, device);
+  }
+  return launch_big(gemm_mxfp4_pp<BM, BN, 2, 4, STAGES, 4>, mx_lds_bytes<BM, BN, 2, 4, STAGES>(), ready[0], g, s, device);
+}
+
+template <bool F16A>
+hipError_t launch_skinny(const MxGemmArgs& g, hipStream_t s) {
+  const dim3 grid((unsigned)((g.N + 15) / 16)), block(64 * kSkinnyWaves);
+  switch ((g.M + 15) / 16) {
+    case 1: hipLaunchKernelGGL((gemm_mxfp4_skinny<1, F16A>), grid, block, 0, s, g); break;
+    case 2: hipLaunchKernelGGL((gemm_mxfp4_skinny<2, F16A>), grid, block, 0, s, g); break;
+    case 3: hipLaunchKernelGGL((gemm_mxfp4_skinny<3, F16A>), grid, block, 0, s, g); break;
+    default: hipLaunchKernelGGL((gemm_mxfp4_skinny<4, F16A>), grid, block, 0, s, g); break;
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_mxfp4(int cfg, bool f16_a, const MxGemmArgs& args, hipStream_t s, int device) {
+  MxGemmArgs g = args;
+  const int tile = cfg == kMx256 ? 256 : 128;
+  g.tiles_m = (int)ceil_div(g.M, tile);
+  g.tiles_n = (int)ceil_div(g.N, tile);
+  switch (cfg) {
+    case kMxSkinny: return f16_a ? launch_skinny<true>(g, s) : launch_skinny<false>(g, s);
+    case kMx128: return launch_mx_pp<128, 128, 4>(f16_a, g, s, device);
+    case kMx256: return launch_mx_pp<256, 256, 4>(f16_a, g, s, device);
+    default: break;
+  }
+  const dim3 grid((unsigned)((int64_t)g.tiles_m * g.tiles_n));
+  if (f16_a)
+    hipLaunchKernelGGL(gemm_mxfp4_generic<true>, grid, dim3(256), 0, s, g);
+  else
+    hipLaunchKernelGGL(gemm_mxfp4_generic<false>, grid, dim3(256), 0, s, g);
+  return hipGetLastError();
+}
+
+hipError_t launch_quant_mxfp4(const MxQuantArgs& q, hipStream_t s) {
+  if (q.QT != nullptr) {
+    const int64_t tiles = ceil_div(q.R, 256) * ceil_div(q.K, 128);
+    if (q.Q != nullptr)
+      hipLaunchKernelGGL(quant_mxfp4_cols<true>, dim3((unsigned)tiles), dim3(256), 0, s, q);
+    else
+      hipLaunchKernelGGL(quant_mxfp4_cols<false>, dim3((unsigned)tiles), dim3(256), 0, s, q);
+  } else {
+    const int64_t blocks = (int64_t)q.R * ceil_div(q.K, kMxBlock);
+    hipLaunchKernelGGL(quant_mxfp4_rows<2>, dim3((unsigned)ceil_div(blocks, 128)), dim3(256), 0, s, q);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_dequant_mxfp4(const MxDequantArgs& q, hipStream_t s) {
+  const int64_t blocks = (int64_t)q.R * ceil_div(q.K, kMxBlock);
+  hipLaunchKernelGGL(dequant_mxfp4_rows<2>, dim3((unsigned)ceil_div(blocks, 128)), dim3(256), 0, s, q);
+  return hipGetLastError();
+}
+
+}  // namespace tgemm
