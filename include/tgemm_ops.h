@@ -1,6 +1,7 @@
 /*
  * tgemm_ops.h -- C ABI of libtgemm, the operators beside the GEMMs of tgemm.h: MXFP4 (4-bit
- * microscaled) matrices with their quantiser and products. The same library and conventions
+ * microscaled) matrices with their quantiser and products, and the orthogonalisation of a
+ * weight's update. The same library and conventions
  * (row-major storage, device pointers owned by the caller, nothing allocated, enqueue-only calls
  * on the given stream, the TGEMM_E* codes of tgemm.h, C not overlapping an input).
  */
@@ -72,6 +73,37 @@ TGEMM_API int mxfp4_gemm(int64_t M, int64_t N, int64_t K,
 TGEMM_API int mxfp4_gemm_f16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
                              const void* B, int64_t ldb, const void* scale_b, int64_t ldsb,
                              void* C, int64_t ldc, int relu, void* stream);
+
+/*
+ * Orthogonalisation of a weight's update by Newton-Schulz products: for each of `batch` matrices
+ * G (R x C, row stride ldg, matrix stride stride_g, in elements; dtype TGEMM_DTYPE_F16 or
+ * TGEMM_DTYPE_F32),
+ *   X_0 = G / (|G|_F + 1e-7);  `steps` times  A = X X^T,  X <- a X + (b A + c A A) X;
+ *   the result scale * X as binary16 (row stride ldx, matrix stride stride_x; only R x C values
+ *   of each matrix written),
+ * which leaves G's singular vectors and moves its singular values towards one (a, b, c = 3.4445,
+ * -4.7750, 2.0315 with 5 steps: into about 0.7 .. 1.2). For R > C the products run on X^T X, which
+ * gives the same X. The norm is summed in float64, the products are binary16 MFMAs with float32
+ * sums, the iterate is kept to 22 bits and the diagonals of A and of the polynomial in float32: on
+ * random matrices the result is within 1e-3 of the exact one (Frobenius norms; binary16's own
+ * rounding is 2e-4 of it).
+ *   workspace : caller-owned device memory, 256-byte aligned, at least
+ *               orthogonalize_workspace_bytes(batch, R, C) bytes, nothing expected of its
+ *               contents; calls that may overlap in time need different ones.
+ * X may be G (same strides, binary16), no other overlap. min(R, C) is at most 32768, max(R, C) at
+ * most TGEMM_FAST_MAX_LD, steps 1 .. 64 (else TGEMM_EINVAL_DIM, as for an unknown dtype); stride_x
+ * must keep the results apart (TGEMM_EINVAL_LD). An empty batch or matrix is a no-op; a matrix of
+ * zeros gives zeros; one that holds an infinity or a NaN gives NaN in that matrix. X must be
+ * 2-byte and G aligned to its type.
+ */
+#define TGEMM_DTYPE_F16 0
+#define TGEMM_DTYPE_F32 1
+TGEMM_API int64_t orthogonalize_workspace_bytes(int64_t batch, int64_t R, int64_t C);
+TGEMM_API int orthogonalize_f16(int64_t batch, int64_t R, int64_t C, int dtype,
+                                const void* G, int64_t ldg, int64_t stride_g,
+                                void* X, int64_t ldx, int64_t stride_x,
+                                int steps, float a, float b, float c, float scale,
+                                void* workspace, int64_t workspace_bytes, void* stream);
 
 /* MXFP4 tooling: the two products forced to kernel idx (TGEMM_MX_*; TGEMM_EINVAL_CFG for an
  * index out of range, a fast kernel that cannot take the arguments, or the skinny kernel with M

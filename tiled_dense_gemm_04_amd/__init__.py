@@ -23,7 +23,8 @@ through gemm_f16_ex).
 The operators of ``include/tgemm_ops.h``: MXFP4 (4-bit microscaled) matrices in
 ``mxfp4.py`` (``mxfp4_quant``, ``mxfp4_dequant``, ``mxfp4_gemm``, ``mxfp4_gemm_f16``,
 ``mxfp4_linear``, and the autograd forms ``Mxfp4LinearFunction`` and
-``Mxfp4WeightFunction``).
+``Mxfp4WeightFunction``), and the Newton-Schulz orthogonalisation of weight updates,
+``orthogonalize``.
 
 The tooling
 twin ``libtgemm_stamps.so`` (``stamps_lib()``, measurement tools only) compiles every config
@@ -815,7 +816,9 @@ from . import mxfp4  # noqa: E402
 from .mxfp4 import (MX_128, MX_256, MX_BLOCK, MX_BLOCK_BYTES, MX_GENERIC, MX_MAX_DIM, MX_SKINNY,  # noqa: E402,F401
                     MX_SKINNY_ROWS, mxfp4_dequant, mxfp4_empty, mxfp4_gemm, mxfp4_gemm_f16, mxfp4_linear, mxfp4_quant,
                     mxfp4_select_config)
+from . import newton_schulz  # noqa: E402
+from .newton_schulz import NS_COEFFICIENTS, orthogonalize, orthogonalize_workspace_bytes  # noqa: E402,F401
 
-OPS_SIGNATURES = {**mxfp4.SIGNATURES}
+OPS_SIGNATURES = {**mxfp4.SIGNATURES, **newton_schulz.SIGNATURES}
 # Every symbol include/tgemm_ops.h declares.
 OPS_EXPORTS = tuple(OPS_SIGNATURES)

@@ -29,8 +29,9 @@ VARIANTS = {
 ARCH = "gfx950"
 
 SOURCES = [os.path.join(CSRC, "tgemm_kernels.hip"), os.path.join(CSRC, "tgemm_fp8.hip"),
-           os.path.join(CSRC, "tgemm_mx.hip"), os.path.join(CSRC, "tgemm_api.cpp"),
-           os.path.join(CSRC, "tgemm_mx_api.cpp")]
+           os.path.join(CSRC, "tgemm_mx.hip"), os.path.join(CSRC, "tgemm_orth.hip"),
+           os.path.join(CSRC, "tgemm_api.cpp"),
+           os.path.join(CSRC, "tgemm_mx_api.cpp"), os.path.join(CSRC, "tgemm_orth_api.cpp")]
 
 # Device code: gfx950 only. Packed-fp32 instruction selection is switched off for all
 # device code; -fvisibility=hidden keeps everything but the TGEMM_API entry points local.

@@ -1,0 +1,381 @@
+// tgemm_orth.hip -- gfx950 kernels of the Newton-Schulz orthogonalisation.
+//
+// X_0 = G / (|G|_F + 1e-7) (transposed if tall so that m <= n), then `steps` times
+//   A = X X^T,  X <- a X + (b A + c A A) X,
+// which drives every singular value of X towards one; the result is scale * X. A tall G keeps
+// its orientation: A = X^T X and X <- a X + X (b A + c A A), so nothing is transposed.
+//
+// The products run on the binary16 MFMAs with float32 sums; what they lose is kept small by
+// where binary16 is used:
+//   * the iterate is held as two halves, hi + lo 2^-11 (22 bits), and only products read hi
+//     alone;
+//   * the diagonals, which dominate A and the polynomial P = a I + b A + c A A once X is near
+//     orthogonal, stay in float32 and out of the products: with A = diag(D) + E,
+//       P_ij = b E_ij + c ((D_i + D_j) E_ij + (E E)_ij)        (i != j, binary16)
+//       P_ii = a + b D_i + c (D_i^2 + (E E)_ii)                (float32)
+//       X'   = diag(P) X + offdiag(P) hi(X).
+//     Rounding then touches off-diagonal values only, which are small and of random sign
+//     (relative error of the result on random 1024 x 1024: 7e-4; 1.7e-3 with A and P rounded
+//     whole, 1.2e-3 to 7e-3 with X in binary16 as well);
+//   * A and E E are symmetric: only tiles on and above the diagonal are computed, each stored
+//     a second time transposed.
+#include "tgemm_orth.h"
+#include "tgemm_pingpong.h"
+
+#include <atomic>
+
+namespace tgemm {
+namespace {
+
+typedef float float4v __attribute__((ext_vector_type(4)));
+
+constexpr float kLo = 2048.0f;  // the low half is held times 2^11: away from the subnormals
+constexpr double kNormEps = 1e-7;
+
+__device__ __forceinline__ float joined(_Float16 hi, _Float16 lo) { return (float)hi + (float)lo * (1.0f / kLo); }
+__device__ __forceinline__ _Float16 low_half(float x, _Float16 hi) { return (_Float16)((x - (float)hi) * kLo); }
+
+// Sums of squares of a matrix, kOrthParts partial sums in float64 (squares of float32 values
+// leave float32's range). Bound by reading G.
+__global__ __launch_bounds__(256) void orth_norm(OrthArgs g) {
+  __shared__ double w[4];
+  const int part = blockIdx.x % kOrthParts, bt = blockIdx.x / kOrthParts;
+  const int64_t total = (int64_t)g.R * g.C;
+  const int64_t per = ((total + kOrthParts - 1) / kOrthParts + 7) / 8 * 8;
+  const int64_t lo = part * per, hi = lo + per < total ? lo + per : total;
+  double s = 0.0;
+  for (int64_t i = lo + (int64_t)threadIdx.x * 8; i < hi; i += 256 * 8) {
+    int64_t r = i / g.C;
+    int c = (int)(i - r * g.C);
+    int64_t at = (int64_t)bt * g.stride_g + r * g.ldg;
+    if (c + 8 <= g.C && i + 8 <= hi) {
+      float v[8];
+      if (g.f32) {
+        __builtin_memcpy(v, (const float*)g.G + at + c, 32);
+      } else {
+        half8 h;
+        __builtin_memcpy(&h, (const _Float16*)g.G + at + c, 16);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = (float)h[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += (double)v[e] * (double)v[e];
+    } else {
+      for (int e = 0; e < 8 && i + e < hi; ++e) {
+        const double v = g.f32 ? (double)((const float*)g.G)[at + c] : (double)((const _Float16*)g.G)[at + c];
+        s += v * v;
+        if (++c == g.C) {
+          c = 0;
+          at += g.ldg;
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
+  if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) g.parts[blockIdx.x] = (w[0] + w[1]) + (w[2] + w[3]);
+}
+
+// X_0 = G / (|G| + eps) as two halves, padded with zeros: eight values per thread.
+__global__ __launch_bounds__(256) void orth_start(OrthArgs g) {
+  __shared__ double inv;
+  const int rp = g.tall ? g.np : g.mp, cp = g.tall ? g.mp : g.np;
+  const int64_t chunks = (int64_t)rp * (cp / 8), groups = (chunks + 255) / 256;
+  const int bt = (int)(blockIdx.x / groups);
+  if (threadIdx.x < 64) {
+    double s = g.parts[bt * kOrthParts + threadIdx.x] + g.parts[bt * kOrthParts + 64 + threadIdx.x];
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
+    if (threadIdx.x == 0) inv = 1.0 / (sqrt(s) + kNormEps);
+  }
+  __syncthreads();
+  const int64_t u = (blockIdx.x - bt * groups) * 256 + threadIdx.x;
+  if (u >= chunks) return;
+  const int r = (int)(u / (cp / 8)), c = (int)(u % (cp / 8)) * 8;
+  half8 hi, lo;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float x = 0.0f;
+    if (r < g.R && c + e < g.C) {
+      const int64_t at = (int64_t)bt * g.stride_g + (int64_t)r * g.ldg + c + e;
+      x = (float)((g.f32 ? (double)((const float*)g.G)[at] : (double)((const _Float16*)g.G)[at]) * inv);
+    }
+    hi[e] = (_Float16)x;
+    lo[e] = low_half(x, hi[e]);
+  }
+  const int64_t o = (int64_t)bt * rp * cp + (int64_t)r * cp + c;
+  *(half8*)(g.hi[0] + o) = hi;
+  *(half8*)(g.lo[0] + o) = lo;
+}
+
+// ------------------------------------------------------------------------------------
+// The three products of a step, one ping-pong kernel each (tgemm_pingpong.h) on BM x BM
+// tiles of one matrix of the batch; what differs is the operands and the epilogue.
+enum Product { kGram, kSquare, kApply };
+
+struct OrthStep {
+  int in, last;  // which of the two iterate buffers is read; the final step writes the result
+};
+
+template <int BM>
+constexpr int orth_lds_bytes() {
+  // the operand ring, or the staged tiles of the epilogue (per wave, transposed with a 16-byte
+  // pad per column), whichever is larger
+  constexpr int ring = 4 * 2 * BM * 64, st = 8 * (BM / 4) * (BM / 2 * 2 + 16);
+  return ring > st ? ring : st;
+}
+
+template <Product P, int BM, bool TALL>
+__global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
+  constexpr int NW = 8, WM = 2, WN = 4, STAGES = 4, BK = 32;
+  constexpr int WTM = BM / WM, WTN = BM / WN, FM = WTM / 16, FN = WTN / 16;
+  // Gram: rows of the wide iterate, or columns of the tall one; Square: E is its own
+  // transpose; Apply: P times the wide iterate (k along its rows), or the tall one times P.
+  constexpr bool A_KMAJ = P != kGram || !TALL, B_KMAJ = P == kSquare || (P == kGram) != TALL;
+  using OpA = PpOperand<BM, BK, 16, A_KMAJ, NW>;
+  using OpB = PpOperand<BM, BK, 16, B_KMAJ, NW>;
+  constexpr int A_BYTES = OpA::BYTES, B_BYTES = OpB::BYTES, PT = OpA::LD + OpB::LD;
+  static_assert(OpA::REM == 0 && OpB::REM == 0, "copies split evenly");
+
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  char* const a_lds = smem;
+  char* const b_lds = smem + STAGES * A_BYTES;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+  const int rows = P == kApply && TALL ? g.np : g.mp, cols = P == kApply && !TALL ? g.np : g.mp;
+  const int K = P == kGram ? g.np : g.mp;
+  const int tiles_m = (rows + BM - 1) / BM, tiles_n = (cols + BM - 1) / BM;
+  const int tiles = P == kApply ? tiles_m * tiles_n : tiles_n * (tiles_n + 1) / 2;
+  const int64_t lid = xcd_logical_id(blockIdx.x, (int64_t)tiles * g.batch, 1);
+  const int bt = (int)(lid / tiles), t = (int)(lid % tiles);
+  int tm, tn;
+  if (P == kApply) {
+    int64_t a, b;
+    panel_tile(t, tiles_m, tiles_n, 4, &a, &b);
+    tm = (int)a;
+    tn = (int)b;
+  } else {  // tile t of the upper triangle, column by column
+    tn = (int)((sqrtf(8.0f * t + 1.0f) - 1.0f) * 0.5f);
+    while (tn * (tn + 1) / 2 > t) --tn;
+    while ((tn + 1) * (tn + 2) / 2 <= t) ++tn;
+    tm = t - tn * (tn + 1) / 2;
+  }
+  const int row0 = tm * BM, col0 = tn * BM;
+  const int mvalid = min(BM, rows - row0), nvalid = min(BM, cols - col0);
+  const int nk = K / BK;
+
+  const int64_t xsz = (int64_t)g.mp * g.np, esz = (int64_t)g.mp * g.mp;
+  const _Float16* const hi = g.hi[st.in] + bt * xsz;
+  const _Float16* const lo = g.lo[st.in] + bt * xsz;
+  _Float16* const E = g.E + bt * esz;
+  _Float16* const PM = g.P + bt * esz;
+  float* const D = g.D + (int64_t)bt * g.mp;
+  float* const DP = g.DP + (int64_t)bt * g.mp;
+  const int ldx = TALL ? g.mp : g.np;  // the iterate's row length
+  const _Float16* const Aop = P == kGram ? hi : P == kSquare ? E : TALL ? hi : PM;
+  const _Float16* const Bop = P == kGram ? hi : P == kSquare ? E : TALL ? PM : hi;
+  const int lda = P == kGram || (P == kApply && TALL) ? ldx : g.mp;
+  const int ldb = P == kGram || (P == kApply && !TALL) ? ldx : g.mp;
+
+  OpA opa;
+  OpB opb;
+  opa.init_copies(Aop, lda, row0, mvalid, BK, wave, lane);
+  opb.init_copies(Bop, ldb, col0, nvalid, BK, wave, lane);
+  const uint32_t a_lds0 = lds_addr(a_lds) + wave * 1024, b_lds0 = lds_addr(b_lds) + wave * 1024;
+  auto copy_tile = [&](int kt, auto) __attribute__((always_inline)) {
+    const int4v ra = opa.rsrc(kt, nk, nk), rb = opb.rsrc(kt, nk, nk);
+    const int slot = kt % STAGES;
+#pragma unroll
+    for (int j = 0; j < OpA::LD; ++j) dma_to_lds(ra, a_lds0 + slot * A_BYTES + j * NW * 1024, opa.off[j]);
+#pragma unroll
+    for (int j = 0; j < OpB::LD; ++j) dma_to_lds(rb, b_lds0 + slot * B_BYTES + j * NW * 1024, opb.off[j]);
+  };
+  const int wm = wave / WN, wn = wave % WN, lrow = lane & 15, lkg = lane >> 4;
+  opa.init_frags(wm * WTM, lane);
+  opb.init_frags(wn * WTN, lane);
+  half8 fa[FM], fb[FN];
+  auto read_tile = [&](int kt) __attribute__((always_inline)) {
+    const char* const As = a_lds + (kt % STAGES) * A_BYTES;
+    const char* const Bs = b_lds + (kt % STAGES) * B_BYTES;
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) fa[fm] = opa.frag(As, fm, 0);
+#pragma unroll
+    for (int fn = 0; fn < FN; ++fn) fb[fn] = opb.frag(Bs, fn, 0);
+  };
+  float4v acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
+  auto mma_tile = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn)
+        acc[fm][fn] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[fn], fa[fm], acc[fm][fn], 0, 0, 0);
+  };
+  pingpong_schedule<STAGES, PT, PT, (A_KMAJ && B_KMAJ && BM == 256)>(wave / 4, nk, copy_tile, read_tile, mma_tile);
+  __syncthreads();  // the ring is free for staging
+
+  // Epilogue. The lane holds row r and columns c .. c + 3 of each 16 x 16 tile; the padded sizes
+  // are multiples of 64, so a group of four lies inside the matrix or outside it.
+  const int wr0 = row0 + wm * WTM, wc0 = col0 + wn * WTN;
+  using ST = StagedTile<WTM, WTN>;
+  char* const stage = smem + wave * (orth_lds_bytes<BM>() / NW);
+  static_assert(ST::BYTES <= orth_lds_bytes<BM>() / NW, "staged tile");
+  const int rv = rows - wr0, cv = cols - wc0;
+
+  if constexpr (P == kApply) {
+    // X' = diag(P) X + offdiag(P) hi(X)
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) {
+      const int r = wr0 + 16 * fm + lrow;
+      const float dr = !TALL && r < rows ? DP[r] : 0.0f;
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn) {
+        const int c = wc0 + 16 * fn + 4 * lkg;
+        if (r >= rows || c >= cols) continue;
+        const half4 h = *(const half4*)(hi + (int64_t)r * ldx + c), l = *(const half4*)(lo + (int64_t)r * ldx + c);
+        float4v d = {dr, dr, dr, dr};
+        if (TALL) d = *(const float4v*)(DP + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[fm][fn][e] += d[e] * joined(h[e], l[e]);
+      }
+      __builtin_amdgcn_sched_barrier(0);  // one row's loads in flight: all of them would spill
+    }
+    if (st.last) {
+#pragma unroll
+      for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn) acc[fm][fn] *= g.scale;
+      ST::template stage<false>(stage, acc, lane);
+      ST::wave_fence();
+      _Float16* const X = g.X + bt * g.stride_x;
+      const int vec = (reinterpret_cast<uintptr_t>(X) & 15) == 0 && g.ldx % 8 == 0;
+      store_staged<ST, WTM>(stage, lane, X + (int64_t)wr0 * g.ldx + wc0, g.ldx, g.R - wr0, g.C - wc0, vec);
+    } else {
+      ST::template stage<false>(stage, acc, lane);
+      ST::wave_fence();
+      const int64_t o = bt * xsz + (int64_t)wr0 * ldx + wc0;
+      store_staged<ST, WTM, false>(stage, lane, g.hi[st.in ^ 1] + o, ldx, rv, cv, 1);
+      ST::wave_fence();
+#pragma unroll
+      for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn) {
+          asm volatile("" : "+v"(acc[fm][fn]));  // round again: the rounded values kept from above would spill
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = acc[fm][fn][e];
+            acc[fm][fn][e] = (x - (float)(_Float16)x) * kLo;
+          }
+        }
+      ST::template stage<false>(stage, acc, lane);
+      ST::wave_fence();
+      store_staged<ST, WTM, false>(stage, lane, g.lo[st.in ^ 1] + o, ldx, rv, cv, 1);
+    }
+  } else {
+    _Float16* const out = P == kGram ? E : PM;
+    float* const dout = P == kGram ? D : DP;
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) {
+      const int r = wr0 + 16 * fm + lrow;
+      const float dr = P == kSquare && r < rows ? D[r] : 0.0f;
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn) {
+        const int c = wc0 + 16 * fn + 4 * lkg;
+        if (r >= rows || c >= cols) continue;
+        if constexpr (P == kSquare) {
+          const half4 x = *(const half4*)(E + (int64_t)r * g.mp + c);
+          const float4v d = *(const float4v*)(D + c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float s = acc[fm][fn][e];
+            acc[fm][fn][e] = r == c + e ? g.a + g.b * dr + g.c * (dr * dr + s)
+                                        : g.b * (float)x[e] + g.c * ((dr + d[e]) * (float)x[e] + s);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (r == c + e) {
+            dout[r] = acc[fm][fn][e];
+            acc[fm][fn][e] = 0.0f;
+          }
+      }
+    }
+    ST::template stage<false>(stage, acc, lane);
+    ST::wave_fence();
+    store_staged<ST, WTM, false>(stage, lane, out + (int64_t)wr0 * g.mp + wc0, g.mp, rv, cv, 1);
+    if (tm != tn) {
+      // the transposed copy: columns of the wave's tile become rows, through LDS at WTM halves
+      // and 16 bytes a column (the pad moves neighbouring columns to other banks)
+      constexpr int PITCH = WTM * 2 + 16;
+      static_assert(WTN * PITCH <= orth_lds_bytes<BM>() / NW, "transposed tile");
+      ST::wave_fence();
+#pragma unroll
+      for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *(TG_LDS _Float16*)(stage + (16 * fn + 4 * lkg + e) * PITCH + (16 * fm + lrow) * 2) = (_Float16)acc[fm][fn][e];
+      ST::wave_fence();
+      constexpr int CPR = WTM / 8;
+#pragma unroll
+      for (int i = 0; i < WTN * CPR / 64; ++i) {
+        const int u = i * 64 + lane, c = u / CPR, ch = u % CPR;
+        const half8 v = *(const TG_LDS half8*)(stage + c * PITCH + ch * 16);
+        if (c < cv && 8 * ch < rv) *(half8*)(out + (int64_t)(wc0 + c) * g.mp + wr0 + 8 * ch) = v;
+      }
+    }
+  }
+}
+
+template <Product P, int BM, bool TALL>
+hipError_t launch_product(const OrthArgs& g, OrthStep st, hipStream_t s, int device) {
+  static std::atomic<uint64_t> ready{0};
+  void (*const kern)(OrthArgs, OrthStep) = orth_product<P, BM, TALL>;
+  constexpr int lds = orth_lds_bytes<BM>();
+  const uint64_t bit = 1ull << (device & 63);
+  if (!(ready.load(std::memory_order_acquire) & bit)) {
+    const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_acq_rel);
+  }
+  const int64_t tm = ceil_div(g.mp, BM), tn = ceil_div(P == kApply ? g.np : g.mp, BM);
+  const int64_t tiles = P == kApply ? tm * tn : tn * (tn + 1) / 2;
+  hipLaunchKernelGGL(kern, dim3((unsigned)(tiles * g.batch)), dim3(512), lds, s, g, st);
+  return hipGetLastError();
+}
+
+// 256 x 256 tiles where they fill half of the 256 compute units, else 128 x 128.
+template <Product P>
+hipError_t launch_any(const OrthArgs& g, OrthStep st, hipStream_t s, int device) {
+  const int64_t tm = ceil_div(g.mp, 256), tn = ceil_div(P == kApply ? g.np : g.mp, 256);
+  const bool big = (P == kApply ? tm * tn : tn * (tn + 1) / 2) * g.batch >= 128;
+  if (g.tall) return big ? launch_product<P, 256, true>(g, st, s, device) : launch_product<P, 128, true>(g, st, s, device);
+  return big ? launch_product<P, 256, false>(g, st, s, device) : launch_product<P, 128, false>(g, st, s, device);
+}
+
+}  // namespace
+
+hipError_t launch_orthogonalize(const OrthArgs& g, int steps, hipStream_t s, int device) {
+  hipLaunchKernelGGL(orth_norm, dim3((unsigned)(g.batch * kOrthParts)), dim3(256), 0, s, g);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t groups = ceil_div((int64_t)g.mp * g.np / 8, 256);
+  hipLaunchKernelGGL(orth_start, dim3((unsigned)(groups * g.batch)), dim3(256), 0, s, g);
+  e = hipGetLastError();
+  for (int i = 0; i < steps && e == hipSuccess; ++i) {
+    const OrthStep st{i & 1, i == steps - 1};
+    e = launch_any<kGram>(g, st, s, device);
+    if (e == hipSuccess) e = launch_any<kSquare>(g, st, s, device);
+    if (e == hipSuccess) e = launch_any<kApply>(g, st, s, device);
+  }
+  return e;
+}
+
+}  // namespace tgemm

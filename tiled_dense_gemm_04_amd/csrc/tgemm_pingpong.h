@@ -73,8 +73,9 @@ __device__ __forceinline__ void pingpong_schedule(int grp, int nk, Copy&& copy, 
 }
 
 // Stores a staged tile (StagedTile) to any C: 16-byte chunks where `vec` says that every
-// chunk of C is 16-byte aligned, single elements otherwise and in a chunk that N cuts.
-template <typename ST, int WTM>
+// chunk of C is 16-byte aligned, single elements otherwise and in a chunk that N cuts. NT: the
+// result streams out (store_c); false for one that the next kernel reads.
+template <typename ST, int WTM, bool NT = true>
 __device__ __forceinline__ void store_staged(const char* region, int lane, _Float16* C, int64_t ldc, int mvalid,
                                              int nvalid, int vec) {
 #pragma unroll
@@ -86,7 +87,10 @@ __device__ __forceinline__ void store_staged(const char* region, int lane, _Floa
     if (r >= mvalid || 8 * c >= nvalid) continue;
     _Float16* const p = C + (int64_t)r * ldc + 8 * c;
     if (vec && 8 * c + 8 <= nvalid) {
-      store_c(p, x);
+      if (NT)
+        store_c(p, x);
+      else
+        *(half8*)p = x;
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)

@@ -7,6 +7,7 @@ E8M0, in rows padded to 16 bytes where this module allocates them (the fast kern
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 from . import (SELECT_NOOP, SELECT_ZERO_FILL, TGEMM_OK, TgemmError, _as_stored, _dense_2d, _operand, lib,  # noqa: F401
@@ -47,6 +48,15 @@ def _stream(stream, device):
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(device.index)
     return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _allocating(stream, device):
+    """Context in which a tensor made for a call on ``stream`` is allocated: on that stream, so
+    that neither the memory's former nor its next user is on another one."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
 
 
 def _rows_of_bytes(t, name):
@@ -101,7 +111,8 @@ def mxfp4_quant(x, dims: str = "rows", stream=None, library=None):
     out, args = (), []
     for want, rows, k in ((dims != "cols", R, K), (dims != "rows", K, R)):
         if want:
-            q, s = mxfp4_empty(rows, k, x.device)
+            with _allocating(stream, x.device):
+                q, s = mxfp4_empty(rows, k, x.device)
             out += (q, s)
             args += [q.data_ptr(), max(MX_BLOCK_BYTES, q.shape[1]), s.data_ptr(), max(1, -(-s.shape[1] // 16) * 16)]
         else:
@@ -119,7 +130,8 @@ def mxfp4_dequant(codes, scale, k: int, out=None, stream=None, library=None):
     if -(-k // MX_BLOCK) != kb:
         raise ValueError(f"rows of {kb} blocks do not hold k = {k} values")
     if out is None:
-        out = torch.empty((R, k), dtype=torch.float16, device=codes.device)
+        with _allocating(stream, codes.device):
+            out = torch.empty((R, k), dtype=torch.float16, device=codes.device)
     Ro, Ko, ldo = _operand(out, "out")
     if (Ro, Ko) != (R, k):
         raise ValueError(f"out has shape {tuple(out.shape)}, expected {(R, k)}")
@@ -132,10 +144,11 @@ def mxfp4_dequant(codes, scale, k: int, out=None, stream=None, library=None):
     return out
 
 
-def _output(c, M, N, device):
+def _output(c, M, N, device, stream):
     import torch
     if c is None:
-        return torch.empty((M, N), dtype=torch.float16, device=device), max(1, N)
+        with _allocating(stream, device):
+            return torch.empty((M, N), dtype=torch.float16, device=device), max(1, N)
     Mc, Nc, ldc = _operand(c, "c")
     if (Mc, Nc) != (M, N):
         raise ValueError(f"c has shape {tuple(c.shape)}, expected {(M, N)}")
@@ -153,7 +166,7 @@ def mxfp4_gemm(a, scale_a, b, scale_b, c=None, relu: bool = False, stream=None, 
         raise ValueError(f"inner dimensions differ: rows of {kb} and {kb2} blocks")
     if a.device != b.device:
         raise ValueError("all operands must be on the same device")
-    c, ldc = _output(c, M, N, a.device)
+    c, ldc = _output(c, M, N, a.device, stream)
     args = (M, N, kb * MX_BLOCK, a.data_ptr(), lda, scale_a.data_ptr(), ldsa, b.data_ptr(), ldb, scale_b.data_ptr(),
             ldsb, c.data_ptr(), ldc, int(relu), _stream(stream, a.device))
     rc = (_call("mxfp4_gemm", args, a.device, library) if cfg is None
@@ -172,7 +185,7 @@ def mxfp4_gemm_f16(a, b, scale_b, c=None, relu: bool = False, stream=None, cfg: 
         raise ValueError(f"inner dimensions differ: a has {K} columns, b rows of {kb} blocks")
     if a.device != b.device:
         raise ValueError("all operands must be on the same device")
-    c, ldc = _output(c, M, N, a.device)
+    c, ldc = _output(c, M, N, a.device, stream)
     if M == 1 and lda % 8:  # one row: its stride is only its length (which the fast kernels want padded)
         lda = -(-lda // 8) * 8
     args = (M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb, scale_b.data_ptr(), ldsb, c.data_ptr(), ldc, int(relu),
