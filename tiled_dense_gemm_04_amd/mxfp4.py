@@ -10,8 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 
-from . import (SELECT_NOOP, SELECT_ZERO_FILL, TGEMM_OK, TgemmError, _as_stored, _dense_2d, _operand, lib,  # noqa: F401
-               matmul)
+from . import TGEMM_OK, TgemmError, _operand, lib, matmul
 
 MX_BLOCK = 32
 MX_BLOCK_BYTES = 16
@@ -37,7 +36,7 @@ def _call(name, args, device, library=None):
     """The library's entry point on ``device`` (made current for the call if it is not)."""
     import torch
     fn = getattr(library or lib(), name)
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         return fn(*args)
     with torch.cuda.device(device):
         return fn(*args)
@@ -59,37 +58,33 @@ def _allocating(stream, device):
     return torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream)
 
 
-def _rows_of_bytes(t, name):
-    """(rows, bytes per row, row stride) of a 2-D uint8 device tensor with contiguous rows."""
-    import torch
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.uint8:
-        raise TypeError(f"{name} must be uint8, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    rows, cols = t.shape
-    if rows == 0 or cols == 0:
-        return rows, cols, max(1, cols)
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have contiguous rows (stride(1) == 1)")
-    return rows, cols, t.stride(0) if rows > 1 else cols
-
-
 def _matrix(codes, scale, name):
-    """(rows, blocks, code stride, scale stride) of an MXFP4 matrix."""
-    rows, nbytes, ldq = _rows_of_bytes(codes, name)
-    srows, kb, lds = _rows_of_bytes(scale, f"scale of {name}")
+    """(rows, blocks, code stride, scale stride, device) of an MXFP4 matrix."""
+    import torch
+    for t, part in ((codes, name), (scale, f"scale of {name}")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{part} must be a torch.Tensor")
+        if t.dtype != torch.uint8:
+            raise TypeError(f"{part} must be uint8, got {t.dtype}")
+        if t.dim() != 2:
+            raise ValueError(f"{part} must be 2-D")
+        if not t.is_cuda:
+            raise ValueError(f"{part} must be a device tensor")
+    (rows, nbytes), (srows, kb) = codes.shape, scale.shape
     if nbytes != kb * MX_BLOCK_BYTES or srows != rows:
         raise ValueError(f"{name}: codes {tuple(codes.shape)} and scale {tuple(scale.shape)} do not belong together "
                          f"(rows of {MX_BLOCK_BYTES} bytes per block of {MX_BLOCK})")
-    if codes.device != scale.device:
+    device = codes.device
+    if scale.device != device:
         raise ValueError(f"{name}: codes and scale must be on the same device")
-    if rows <= 1:  # one row: its stride is only its length (which the fast kernels want padded)
-        lds = -(-lds // 16) * 16
-    return rows, kb, max(MX_BLOCK_BYTES, ldq), max(1, lds)
+    if rows == 0 or kb == 0:
+        return rows, kb, max(MX_BLOCK_BYTES, nbytes), max(1, kb), device
+    (ldq, cq), (lds, cs) = codes.stride(), scale.stride()
+    if cq != 1 or (cs != 1 and kb > 1):
+        raise ValueError(f"{name} must have contiguous rows (stride(1) == 1)")
+    if rows == 1:  # one row: its stride is only its length (for the scales padded as the fast kernels want it)
+        return 1, kb, nbytes, -(-kb // 16) * 16, device
+    return rows, kb, ldq, lds, device
 
 
 def mxfp4_empty(rows: int, k: int, device):
@@ -108,69 +103,69 @@ def mxfp4_quant(x, dims: str = "rows", stream=None, library=None):
     R, K, ldx = _operand(x, "x")
     if dims not in ("rows", "cols", "both"):
         raise ValueError(f"dims must be 'rows', 'cols' or 'both', got {dims!r}")
+    device = x.device
     out, args = (), []
     for want, rows, k in ((dims != "cols", R, K), (dims != "rows", K, R)):
         if want:
-            with _allocating(stream, x.device):
-                q, s = mxfp4_empty(rows, k, x.device)
+            if stream is None:
+                q, s = mxfp4_empty(rows, k, device)
+            else:
+                with _allocating(stream, device):
+                    q, s = mxfp4_empty(rows, k, device)
+            kb = -(-k // MX_BLOCK)
             out += (q, s)
-            args += [q.data_ptr(), max(MX_BLOCK_BYTES, q.shape[1]), s.data_ptr(), max(1, -(-s.shape[1] // 16) * 16)]
+            args += (q.data_ptr(), max(1, kb) * MX_BLOCK_BYTES, s.data_ptr(), max(1, -(-kb // 16) * 16))
         else:
-            args += [None, 0, None, 0]
-    rc = _call("mxfp4_quant", (R, K, x.data_ptr(), ldx, *args, _stream(stream, x.device)), x.device, library)
+            args += (None, 0, None, 0)
+    rc = _call("mxfp4_quant", (R, K, x.data_ptr(), ldx, *args, _stream(stream, device)), device, library)
     if rc != TGEMM_OK:
         raise TgemmError(rc, "mxfp4_quant")
     return out
 
 
-def mxfp4_dequant(codes, scale, k: int, out=None, stream=None, library=None):
-    """The fp16 values (R, k) of an MXFP4 matrix whose rows hold k values."""
-    import torch
-    R, kb, ldq, lds = _matrix(codes, scale, "codes")
-    if -(-k // MX_BLOCK) != kb:
-        raise ValueError(f"rows of {kb} blocks do not hold k = {k} values")
-    if out is None:
-        with _allocating(stream, codes.device):
-            out = torch.empty((R, k), dtype=torch.float16, device=codes.device)
-    Ro, Ko, ldo = _operand(out, "out")
-    if (Ro, Ko) != (R, k):
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(R, k)}")
-    if out.device != codes.device:
-        raise ValueError("codes and out must be on the same device")
-    rc = _call("mxfp4_dequant", (R, k, codes.data_ptr(), ldq, scale.data_ptr(), lds, out.data_ptr(), ldo,
-                                 _stream(stream, codes.device)), codes.device, library)
-    if rc != TGEMM_OK:
-        raise TgemmError(rc, "mxfp4_dequant")
-    return out
-
-
-def _output(c, M, N, device, stream):
-    import torch
+def _output(c, M, N, device, stream, name="c"):
+    """The fp16 output (allocated on the call's stream if None) and its row stride."""
     if c is None:
+        import torch
+        if stream is None:
+            return torch.empty((M, N), dtype=torch.float16, device=device), N or 1
         with _allocating(stream, device):
-            return torch.empty((M, N), dtype=torch.float16, device=device), max(1, N)
-    Mc, Nc, ldc = _operand(c, "c")
+            return torch.empty((M, N), dtype=torch.float16, device=device), N or 1
+    Mc, Nc, ldc = _operand(c, name)
     if (Mc, Nc) != (M, N):
-        raise ValueError(f"c has shape {tuple(c.shape)}, expected {(M, N)}")
+        raise ValueError(f"{name} has shape {tuple(c.shape)}, expected {(M, N)}")
     if c.device != device:
         raise ValueError("all operands must be on the same device")
     return c, ldc
 
 
+def mxfp4_dequant(codes, scale, k: int, out=None, stream=None, library=None):
+    """The fp16 values (R, k) of an MXFP4 matrix whose rows hold k values."""
+    R, kb, ldq, lds, device = _matrix(codes, scale, "codes")
+    if -(-k // MX_BLOCK) != kb:
+        raise ValueError(f"rows of {kb} blocks do not hold k = {k} values")
+    out, ldo = _output(out, R, k, device, stream, "out")
+    rc = _call("mxfp4_dequant", (R, k, codes.data_ptr(), ldq, scale.data_ptr(), lds, out.data_ptr(), ldo,
+                                 _stream(stream, device)), device, library)
+    if rc != TGEMM_OK:
+        raise TgemmError(rc, "mxfp4_dequant")
+    return out
+
+
 def mxfp4_gemm(a, scale_a, b, scale_b, c=None, relu: bool = False, stream=None, cfg: int | None = None, library=None):
     """C = ReLU?(A @ B^T) of two MXFP4 matrices, A (M x K) and B (N x K); c: (M, N) fp16
     (allocated if None). ``cfg`` forces a kernel (MX_*)."""
-    M, kb, lda, ldsa = _matrix(a, scale_a, "a")
-    N, kb2, ldb, ldsb = _matrix(b, scale_b, "b")
+    M, kb, lda, ldsa, device = _matrix(a, scale_a, "a")
+    N, kb2, ldb, ldsb, device_b = _matrix(b, scale_b, "b")
     if kb != kb2:
         raise ValueError(f"inner dimensions differ: rows of {kb} and {kb2} blocks")
-    if a.device != b.device:
+    if device_b != device:
         raise ValueError("all operands must be on the same device")
-    c, ldc = _output(c, M, N, a.device, stream)
+    c, ldc = _output(c, M, N, device, stream)
     args = (M, N, kb * MX_BLOCK, a.data_ptr(), lda, scale_a.data_ptr(), ldsa, b.data_ptr(), ldb, scale_b.data_ptr(),
-            ldsb, c.data_ptr(), ldc, int(relu), _stream(stream, a.device))
-    rc = (_call("mxfp4_gemm", args, a.device, library) if cfg is None
-          else _call("mxfp4_gemm_cfg", (cfg, *args), a.device, library))
+            ldsb, c.data_ptr(), ldc, int(relu), _stream(stream, device))
+    rc = (_call("mxfp4_gemm", args, device, library) if cfg is None
+          else _call("mxfp4_gemm_cfg", (cfg, *args), device, library))
     if rc != TGEMM_OK:
         raise TgemmError(rc, "mxfp4_gemm" if cfg is None else f"mxfp4_gemm_cfg[{cfg}]")
     return c
@@ -180,18 +175,18 @@ def mxfp4_gemm_f16(a, b, scale_b, c=None, relu: bool = False, stream=None, cfg: 
     """C = ReLU?(a @ W^T) of fp16 a (M, K) and an MXFP4 weight W (N x K values decoded to
     fp16); c: (M, N) fp16 (allocated if None). ``cfg`` forces a kernel (MX_*)."""
     M, K, lda = _operand(a, "a")
-    N, kb, ldb, ldsb = _matrix(b, scale_b, "b")
+    N, kb, ldb, ldsb, device = _matrix(b, scale_b, "b")
     if -(-K // MX_BLOCK) != kb:
         raise ValueError(f"inner dimensions differ: a has {K} columns, b rows of {kb} blocks")
-    if a.device != b.device:
+    if a.device != device:
         raise ValueError("all operands must be on the same device")
-    c, ldc = _output(c, M, N, a.device, stream)
+    c, ldc = _output(c, M, N, device, stream)
     if M == 1 and lda % 8:  # one row: its stride is only its length (which the fast kernels want padded)
         lda = -(-lda // 8) * 8
     args = (M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb, scale_b.data_ptr(), ldsb, c.data_ptr(), ldc, int(relu),
-            _stream(stream, a.device))
-    rc = (_call("mxfp4_gemm_f16", args, a.device, library) if cfg is None
-          else _call("mxfp4_gemm_f16_cfg", (cfg, *args), a.device, library))
+            _stream(stream, device))
+    rc = (_call("mxfp4_gemm_f16", args, device, library) if cfg is None
+          else _call("mxfp4_gemm_f16_cfg", (cfg, *args), device, library))
     if rc != TGEMM_OK:
         raise TgemmError(rc, "mxfp4_gemm_f16" if cfg is None else f"mxfp4_gemm_f16_cfg[{cfg}]")
     return c
@@ -217,10 +212,59 @@ def mxfp4_linear(x, w_codes, scale_w, relu: bool = False, out=None, stream=None)
     return mxfp4_gemm(q, s, w_codes, scale_w, c=out, relu=relu, stream=stream)
 
 
-def _row_major(x):
-    """A gradient as the library takes it: rows contiguous (a copy for any other view)."""
-    x = _dense_2d(x)
-    return x if x.shape[1] <= 1 or x.stride(1) == 1 else x.contiguous()
+def _row_major(x, name):
+    """A 2-D fp16 device tensor as the library takes it: rows contiguous (a copy for any other
+    view)."""
+    import torch
+    if not isinstance(x, torch.Tensor) or x.dtype != torch.float16 or x.dim() != 2 or not x.is_cuda:
+        raise TypeError(f"{name} must be a 2-D float16 device tensor")
+    rows, cols = x.shape
+    ld, step = x.stride()
+    return x if (cols <= 1 or step == 1) and (rows <= 1 or ld >= cols) else x.contiguous()
+
+
+class _Packed:
+    """MXFP4 matrices in one allocation (a step of a linear layer makes six of them): ``add``
+    plans one and returns (rows, k, code offset, code stride, scale offset, scale stride)."""
+
+    def __init__(self, device):
+        self.device, self.nbytes, self.base = device, 0, 0
+
+    def add(self, rows, k):
+        kb = -(-k // MX_BLOCK) or 1
+        ldq, lds = kb * MX_BLOCK_BYTES, -(-kb // 16) * 16
+        at = self.nbytes
+        self.nbytes = at + rows * (ldq + lds)
+        return rows, k, at, ldq, at + rows * ldq, lds
+
+    def allocate(self):
+        import torch
+        self.tensor = torch.empty(self.nbytes, dtype=torch.uint8, device=self.device)
+        self.base = self.tensor.data_ptr()
+        return self.tensor
+
+
+def _packed_quant(x, rows, cols, rows_base, cols_base):
+    """Quantise x into planned matrices (None: not wanted)."""
+    R, K = x.shape
+    ldx = x.stride(0) if R > 1 else max(1, K)
+    a = (rows_base + rows[2], rows[3], rows_base + rows[4], rows[5]) if rows else (None, 0, None, 0)
+    b = (cols_base + cols[2], cols[3], cols_base + cols[4], cols[5]) if cols else (None, 0, None, 0)
+    device = x.device
+    rc = _call("mxfp4_quant", (R, K, x.data_ptr(), ldx, *a, *b, _stream(None, device)), device)
+    if rc != TGEMM_OK:
+        raise TgemmError(rc, "mxfp4_quant")
+
+
+def _packed_gemm(a, a_base, b, b_base, device):
+    import torch
+    M, N = a[0], b[0]
+    c = torch.empty((M, N), dtype=torch.float16, device=device)
+    rc = _call("mxfp4_gemm", (M, N, a[1], a_base + a[2], a[3], a_base + a[4], a[5], b_base + b[2], b[3], b_base + b[4],
+                              b[5], c.data_ptr(), N or 1, 0, _stream(None, device)), device)
+    if rc != TGEMM_OK:
+        raise TgemmError(rc, "mxfp4_gemm")
+    return c
 
 
 def autograd_functions():
@@ -235,23 +279,35 @@ def autograd_functions():
 
         @staticmethod
         def forward(ctx, x, w):
-            if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
-                raise ValueError(f"x {tuple(x.shape)} and w {tuple(w.shape)} must be (M, K) and (N, K)")
-            x, w = _row_major(x), _row_major(w)
-            xq = mxfp4_quant(x, "both" if ctx.needs_input_grad[1] else "rows")
-            wq = mxfp4_quant(w, "both" if ctx.needs_input_grad[0] else "rows")
-            ctx.save_for_backward(*xq[2:], *wq[2:])
-            return mxfp4_gemm(*xq[:2], *wq[:2])
+            x, w = _row_major(x, "x"), _row_major(w, "w")
+            if x.shape[1] != w.shape[1] or x.device != w.device:
+                raise ValueError(f"x {tuple(x.shape)} and w {tuple(w.shape)} must be (M, K) and (N, K) on one device")
+            need_x, need_w = ctx.needs_input_grad
+            rows, cols = _Packed(x.device), _Packed(x.device)
+            xq, wq = rows.add(*x.shape), rows.add(*w.shape)
+            ctx.xt = cols.add(x.shape[1], x.shape[0]) if need_w else None
+            ctx.wt = cols.add(w.shape[1], w.shape[0]) if need_x else None
+            kept = cols.allocate()
+            rows.allocate()
+            ctx.save_for_backward(kept)
+            _packed_quant(x, xq, ctx.xt, rows.base, cols.base)
+            _packed_quant(w, wq, ctx.wt, rows.base, cols.base)
+            return _packed_gemm(xq, rows.base, wq, rows.base, x.device)
 
         @staticmethod
         @once_differentiable
         def backward(ctx, dy):
-            saved = ctx.saved_tensors
             need_x, need_w = ctx.needs_input_grad
-            dims = "both" if need_x and need_w else "rows" if need_x else "cols"
-            q = mxfp4_quant(_row_major(dy), dims)
-            dx = mxfp4_gemm(*q[:2], *saved[-2:]) if need_x else None
-            dw = mxfp4_gemm(*q[-2:], *saved[:2]) if need_w else None
+            dy = _row_major(dy, "dy")
+            tmp = _Packed(dy.device)
+            M, N = dy.shape
+            q = tmp.add(M, N) if need_x else None
+            qt = tmp.add(N, M) if need_w else None
+            tmp.allocate()
+            kept = ctx.saved_tensors[0].data_ptr()
+            _packed_quant(dy, q, qt, tmp.base, tmp.base)
+            dx = _packed_gemm(q, tmp.base, ctx.wt, kept, dy.device) if need_x else None
+            dw = _packed_gemm(qt, tmp.base, ctx.xt, kept, dy.device) if need_w else None
             return dx, dw
 
     class Mxfp4WeightFunction(torch.autograd.Function):
@@ -260,7 +316,7 @@ def autograd_functions():
 
         @staticmethod
         def forward(ctx, x, codes, scale):
-            x = _row_major(x)
+            x = _row_major(x, "x")
             ctx.save_for_backward(codes, scale)
             ctx.k = x.shape[1]
             return mxfp4_gemm_f16(x, codes, scale)
@@ -271,6 +327,6 @@ def autograd_functions():
             if not ctx.needs_input_grad[0]:
                 return None, None, None
             codes, scale = ctx.saved_tensors
-            return matmul(_row_major(dy), mxfp4_dequant(codes, scale, ctx.k)), None, None
+            return matmul(_row_major(dy, "dy"), mxfp4_dequant(codes, scale, ctx.k)), None, None
 
     return {"Mxfp4LinearFunction": Mxfp4LinearFunction, "Mxfp4WeightFunction": Mxfp4WeightFunction}
