@@ -255,28 +255,32 @@ __global__ __launch_bounds__(256) void dequant_mxfp4_rows(MxDequantArgs q) {
 // its scale byte sits in a register beside it, so nothing is folded outside the MFMA.
 // A k-tile of 128 codes is 64 bytes a row, the bytes of a binary16 k-tile of 32: operand
 // copies, range-checked edges, swizzle and the four-slot ring are the binary16 ping-pong's
-// (PpOperand on code rows seen as halves).
-// Scales come in groups of four k-tiles, 16 bytes a row and one 16-byte copy per row, in a
-// ring of two groups: group s goes with tile 4 s, when the last read of group s - 2 (tile
-// 4 s - 5) lies a barrier back. In the last group bytes past KB are whatever the padding
-// holds: a lane whose block lies past KB takes the last block's scale instead, and its codes
-// are zeros (out-of-range copies).
+// (PpOperand on code rows seen as halves). 128 x 128 tiles take k-tiles of 256 codes (KS = 2):
+// their few MFMAs per k-tile leave the barriers and latencies between them in the open.
+// Scales come in groups of 16 blocks, 16 bytes a row and one 16-byte copy per row, with the
+// first k-tile of the group. In the last group bytes past KB are whatever the padding holds: a
+// lane whose block lies past KB takes the last block's scale instead, and its codes are zeros
+// (out-of-range copies).
 // Requirements (host): A, B, SA, SB 16-byte aligned, their row strides multiples of 16.
-struct MxScaleRing {
-  static constexpr int GROUP = 4;  // k-tiles per group
-};
+// Slots of the scale ring. Group 1 copies scale group s with its first tile t = G s (G = 4 / KS
+// k-tiles per group) in iteration t - STAGES + 1, when tiles up to that one may still be read: the
+// slot's former group s - slots must end before it, G (s - slots) + G - 1 < G s - STAGES + 1.
+constexpr int mx_scale_slots(int ks, int stages) { return (4 / ks) * (2 - 1) > stages - 2 ? 2 : 4; }
+static_assert(4 * (4 - 1) > 4 - 2 && 2 * (4 - 1) > 4 - 2, "four slots are enough for both k-tiles");
 
-template <int BM, int BN, int WM, int WN, int STAGES>
+template <int BM, int BN, int KS, int STAGES>
 constexpr int mx_lds_bytes() {
-  return STAGES * (BM + BN) * 64 + 2 * (BM + BN) * 16;
+  return STAGES * (BM + BN) * 64 * KS + mx_scale_slots(KS, STAGES) * (BM + BN) * 16;
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES, int PANEL>
+template <int BM, int BN, int KS, int WM, int WN, int STAGES, int PANEL>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_mxfp4_pp(MxGemmArgs g) {
   constexpr int NW = WM * WN, WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
-  using OpA = PpOperand<BM, 32, 16, true, NW>;
-  using OpB = PpOperand<BN, 32, 16, true, NW>;
+  using OpA = PpOperand<BM, 32 * KS, 16, true, NW>;
+  using OpB = PpOperand<BN, 32 * KS, 16, true, NW>;
   constexpr int A_BYTES = OpA::BYTES, B_BYTES = OpB::BYTES, PT = OpA::LD + OpB::LD;
+  constexpr int TB = 4 * KS, GROUP = 16 / TB;       // blocks per row of a k-tile, k-tiles per scale group
+  constexpr int SLOTS = mx_scale_slots(KS, STAGES);
   constexpr int SG_BYTES = (BM + BN) * 16;  // one scale group: A's rows, then B's
   constexpr int SC_A = BM / 64, SC_B = BN / 64;
   static_assert(NW == 8 && OpA::REM == 0 && OpB::REM == 0 && (SC_A + SC_B == 4 || SC_A + SC_B == 8) && STAGES <= 4, "copies");
@@ -292,8 +296,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_mxfp4_pp(MxGemmArgs g) {
   tile_of(blockIdx.x, g.tiles_m, g.tiles_n, PANEL, 1, &tm, &tn);
   const int row0 = (int)tm * BM, col0 = (int)tn * BN;
   const int mvalid = min(BM, g.M - row0), nvalid = min(BN, g.N - col0);
-  const int nk = (g.KB + 3) / 4;
-  const int kin_last = (g.KB - (nk - 1) * 4) * (kMxBlockBytes / 2);  // in halves
+  const int nk = (g.KB + TB - 1) / TB;
+  const int kin_last = (g.KB - (nk - 1) * TB) * (kMxBlockBytes / 2);  // in halves
 
   OpA opa;
   OpB opb;
@@ -310,13 +314,13 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_mxfp4_pp(MxGemmArgs g) {
     const int64_t ld = is_a ? g.ldsa : g.ldsb;
     const uint8_t* const base = is_a ? g.SA + (int64_t)(row0 + r) * ld : g.SB + (int64_t)(col0 + r) * ld;
     const int left = (is_a ? mvalid : nvalid) - r;
-    dma_to_lds(make_rsrc(base + (int64_t)sg * 16, kMaxRange), lds_addr(s_lds) + (sg & 1) * SG_BYTES + part * 1024,
+    dma_to_lds(make_rsrc(base + (int64_t)sg * 16, kMaxRange), lds_addr(s_lds) + (sg % SLOTS) * SG_BYTES + part * 1024,
                lane < left ? (uint32_t)lane * (uint32_t)ld : kOob);
   };
   auto copy_tile = [&](int t, auto group) __attribute__((always_inline)) {
-    if (decltype(group)::value == 1 && t % MxScaleRing::GROUP == 0 && t < nk) {
-      copy_scales(t / MxScaleRing::GROUP, wave - 4);
-      if (SC_A + SC_B > 4) copy_scales(t / MxScaleRing::GROUP, wave);
+    if (decltype(group)::value == 1 && t % GROUP == 0 && t < nk) {
+      copy_scales(t / GROUP, wave - 4);
+      if (SC_A + SC_B > 4) copy_scales(t / GROUP, wave);
     }
     const int4v ra = opa.rsrc(t, nk, nk), rb = opb.rsrc(t, nk, nk);
     const int slot = t % STAGES;
@@ -335,21 +339,25 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_mxfp4_pp(MxGemmArgs g) {
   const char* const sa_lds = s_lds + (wm * WTM + lrow) * 16;
   const char* const sb_lds = s_lds + (BM + wn * WTN + lrow) * 16;
 
-  half8 fa[FM], fb[FN];
-  int sa[FM], sb[FN];
+  half8 fa[KS][FM], fb[KS][FN];
+  int sa[KS][FM], sb[KS][FN];
   auto read_tile = [&](int t) __attribute__((always_inline)) {
     const char* const As = a_lds + (t % STAGES) * A_BYTES;
     const char* const Bs = b_lds + (t % STAGES) * B_BYTES;
-    const int off = ((t / MxScaleRing::GROUP) & 1) * SG_BYTES + 4 * (t % MxScaleRing::GROUP) + max(min(lblk, g.KB - 1 - 4 * t), 0);
+    const int group = (t / GROUP % SLOTS) * SG_BYTES + TB * (t % GROUP);
 #pragma unroll
-    for (int fn = 0; fn < FN; ++fn) {
-      fb[fn] = opb.frag(Bs, fn, 0);
-      sb[fn] = *(const TG_LDS uint8_t*)(sb_lds + off + fn * 256);
-    }
+    for (int ks = 0; ks < KS; ++ks) {
+      const int off = group + max(min(4 * ks + lblk, g.KB - 1 - TB * t), 0);
 #pragma unroll
-    for (int fm = 0; fm < FM; ++fm) {
-      fa[fm] = opa.frag(As, fm, 0);
-      sa[fm] = *(const TG_LDS uint8_t*)(sa_lds + off + fm * 256);
+      for (int fn = 0; fn < FN; ++fn) {
+        fb[ks][fn] = opb.frag(Bs, fn, ks);
+        sb[ks][fn] = *(const TG_LDS uint8_t*)(sb_lds + off + fn * 256);
+      }
+#pragma unroll
+      for (int fm = 0; fm < FM; ++fm) {
+        fa[ks][fm] = opa.frag(As, fm, ks);
+        sa[ks][fm] = *(const TG_LDS uint8_t*)(sa_lds + off + fm * 256);
+      }
     }
   };
 
@@ -365,15 +373,18 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_mxfp4_pp(MxGemmArgs g) {
   // Operands go in as (B fragment, A fragment), so a lane holds four consecutive columns.
   auto mma_tile = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int fm = 0; fm < FM; ++fm)
+    for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int fn = 0; fn < FN; ++fn)
-        acc[fm][fn] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(fb[fn]), wide(fa[fm]), acc[fm][fn], 4, 4, 0, sb[fn], 0, sa[fm]);
+      for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+          acc[fm][fn] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(fb[ks][fn]), wide(fa[ks][fm]), acc[fm][fn], 4, 4, 0,
+                                                                        sb[ks][fn], 0, sa[ks][fm]);
   };
-  pingpong_schedule<STAGES, PT, PT, (BM == 256 && BN == 256)>(wave / 4, nk, copy_tile, read_tile, mma_tile);
+  pingpong_schedule<STAGES, PT, PT, false>(wave / 4, nk, copy_tile, read_tile, mma_tile);
 
   using ST = StagedTile<WTM, WTN>;
-  static_assert(NW * ST::BYTES <= mx_lds_bytes<BM, BN, WM, WN, STAGES>(), "staged tile fits in the ring");
+  static_assert(NW * ST::BYTES <= mx_lds_bytes<BM, BN, KS, STAGES>(), "staged tile fits in the ring");
   __syncthreads();
   char* const stage = smem + wave * ST::BYTES;
   if (g.relu != 0)
@@ -483,7 +494,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f16_mxfp4_pp(MxGemmArgs g) 
   };
   // every wave copies at least A's share of a tile (waves 0 .. BW-1 one more)
   constexpr int PT = OpA::LD;
-  pingpong_schedule<STAGES, PT, PT, (BM == 256 && BN == 256)>(wave / 4, nk, copy_tile, read_tile, mma_tile);
+  pingpong_schedule<STAGES, PT, PT, false>(wave / 4, nk, copy_tile, read_tile, mma_tile);
 
   using ST = StagedTile<WTM, WTN>;
   static_assert(NW * ST::BYTES <= 160 * 1024, "staged tile");
@@ -695,14 +706,14 @@ hipError_t launch_big(K kern, int lds, std::atomic<uint64_t>& ready, const MxGem
   return hipGetLastError();
 }
 
-template <int BM, int BN, int STAGES>
+template <int BM, int BN, int KS, int STAGES>
 hipError_t launch_mx_pp(bool f16_a, const MxGemmArgs& g, hipStream_t s, int device) {
   static std::atomic<uint64_t> ready[2];
   if (f16_a) {
     constexpr int ring = wq_lds_bytes<BM, BN, 2, 4, STAGES>(), st = 8 * StagedTile<BM / 2, BN / 4>::BYTES;
     return launch_big(gemm_f16_mxfp4_pp<BM, BN, 2, 4, STAGES, 4>, ring > st ? ring : st, ready[1], g, s, device);
   }
-  return launch_big(gemm_mxfp4_pp<BM, BN, 2, 4, STAGES, 4>, mx_lds_bytes<BM, BN, 2, 4, STAGES>(), ready[0], g, s, device);
+  return launch_big(gemm_mxfp4_pp<BM, BN, KS, 2, 4, STAGES, 4>, mx_lds_bytes<BM, BN, KS, STAGES>(), ready[0], g, s, device);
 }
 
 template <bool F16A>
@@ -726,8 +737,8 @@ hipError_t launch_mxfp4(int cfg, bool f16_a, const MxGemmArgs& args, hipStream_t
   g.tiles_n = (int)ceil_div(g.N, tile);
   switch (cfg) {
     case kMxSkinny: return f16_a ? launch_skinny<true>(g, s) : launch_skinny<false>(g, s);
-    case kMx128: return launch_mx_pp<128, 128, 4>(f16_a, g, s, device);
-    case kMx256: return launch_mx_pp<256, 256, 4>(f16_a, g, s, device);
+    case kMx128: return launch_mx_pp<128, 128, 2, 4>(f16_a, g, s, device);
+    case kMx256: return launch_mx_pp<256, 256, 1, 4>(f16_a, g, s, device);
     default: break;
   }
   const dim3 grid((unsigned)((int64_t)g.tiles_m * g.tiles_n));

@@ -10,7 +10,7 @@ namespace tgemm {
 // padded to multiples of kOrthPad in the workspace (zeros there). The iterate keeps G's
 // orientation: m x n, or n x m when G is tall.
 constexpr int kOrthPad = 64;
-constexpr int kOrthParts = 128;  // partial sums of squares per matrix
+constexpr int kOrthParts = 512;  // partial sums of squares per matrix, at most
 
 struct OrthArgs {
   const void* G;
@@ -18,6 +18,7 @@ struct OrthArgs {
   int64_t ldg, stride_g, ldx, stride_x;  // elements
   int batch, R, C, f32, tall;
   int mp, np;                            // padded m and n
+  int nparts;                            // partial sums of squares per matrix
   float a, b, c, scale;
   // workspace (batch of each): sums of squares, the iterate's high and low halves twice, the
   // Gram matrix without its diagonal and its diagonal, the polynomial likewise

@@ -35,79 +35,90 @@ constexpr double kNormEps = 1e-7;
 __device__ __forceinline__ float joined(_Float16 hi, _Float16 lo) { return (float)hi + (float)lo * (1.0f / kLo); }
 __device__ __forceinline__ _Float16 low_half(float x, _Float16 hi) { return (_Float16)((x - (float)hi) * kLo); }
 
-// Sums of squares of a matrix, kOrthParts partial sums in float64 (squares of float32 values
-// leave float32's range). Bound by reading G.
+// Eight values of row r, columns c .. c + 7, of matrix bt as float32, zeros past the row (any
+// alignment: one or two 16-byte loads, single ones at the row's end).
+__device__ __forceinline__ void load_g(const OrthArgs& g, int bt, uint32_t r, uint32_t c, float (&v)[8]) {
+  const int64_t at = (int64_t)bt * g.stride_g + (int64_t)r * g.ldg + c;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+  if (r >= (uint32_t)g.R) return;
+  if (c + 8 <= (uint32_t)g.C) {
+    if (g.f32) {
+      __builtin_memcpy(v, (const float*)g.G + at, 32);
+    } else {
+      half8 h;
+      __builtin_memcpy(&h, (const _Float16*)g.G + at, 16);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = (float)h[e];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+      if (c + e < (uint32_t)g.C) v[e] = g.f32 ? ((const float*)g.G)[at + e] : (float)((const _Float16*)g.G)[at + e];
+  }
+}
+
+// Sums of squares of a matrix, g.nparts partial sums in float64 (squares of float32 values
+// leave float32's range), four chunks of eight values per thread in flight. Bound by reading G.
 __global__ __launch_bounds__(256) void orth_norm(OrthArgs g) {
   __shared__ double w[4];
-  const int part = blockIdx.x % kOrthParts, bt = blockIdx.x / kOrthParts;
-  const int64_t total = (int64_t)g.R * g.C;
-  const int64_t per = ((total + kOrthParts - 1) / kOrthParts + 7) / 8 * 8;
-  const int64_t lo = part * per, hi = lo + per < total ? lo + per : total;
+  const uint32_t part = blockIdx.x % g.nparts, bt = blockIdx.x / g.nparts;
+  const uint32_t cpr = ((uint32_t)g.C + 7) / 8, total = cpr * (uint32_t)g.R;
   double s = 0.0;
-  for (int64_t i = lo + (int64_t)threadIdx.x * 8; i < hi; i += 256 * 8) {
-    int64_t r = i / g.C;
-    int c = (int)(i - r * g.C);
-    int64_t at = (int64_t)bt * g.stride_g + r * g.ldg;
-    if (c + 8 <= g.C && i + 8 <= hi) {
-      float v[8];
-      if (g.f32) {
-        __builtin_memcpy(v, (const float*)g.G + at + c, 32);
-      } else {
-        half8 h;
-        __builtin_memcpy(&h, (const _Float16*)g.G + at + c, 16);
+  for (uint32_t u0 = part * 1024 + threadIdx.x; u0 < total; u0 += g.nparts * 1024) {
+    float v[4][8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = (float)h[e];
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s += (double)v[e] * (double)v[e];
-    } else {
-      for (int e = 0; e < 8 && i + e < hi; ++e) {
-        const double v = g.f32 ? (double)((const float*)g.G)[at + c] : (double)((const _Float16*)g.G)[at + c];
-        s += v * v;
-        if (++c == g.C) {
-          c = 0;
-          at += g.ldg;
-        }
-      }
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = u0 + 256 * i, r = u / cpr;
+      load_g(g, bt, u < total ? r : (uint32_t)g.R, (u - r * cpr) * 8, v[i]);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += (double)v[i][e] * (double)v[i][e];
   }
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
   if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = s;
   __syncthreads();
-  if (threadIdx.x == 0) g.parts[blockIdx.x] = (w[0] + w[1]) + (w[2] + w[3]);
+  if (threadIdx.x == 0) g.parts[bt * kOrthParts + part] = (w[0] + w[1]) + (w[2] + w[3]);
 }
 
-// X_0 = G / (|G| + eps) as two halves, padded with zeros: eight values per thread.
+// X_0 = G / (|G| + eps) as two halves, padded with zeros: two chunks of eight values per thread.
 __global__ __launch_bounds__(256) void orth_start(OrthArgs g) {
   __shared__ double inv;
-  const int rp = g.tall ? g.np : g.mp, cp = g.tall ? g.mp : g.np;
-  const int64_t chunks = (int64_t)rp * (cp / 8), groups = (chunks + 255) / 256;
-  const int bt = (int)(blockIdx.x / groups);
+  const uint32_t rp = g.tall ? g.np : g.mp, cpr = (g.tall ? g.mp : g.np) / 8;
+  const uint32_t total = rp * cpr, groups = (total + 511) / 512;
+  const uint32_t bt = blockIdx.x / groups, u0 = (blockIdx.x - bt * groups) * 512 + threadIdx.x;
+  float v[2][8];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t u = u0 + 256 * i, r = u / cpr;
+    load_g(g, bt, u < total ? r : (uint32_t)g.R, (u - r * cpr) * 8, v[i]);
+  }
   if (threadIdx.x < 64) {
-    double s = g.parts[bt * kOrthParts + threadIdx.x] + g.parts[bt * kOrthParts + 64 + threadIdx.x];
+    double s = 0.0;
+    for (uint32_t i = threadIdx.x; i < (uint32_t)g.nparts; i += 64) s += g.parts[bt * kOrthParts + i];
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o, 64);
     if (threadIdx.x == 0) inv = 1.0 / (sqrt(s) + kNormEps);
   }
   __syncthreads();
-  const int64_t u = (blockIdx.x - bt * groups) * 256 + threadIdx.x;
-  if (u >= chunks) return;
-  const int r = (int)(u / (cp / 8)), c = (int)(u % (cp / 8)) * 8;
-  half8 hi, lo;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    float x = 0.0f;
-    if (r < g.R && c + e < g.C) {
-      const int64_t at = (int64_t)bt * g.stride_g + (int64_t)r * g.ldg + c + e;
-      x = (float)((g.f32 ? (double)((const float*)g.G)[at] : (double)((const _Float16*)g.G)[at]) * inv);
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t u = u0 + 256 * i;
+    if (u >= total) continue;
+    half8 hi, lo;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = (float)((double)v[i][e] * inv);
+      hi[e] = (_Float16)x;
+      lo[e] = low_half(x, hi[e]);
     }
-    hi[e] = (_Float16)x;
-    lo[e] = low_half(x, hi[e]);
+    const int64_t o = ((int64_t)bt * total + u) * 8;
+    *(half8*)(g.hi[0] + o) = hi;
+    *(half8*)(g.lo[0] + o) = lo;
   }
-  const int64_t o = (int64_t)bt * rp * cp + (int64_t)r * cp + c;
-  *(half8*)(g.hi[0] + o) = hi;
-  *(half8*)(g.lo[0] + o) = lo;
 }
 
 // ------------------------------------------------------------------------------------
@@ -119,17 +130,22 @@ struct OrthStep {
   int in, last;  // which of the two iterate buffers is read; the final step writes the result
 };
 
+// k-tiles of 32, or of 64 for the smaller tiles, whose few MFMAs per k-tile leave the barriers
+// and latencies between them in the open.
+template <int BM>
+constexpr int kOrthKs = BM == 128 ? 2 : 1;
+
 template <int BM>
 constexpr int orth_lds_bytes() {
   // the operand ring, or the staged tiles of the epilogue (per wave, transposed with a 16-byte
   // pad per column), whichever is larger
-  constexpr int ring = 4 * 2 * BM * 64, st = 8 * (BM / 4) * (BM / 2 * 2 + 16);
+  constexpr int ring = 4 * 2 * BM * 64 * kOrthKs<BM>, st = 8 * (BM / 4) * (BM / 2 * 2 + 16);
   return ring > st ? ring : st;
 }
 
 template <Product P, int BM, bool TALL>
 __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
-  constexpr int NW = 8, WM = 2, WN = 4, STAGES = 4, BK = 32;
+  constexpr int NW = 8, WM = 2, WN = 4, STAGES = 4, KS = kOrthKs<BM>, BK = 32 * KS;
   constexpr int WTM = BM / WM, WTN = BM / WN, FM = WTM / 16, FN = WTN / 16;
   // Gram: rows of the wide iterate, or columns of the tall one; Square: E is its own
   // transpose; Apply: P times the wide iterate (k along its rows), or the tall one times P.
@@ -196,14 +212,17 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
   const int wm = wave / WN, wn = wave % WN, lrow = lane & 15, lkg = lane >> 4;
   opa.init_frags(wm * WTM, lane);
   opb.init_frags(wn * WTN, lane);
-  half8 fa[FM], fb[FN];
+  half8 fa[KS][FM], fb[KS][FN];
   auto read_tile = [&](int kt) __attribute__((always_inline)) {
     const char* const As = a_lds + (kt % STAGES) * A_BYTES;
     const char* const Bs = b_lds + (kt % STAGES) * B_BYTES;
 #pragma unroll
-    for (int fm = 0; fm < FM; ++fm) fa[fm] = opa.frag(As, fm, 0);
+    for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll
-    for (int fn = 0; fn < FN; ++fn) fb[fn] = opb.frag(Bs, fn, 0);
+      for (int fm = 0; fm < FM; ++fm) fa[ks][fm] = opa.frag(As, fm, ks);
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn) fb[ks][fn] = opb.frag(Bs, fn, ks);
+    }
   };
   float4v acc[FM][FN];
 #pragma unroll
@@ -212,10 +231,12 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
     for (int j = 0; j < FN; ++j) acc[i][j] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
   auto mma_tile = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int fm = 0; fm < FM; ++fm)
+    for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int fn = 0; fn < FN; ++fn)
-        acc[fm][fn] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[fn], fa[fm], acc[fm][fn], 0, 0, 0);
+      for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+          acc[fm][fn] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[ks][fn], fa[ks][fm], acc[fm][fn], 0, 0, 0);
   };
   pingpong_schedule<STAGES, PT, PT, (A_KMAJ && B_KMAJ && BM == 256)>(wave / 4, nk, copy_tile, read_tile, mma_tile);
   __syncthreads();  // the ring is free for staging
@@ -229,23 +250,38 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
   const int rv = rows - wr0, cv = cols - wc0;
 
   if constexpr (P == kApply) {
-    // X' = diag(P) X + offdiag(P) hi(X)
-#pragma unroll
-    for (int fm = 0; fm < FM; ++fm) {
-      const int r = wr0 + 16 * fm + lrow;
-      const float dr = !TALL && r < rows ? DP[r] : 0.0f;
+    // X' = diag(P) X + offdiag(P) hi(X). The old values of kAhead rows of tiles are in flight.
+    constexpr int kAhead = FM < 3 ? FM : 3;
+    half4 h[kAhead][FN], l[kAhead][FN];
+    float dr[kAhead];
+    auto fetch = [&](auto fm_c) __attribute__((always_inline)) {
+      constexpr int fm = decltype(fm_c)::value;
+      const int r = wr0 + 16 * fm + lrow, rr = min(r, rows - 1);
+      dr[fm % kAhead] = TALL ? 0.0f : DP[rr];
 #pragma unroll
       for (int fn = 0; fn < FN; ++fn) {
-        const int c = wc0 + 16 * fn + 4 * lkg;
-        if (r >= rows || c >= cols) continue;
-        const half4 h = *(const half4*)(hi + (int64_t)r * ldx + c), l = *(const half4*)(lo + (int64_t)r * ldx + c);
-        float4v d = {dr, dr, dr, dr};
-        if (TALL) d = *(const float4v*)(DP + c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[fm][fn][e] += d[e] * joined(h[e], l[e]);
+        const int c = min(wc0 + 16 * fn + 4 * lkg, cols - 4);
+        h[fm % kAhead][fn] = *(const half4*)(hi + (int64_t)rr * ldx + c);
+        l[fm % kAhead][fn] = *(const half4*)(lo + (int64_t)rr * ldx + c);
       }
-      __builtin_amdgcn_sched_barrier(0);  // one row's loads in flight: all of them would spill
+    };
+    float4v dc[FN];
+    if constexpr (TALL) {
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn) dc[fn] = *(const float4v*)(DP + min(wc0 + 16 * fn + 4 * lkg, cols - 4));
     }
+    static_for<kAhead>([&](auto i) __attribute__((always_inline)) { fetch(i); });
+    static_for<FM>([&](auto fm_c) __attribute__((always_inline)) {
+      constexpr int fm = decltype(fm_c)::value;
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          acc[fm][fn][e] += (TALL ? dc[fn][e] : dr[fm % kAhead]) * joined(h[fm % kAhead][fn][e], l[fm % kAhead][fn][e]);
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (fm + kAhead < FM) fetch(std::integral_constant<int, fm + kAhead>{});
+    });
     if (st.last) {
 #pragma unroll
       for (int fm = 0; fm < FM; ++fm)
@@ -280,31 +316,57 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
   } else {
     _Float16* const out = P == kGram ? E : PM;
     float* const dout = P == kGram ? D : DP;
-#pragma unroll
-    for (int fm = 0; fm < FM; ++fm) {
+    // Row fm of tiles: the diagonal, kept apart in float32, leaves the tile.
+    auto split_diagonal = [&](auto fm_c) __attribute__((always_inline)) {
+      constexpr int fm = decltype(fm_c)::value;
       const int r = wr0 + 16 * fm + lrow;
-      const float dr = P == kSquare && r < rows ? D[r] : 0.0f;
 #pragma unroll
       for (int fn = 0; fn < FN; ++fn) {
-        const int c = wc0 + 16 * fn + 4 * lkg;
-        if (r >= rows || c >= cols) continue;
-        if constexpr (P == kSquare) {
-          const half4 x = *(const half4*)(E + (int64_t)r * g.mp + c);
-          const float4v d = *(const float4v*)(D + c);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float s = acc[fm][fn][e];
-            acc[fm][fn][e] = r == c + e ? g.a + g.b * dr + g.c * (dr * dr + s)
-                                        : g.b * (float)x[e] + g.c * ((dr + d[e]) * (float)x[e] + s);
-          }
-        }
+        const int d = r - (wc0 + 16 * fn + 4 * lkg);  // 0 .. 3: the lane holds the diagonal's value
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (r == c + e) {
-            dout[r] = acc[fm][fn][e];
+          if (d == e) {
+            if (r < rows) dout[r] = acc[fm][fn][e];
             acc[fm][fn][e] = 0.0f;
           }
       }
+    };
+    if constexpr (P == kSquare) {
+      // P from E, D and E E; the E values of kAhead rows of tiles are in flight
+      constexpr int kAhead = FM < 3 ? FM : 3;
+      half4 x[kAhead][FN];
+      float dr[kAhead];
+      float4v dc[FN];
+      auto fetch = [&](auto fm_c) __attribute__((always_inline)) {
+        constexpr int fm = decltype(fm_c)::value;
+        const int rr = min(wr0 + 16 * fm + lrow, rows - 1);
+        dr[fm % kAhead] = D[rr];
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+          x[fm % kAhead][fn] = *(const half4*)(E + (int64_t)rr * g.mp + min(wc0 + 16 * fn + 4 * lkg, cols - 4));
+      };
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn) dc[fn] = *(const float4v*)(D + min(wc0 + 16 * fn + 4 * lkg, cols - 4));
+      static_for<kAhead>([&](auto i) __attribute__((always_inline)) { fetch(i); });
+      static_for<FM>([&](auto fm_c) __attribute__((always_inline)) {
+        constexpr int fm = decltype(fm_c)::value;
+        __builtin_amdgcn_sched_barrier(0);
+        const int r = wr0 + 16 * fm + lrow;
+        const float d = dr[fm % kAhead];
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float s = acc[fm][fn][e], y = (float)x[fm % kAhead][fn][e];
+            acc[fm][fn][e] = r == wc0 + 16 * fn + 4 * lkg + e ? g.a + g.b * d + g.c * (d * d + s)
+                                                             : g.b * y + g.c * ((d + dc[fn][e]) * y + s);
+          }
+        split_diagonal(fm_c);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (fm + kAhead < FM) fetch(std::integral_constant<int, fm + kAhead>{});
+      });
+    } else {
+      static_for<FM>([&](auto fm_c) __attribute__((always_inline)) { split_diagonal(fm_c); });
     }
     ST::template stage<false>(stage, acc, lane);
     ST::wave_fence();
@@ -363,10 +425,10 @@ hipError_t launch_any(const OrthArgs& g, OrthStep st, hipStream_t s, int device)
 }  // namespace
 
 hipError_t launch_orthogonalize(const OrthArgs& g, int steps, hipStream_t s, int device) {
-  hipLaunchKernelGGL(orth_norm, dim3((unsigned)(g.batch * kOrthParts)), dim3(256), 0, s, g);
+  hipLaunchKernelGGL(orth_norm, dim3((unsigned)g.batch * g.nparts), dim3(256), 0, s, g);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t groups = ceil_div((int64_t)g.mp * g.np / 8, 256);
+  const int64_t groups = ceil_div((int64_t)g.mp * g.np / 8, 512);
   hipLaunchKernelGGL(orth_start, dim3((unsigned)(groups * g.batch)), dim3(256), 0, s, g);
   e = hipGetLastError();
   for (int i = 0; i < steps && e == hipSuccess; ++i) {

@@ -23,8 +23,10 @@ int check_sizes(int64_t batch, int64_t R, int64_t C) {
   if (batch == 0 || R == 0 || C == 0) return TGEMM_OK;
   const int64_t m = round_up(R < C ? R : C, tgemm::kOrthPad), n = round_up(R < C ? C : R, tgemm::kOrthPad);
   if (m > kMaxM || n > TGEMM_FAST_MAX_LD) return TGEMM_EINVAL_DIM;
-  const int64_t grid = batch * (m * n / (8 * 256) + tgemm::kOrthParts);
-  return grid >= ((int64_t)1 << 31) || batch >= ((int64_t)1 << 24) ? TGEMM_EINVAL_DIM : TGEMM_OK;
+  // chunks of eight values of a matrix are numbered in 32 bits, workgroups of a launch in 31
+  const int64_t grid = batch * (m * n / (8 * 512) + 1 + tgemm::kOrthParts);
+  return m * n / 8 >= ((int64_t)1 << 31) || batch >= ((int64_t)1 << 24) || grid >= ((int64_t)1 << 31) ? TGEMM_EINVAL_DIM
+                                                                                                   : TGEMM_OK;
 }
 
 // Places the workspace's arrays (each on a 256-byte boundary) from base on; returns its bytes.
@@ -56,6 +58,10 @@ OrthArgs sized(int64_t batch, int64_t R, int64_t C) {
   g.tall = R > C;
   g.mp = (int)round_up(R < C ? R : C, tgemm::kOrthPad);
   g.np = (int)round_up(R < C ? C : R, tgemm::kOrthPad);
+  // about 4096 values per workgroup of the norm, four workgroups per compute unit over the batch
+  const int64_t want = tgemm::ceil_div(R * C, 4096), most = tgemm::ceil_div(1024, batch);
+  const int64_t parts = want < most ? want : most;
+  g.nparts = (int)(parts < 1 ? 1 : parts > tgemm::kOrthParts ? tgemm::kOrthParts : parts);
   return g;
 }
 
