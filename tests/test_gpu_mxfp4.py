@@ -428,3 +428,11 @@ def test_strides_past_32_bits(gpu):
     assert np.array_equal(q.cpu().numpy(), mx.quant(a)[0]) and np.array_equal(qt.cpu().numpy(), mx.quant(a.T.copy())[0])
     out = tg.mxfp4_dequant(q, s, K, out=ad)
     assert np.array_equal(out.cpu().numpy(), mx.to_half(mx.values(*mx.quant(a))))
+
+
+def test_no_second_derivative(gpu):
+    x = gpu.ones((4, 64), dtype=gpu.float16, device="cuda", requires_grad=True)
+    w = gpu.ones((8, 64), dtype=gpu.float16, device="cuda", requires_grad=True)
+    for y in (tg.Mxfp4LinearFunction.apply(x, w), tg.Mxfp4WeightFunction.apply(x, *tg.mxfp4_quant(w.detach()))):
+        with pytest.raises(RuntimeError, match="second derivative"):
+            gpu.autograd.grad(y.sum(), x, create_graph=True)

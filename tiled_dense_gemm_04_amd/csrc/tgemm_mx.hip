@@ -511,18 +511,22 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f16_mxfp4_pp(MxGemmArgs g) 
 
 // ------------------------------------------------------------------------------------
 // Few rows (M <= 64: single tokens and small batches): bound by reading the weight once. A
-// workgroup owns 16 rows of the weight and splits K over its waves in runs of 512 (16 blocks:
+// workgroup owns 16 rows of the weight and splits K over its W waves in runs of 512 (16 blocks:
 // one 16-byte load of scales per row, four loads of codes), so all of a wave's loads of a run
-// are in flight at once and nothing passes through LDS but the waves' partial sums, added in
-// wave order. Lane l of the weight's fragment holds block l / 16 (of four) of row l % 16, 32
-// codes. The binary16 product uses them in four MFMAs of 8 k per lane: step j takes k 32 (l /
-// 16) + 8 j .. + 7 on both sides (any order of k will do that both operands share), which is
-// one 16-byte load of A.
-constexpr int kSkinnyWaves = 8;
-
-template <int MT, bool F16A>
-__global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_mxfp4_skinny(MxGemmArgs g) {
-  __shared__ __attribute__((aligned(16))) float4v part[kSkinnyWaves][MT][64];
+// are in flight at once; the waves' partial sums are added in wave order. Lane l of the weight's
+// fragment holds block l / 16 (of four) of row l % 16, 32 codes.
+// Codes of A come the same way. Binary16 A meets a block's codes in four MFMAs of 8 k per lane,
+// step j taking k 32 (l / 16) + 8 j .. + 7 on both sides (any order of k will do that both
+// operands share). Loaded straight into that layout, every lane would touch a 64-byte segment
+// of its own for 16 bytes of it (13 us for 37 x 3000 x 4096, against 9); so the rows of A are
+// loaded 256 contiguous bytes each, four rows per load, and pass through a part of LDS that
+// belongs to the wave (no barrier; chunk c of row r at place c ^ r, free of bank conflicts).
+template <int MT, int W, bool F16A>
+__global__ __launch_bounds__(64 * W) void gemm_mxfp4_skinny(MxGemmArgs g) {
+  constexpr int A_BYTES = F16A ? MT * 16 * 256 : 0;              // per wave: 16 MT rows of 128 k
+  constexpr int P_BYTES = W * MT * 64 * 16;                      // partial sums, in the same place
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  static_assert((W * A_BYTES > P_BYTES ? W * A_BYTES : P_BYTES) <= 128 * 1024, "LDS");
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lrow = lane & 15, lblk = lane >> 4;
@@ -531,11 +535,12 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_mxfp4_skinny(MxGemmArg
   const uint8_t* const brow = g.B + (int64_t)n * g.ldb + lblk * kMxBlockBytes;
   const uint8_t* const srow = g.SB + (int64_t)n * g.ldsb;
   const int runs = (g.KB + 15) / 16;
+  char* const a_lds = smem + wave * A_BYTES;
   float4v acc[MT];
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
 
-  for (int r = wave; r < runs; r += kSkinnyWaves) {
+  for (int r = wave; r < runs; r += W) {
     const int kb0 = r * 16;
     uint4v w[4];
     const uint4v sv = load_any<uint4v>(srow + kb0);
@@ -544,45 +549,76 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_mxfp4_skinny(MxGemmArg
       w[c] = (uint4v){0, 0, 0, 0};
       if (kb0 + 4 * c + lblk < g.KB) w[c] = load_any<uint4v>(brow + (int64_t)(kb0 + 4 * c) * kMxBlockBytes);
     }
+    // blocks past KB: zero codes, and a finite scale whatever the padding holds
+    auto scale_at = [&](const uint4v& s, int c) { return kb0 + 4 * c + lblk < g.KB ? (s[c] >> (8 * lblk)) & 255u : 127u; };
+    if constexpr (F16A) {
+      // rows 4 i + lane / 16 of A, 16 bytes per lane: AHEAD chunks are loaded before they are used
+      // (all four of a run for up to 16 rows)
+      constexpr int AHEAD = MT == 1 ? 4 : MT == 2 ? 2 : 1;
+      half8 x[AHEAD][4 * MT];
+      auto fetch = [&](int c) __attribute__((always_inline)) {
+        const int k = (kb0 + 4 * c) * kMxBlock + 8 * lrow;
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int kb = kb0 + 4 * c;
-      // blocks past KB: zero codes, and a finite scale whatever the padding holds
-      const uint32_t sb = kb + lblk < g.KB ? (sv[c] >> (8 * lblk)) & 255u : 127u;
+        for (int i = 0; i < 4 * MT; ++i) {
+          x[c % AHEAD][i] = (half8){0, 0, 0, 0, 0, 0, 0, 0};
+          const int m = 4 * i + lblk;
+          if (m < g.M && k < g.K) x[c % AHEAD][i] = *(const half8*)((const _Float16*)g.A + (int64_t)m * g.lda + k);
+        }
+      };
+#pragma unroll
+      for (int c = 0; c < AHEAD; ++c) fetch(c);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+#pragma unroll
+        for (int i = 0; i < 4 * MT; ++i) {
+          const int m = 4 * i + lblk;
+          *(TG_LDS half8*)(a_lds + m * 256 + ((lrow ^ (m & 15)) << 4)) = x[c % AHEAD][i];
+        }
+        StagedTile<16, 64>::wave_fence();
+        if (c + AHEAD < 4) fetch(c + AHEAD);
+        const uint32_t sb = scale_at(sv, c);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const half8 b = decode8(w[c][j], sb);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            const half8 a = *(const TG_LDS half8*)(a_lds + (16 * i + lrow) * 256 + (((4 * lblk + j) ^ lrow) << 4));
+            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(b, a, acc[i], 0, 0, 0);
+          }
+        }
+        StagedTile<16, 64>::wave_fence();
+      }
+    } else {
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        const int m = 16 * i + lrow;
-        if constexpr (F16A) {
-          const _Float16* const arow = (const _Float16*)g.A + (int64_t)m * g.lda;
+        const int m = min(16 * i + lrow, g.M - 1);  // rows past M read the last one
+        const uint8_t* const arow = (const uint8_t*)g.A + (int64_t)m * g.lda + (int64_t)(kb0 + lblk) * kMxBlockBytes;
+        const uint4v sa = load_any<uint4v>(g.SA + (int64_t)m * g.ldsa + kb0);
+        uint4v a[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int k = (kb + lblk) * kMxBlock + 8 * j;
-            half8 a = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (m < g.M && k < g.K) a = *(const half8*)(arow + k);
-            acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(decode8(w[c][j], sb), a, acc[i], 0, 0, 0);
-          }
-        } else {
-          int4v a = {0, 0, 0, 0};
-          int sa = 127;
-          if (m < g.M && kb + lblk < g.KB) {
-            a = *(const int4v*)((const uint8_t*)g.A + (int64_t)m * g.lda + (int64_t)(kb + lblk) * kMxBlockBytes);
-            sa = g.SA[(int64_t)m * g.ldsa + kb + lblk];
-          }
-          const int4v b = __builtin_bit_cast(int4v, w[c]);
+        for (int c = 0; c < 4; ++c) {
+          a[c] = (uint4v){0, 0, 0, 0};
+          if (kb0 + 4 * c + lblk < g.KB) a[c] = load_any<uint4v>(arow + 4 * c * kMxBlockBytes);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int4v x = __builtin_bit_cast(int4v, a[c]), b = __builtin_bit_cast(int4v, w[c]);
           acc[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1), __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1),
-              acc[i], 4, 4, 0, (int)sb, 0, sa);
+              __builtin_shufflevector(b, b, 0, 1, 2, 3, -1, -1, -1, -1), __builtin_shufflevector(x, x, 0, 1, 2, 3, -1, -1, -1, -1),
+              acc[i], 4, 4, 0, (int)scale_at(sv, c), 0, (int)scale_at(sa, c));
         }
       }
     }
   }
+  __syncthreads();  // every wave is done with its rows of A
+  float4v* const part = (float4v*)smem;
 #pragma unroll
-  for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+  for (int i = 0; i < MT; ++i) *(TG_LDS float4v*)(part + (wave * MT + i) * 64 + lane) = acc[i];
   __syncthreads();
-  for (int i = wave; i < MT; i += kSkinnyWaves) {
-    float4v s = part[0][i][lane];
+  for (int i = wave; i < MT; i += W) {
+    float4v s = *(const TG_LDS float4v*)(part + i * 64 + lane);
 #pragma unroll
-    for (int w = 1; w < kSkinnyWaves; ++w) s += part[w][i][lane];
+    for (int w = 1; w < W; ++w) s += *(const TG_LDS float4v*)(part + (w * MT + i) * 64 + lane);
     const int m = 16 * i + lrow, c = n0 + 4 * lblk;
     if (m >= g.M) continue;
 #pragma unroll
@@ -695,14 +731,15 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_generic(MxGemmArgs g) {
 // Launch of a kernel with more than the default dynamic LDS: the limit is raised once per
 // kernel and device.
 template <typename K>
-hipError_t launch_big(K kern, int lds, std::atomic<uint64_t>& ready, const MxGemmArgs& g, hipStream_t s, int device) {
+hipError_t launch_big(K kern, int lds, std::atomic<uint64_t>& ready, const MxGemmArgs& g, hipStream_t s, int device,
+                      int threads = 512) {
   const uint64_t bit = 1ull << (device & 63);
   if (!(ready.load(std::memory_order_acquire) & bit)) {
     const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
     ready.fetch_or(bit, std::memory_order_acq_rel);
   }
-  hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n)), dim3(512), lds, s, g);
+  hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n)), dim3(threads), lds, s, g);
   return hipGetLastError();
 }
 
@@ -716,16 +753,27 @@ hipError_t launch_mx_pp(bool f16_a, const MxGemmArgs& g, hipStream_t s, int devi
   return launch_big(gemm_mxfp4_pp<BM, BN, KS, 2, 4, STAGES, 4>, mx_lds_bytes<BM, BN, KS, STAGES>(), ready[0], g, s, device);
 }
 
+template <int MT, int W, bool F16A>
+hipError_t launch_skinny_tile(const MxGemmArgs& g, hipStream_t s, int device) {
+  static std::atomic<uint64_t> ready{0};
+  constexpr int lds = W * MT * (F16A ? 4096 : 1024);
+  MxGemmArgs a = g;
+  a.tiles_m = 1;
+  a.tiles_n = (int)ceil_div(g.N, 16);
+  return launch_big(gemm_mxfp4_skinny<MT, W, F16A>, lds, ready, a, s, device, 64 * W);
+}
+
+// Eight waves, or sixteen for up to 16 rows where K has more than eight runs of 512 (every run
+// of a wave after its first waits for memory again; more rows need the registers).
 template <bool F16A>
-hipError_t launch_skinny(const MxGemmArgs& g, hipStream_t s) {
-  const dim3 grid((unsigned)((g.N + 15) / 16)), block(64 * kSkinnyWaves);
+hipError_t launch_skinny(const MxGemmArgs& g, hipStream_t s, int device) {
   switch ((g.M + 15) / 16) {
-    case 1: hipLaunchKernelGGL((gemm_mxfp4_skinny<1, F16A>), grid, block, 0, s, g); break;
-    case 2: hipLaunchKernelGGL((gemm_mxfp4_skinny<2, F16A>), grid, block, 0, s, g); break;
-    case 3: hipLaunchKernelGGL((gemm_mxfp4_skinny<3, F16A>), grid, block, 0, s, g); break;
-    default: hipLaunchKernelGGL((gemm_mxfp4_skinny<4, F16A>), grid, block, 0, s, g); break;
+    case 1:
+      return g.KB > 8 * 16 ? launch_skinny_tile<1, 16, F16A>(g, s, device) : launch_skinny_tile<1, 8, F16A>(g, s, device);
+    case 2: return launch_skinny_tile<2, 8, F16A>(g, s, device);
+    case 3: return launch_skinny_tile<3, 8, F16A>(g, s, device);
+    default: return launch_skinny_tile<4, 8, F16A>(g, s, device);
   }
-  return hipGetLastError();
 }
 
 }  // namespace
@@ -736,7 +784,7 @@ hipError_t launch_mxfp4(int cfg, bool f16_a, const MxGemmArgs& args, hipStream_t
   g.tiles_m = (int)ceil_div(g.M, tile);
   g.tiles_n = (int)ceil_div(g.N, tile);
   switch (cfg) {
-    case kMxSkinny: return f16_a ? launch_skinny<true>(g, s) : launch_skinny<false>(g, s);
+    case kMxSkinny: return f16_a ? launch_skinny<true>(g, s, device) : launch_skinny<false>(g, s, device);
     case kMx128: return launch_mx_pp<128, 128, 2, 4>(f16_a, g, s, device);
     case kMx256: return launch_mx_pp<256, 256, 1, 4>(f16_a, g, s, device);
     default: break;

@@ -10,7 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 
-from . import TGEMM_OK, TgemmError, _operand, lib, matmul
+from . import TGEMM_OK, TgemmError, _operand, lib, workspace_for
 
 MX_BLOCK = 32
 MX_BLOCK_BYTES = 16
@@ -223,6 +223,32 @@ def _row_major(x, name):
     return x if (cols <= 1 or step == 1) and (rows <= 1 or ld >= cols) else x.contiguous()
 
 
+def _once():
+    """A backward pass runs with gradients recorded only when its own gradient is wanted."""
+    import torch
+    if torch.is_grad_enabled():
+        raise RuntimeError("the MXFP4 functions have no second derivative (create_graph=True)")
+
+
+def _times_weight(dy, w):
+    """dy @ w (M x N by N x K, rows contiguous) through gemm_f16_ws, as ``matmul`` runs it."""
+    import torch
+    (M, N), K, device = dy.shape, w.shape[1], dy.device
+    dx = torch.empty((M, K), dtype=torch.float16, device=device)
+    L, stream = lib(), _stream(None, device)
+    need = L.tgemm_workspace_bytes(0, 0, M, K, N)
+    ws = None
+    if need:  # a captured graph gets a (zeroed) workspace of its own: its replays may overlap other calls
+        ws = (torch.zeros(need, dtype=torch.uint8, device=device) if torch.cuda.is_current_stream_capturing()
+              else workspace_for(need, device, stream))
+    rc = _call("gemm_f16_ws", (0, 0, M, K, N, dy.data_ptr(), dy.stride(0) if M > 1 else max(1, N), w.data_ptr(),
+                               max(1, K), dx.data_ptr(), max(1, K), 0, ws.data_ptr() if need else None,
+                               ws.numel() if need else 0, stream), device)
+    if rc != TGEMM_OK:
+        raise TgemmError(rc, "gemm_f16_ws")
+    return dx
+
+
 class _Packed:
     """MXFP4 matrices in one allocation (a step of a linear layer makes six of them): ``add``
     plans one and returns (rows, k, code offset, code stride, scale offset, scale stride)."""
@@ -269,7 +295,6 @@ def _packed_gemm(a, a_base, b, b_base, device):
 
 def autograd_functions():
     import torch
-    from torch.autograd.function import once_differentiable
 
     class Mxfp4LinearFunction(torch.autograd.Function):
         """y = q(x) q(w)^T for fp16 x (M, K) and w (N, K), every product of the step on MXFP4
@@ -295,8 +320,8 @@ def autograd_functions():
             return _packed_gemm(xq, rows.base, wq, rows.base, x.device)
 
         @staticmethod
-        @once_differentiable
         def backward(ctx, dy):
+            _once()
             need_x, need_w = ctx.needs_input_grad
             dy = _row_major(dy, "dy")
             tmp = _Packed(dy.device)
@@ -322,11 +347,9 @@ def autograd_functions():
             return mxfp4_gemm_f16(x, codes, scale)
 
         @staticmethod
-        @once_differentiable
         def backward(ctx, dy):
-            if not ctx.needs_input_grad[0]:
-                return None, None, None
+            _once()
             codes, scale = ctx.saved_tensors
-            return matmul(_row_major(dy, "dy"), mxfp4_dequant(codes, scale, ctx.k)), None, None
+            return _times_weight(_row_major(dy, "dy"), mxfp4_dequant(codes, scale, ctx.k)), None, None
 
     return {"Mxfp4LinearFunction": Mxfp4LinearFunction, "Mxfp4WeightFunction": Mxfp4WeightFunction}
