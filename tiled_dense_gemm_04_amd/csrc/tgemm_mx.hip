@@ -249,49 +249,38 @@ __global__ __launch_bounds__(256) void dequant_mxfp4_rows(MxDequantArgs q) {
 }
 
 // ------------------------------------------------------------------------------------
-// Product of two MXFP4 matrices, ping-pong kernel. One v_mfma_scale_f32_16x16x128_f8f6f4
-// multiplies 16 x 128 by 128 x 16 codes and applies both operands' block scales itself: lane
-// l's 16 bytes of an operand are one whole block (row l % 16, block l / 16 of the four) and
-// its scale byte sits in a register beside it, so nothing is folded outside the MFMA.
-// A k-tile of 128 codes is 64 bytes a row, the bytes of a binary16 k-tile of 32: operand
-// copies, range-checked edges, swizzle and the four-slot ring are the binary16 ping-pong's
-// (PpOperand on code rows seen as halves). 128 x 128 tiles take k-tiles of 256 codes (KS = 2):
-// their few MFMAs per k-tile leave the barriers and latencies between them in the open.
-// Scales come in groups of 16 blocks, 16 bytes a row and one 16-byte copy per row, with the
-// first k-tile of the group. In the last group bytes past KB are whatever the padding holds: a
-// lane whose block lies past KB takes the last block's scale instead, and its codes are zeros
-// (out-of-range copies).
+// Products of two MXFP4 matrices. One v_mfma_scale_f32_16x16x128_f8f6f4 multiplies 16 x 128 by
+// 128 x 16 codes and applies both operands' block scales itself: lane l's 16 bytes of an operand
+// are one whole block (row l % 16) and its scale byte sits in a register beside it, so nothing
+// is folded outside the MFMA. k-tiles are 256 codes, 128 bytes a row: operand copies,
+// range-checked edges and swizzle are the binary16 kernels' (PpOperand on code rows seen as
+// halves), and whole 128-byte lines move fastest (copies alone reach 118 GB/s per compute unit
+// in long runs, 70 in 64-byte pieces). Scales come in groups of 16 blocks (two k-tiles), 16 bytes
+// a row and one 16-byte copy per row. In the last group bytes past KB are whatever the padding
+// holds; they meet zero codes (out-of-range copies) and are replaced or cleared.
 // Requirements (host): A, B, SA, SB 16-byte aligned, their row strides multiples of 16.
-// Slots of the scale ring. Group 1 copies scale group s with its first tile t = G s (G = 4 / KS
-// k-tiles per group) in iteration t - STAGES + 1, when tiles up to that one may still be read: the
-// slot's former group s - slots must end before it, G (s - slots) + G - 1 < G s - STAGES + 1.
-constexpr int mx_scale_slots(int ks, int stages) { return (4 / ks) * (2 - 1) > stages - 2 ? 2 : 4; }
-static_assert(4 * (4 - 1) > 4 - 2 && 2 * (4 - 1) > 4 - 2, "four slots are enough for both k-tiles");
-
-template <int BM, int BN, int KS, int STAGES>
-constexpr int mx_lds_bytes() {
-  return STAGES * (BM + BN) * 64 * KS + mx_scale_slots(KS, STAGES) * (BM + BN) * 16;
-}
-
-template <int BM, int BN, int KS, int WM, int WN, int STAGES, int PANEL>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_mxfp4_pp(MxGemmArgs g) {
-  constexpr int NW = WM * WN, WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
-  using OpA = PpOperand<BM, 32 * KS, 16, true, NW>;
-  using OpB = PpOperand<BN, 32 * KS, 16, true, NW>;
-  constexpr int A_BYTES = OpA::BYTES, B_BYTES = OpB::BYTES, PT = OpA::LD + OpB::LD;
-  constexpr int TB = 4 * KS, GROUP = 16 / TB;       // blocks per row of a k-tile, k-tiles per scale group
-  constexpr int SLOTS = mx_scale_slots(KS, STAGES);
-  constexpr int SG_BYTES = (BM + BN) * 16;  // one scale group: A's rows, then B's
-  constexpr int SC_A = BM / 64, SC_B = BN / 64;
-  static_assert(NW == 8 && OpA::REM == 0 && OpB::REM == 0 && (SC_A + SC_B == 4 || SC_A + SC_B == 8) && STAGES <= 4, "copies");
+//
+// 128 x 128 tiles, for small output grids: the two-group ping-pong (tgemm_pingpong.h) over four
+// slots. Each group takes half of every k-tile on wave tiles of 64 x 64 (a third fewer LDS reads
+// than 64 x 32 tiles over the whole of it), and the groups' sums are joined at the end.
+template <int PANEL>
+__global__ __launch_bounds__(512) void gemm_mxfp4_pp128(MxGemmArgs g) {
+  constexpr int BM = 128, BN = 128, NW = 8, STAGES = 4, WT = 64, FM = WT / 16, FN = WT / 16;
+  using Op = PpOperand<128, 64, 16, true, NW>;  // both operands
+  constexpr int SLOT = Op::BYTES, LD = Op::LD;
+  constexpr int TB = 8, GROUP = 2;  // blocks per row of a k-tile, k-tiles per scale group
+  // Group 1 copies scale group s with its first k-tile 2 s in iteration 2 s - STAGES + 1, when
+  // that k-tile's group s - 2 may still be read: three slots would do, four make it a mask.
+  constexpr int SLOTS = 4, SG_BYTES = (BM + BN) * 16;
+  static_assert(Op::REM == 0 && STAGES == 4, "copies");
 
   extern __shared__ __attribute__((aligned(16))) char smem[];
   char* const a_lds = smem;
-  char* const b_lds = smem + STAGES * A_BYTES;
-  char* const s_lds = b_lds + STAGES * B_BYTES;
-
+  char* const b_lds = smem + STAGES * SLOT;
+  char* const s_lds = b_lds + STAGES * SLOT;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int grp = wave >> 2;
   int64_t tm, tn;
   tile_of(blockIdx.x, g.tiles_m, g.tiles_n, PANEL, 1, &tm, &tn);
   const int row0 = (int)tm * BM, col0 = (int)tn * BN;
@@ -299,73 +288,58 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_mxfp4_pp(MxGemmArgs g) {
   const int nk = (g.KB + TB - 1) / TB;
   const int kin_last = (g.KB - (nk - 1) * TB) * (kMxBlockBytes / 2);  // in halves
 
-  OpA opa;
-  OpB opb;
+  Op opa, opb;
   opa.init_copies((const _Float16*)g.A, g.lda / 2, row0, mvalid, kin_last, wave, lane);
   opb.init_copies((const _Float16*)g.B, g.ldb / 2, col0, nvalid, kin_last, wave, lane);
   const uint32_t a_lds0 = lds_addr(a_lds) + wave * 1024, b_lds0 = lds_addr(b_lds) + wave * 1024;
-
-  // The scale copies (64 rows of A or B each) are group 1's: the group that runs no tile ahead
-  // has the registers for them. Its wave w takes copies w - 4 and, if there are more than four,
-  // w.
-  auto copy_scales = [&](int sg, int part) __attribute__((always_inline)) {
-    const bool is_a = part < SC_A;
-    const int r = (is_a ? part : part - SC_A) * 64;
-    const int64_t ld = is_a ? g.ldsa : g.ldsb;
-    const uint8_t* const base = is_a ? g.SA + (int64_t)(row0 + r) * ld : g.SB + (int64_t)(col0 + r) * ld;
-    const int left = (is_a ? mvalid : nvalid) - r;
-    dma_to_lds(make_rsrc(base + (int64_t)sg * 16, kMaxRange), lds_addr(s_lds) + (sg % SLOTS) * SG_BYTES + part * 1024,
-               lane < left ? (uint32_t)lane * (uint32_t)ld : kOob);
-  };
+  // The scale copies (64 rows of A or B each) are group 1's, one per wave.
+  const int part = wave & 3;
+  const bool s_is_a = part < 2;
+  const int s_row = (part & 1) * 64;
+  const int64_t s_ld = s_is_a ? g.ldsa : g.ldsb;
+  const uint8_t* const s_base = s_is_a ? g.SA + (int64_t)(row0 + s_row) * s_ld : g.SB + (int64_t)(col0 + s_row) * s_ld;
+  const uint32_t s_off = lane < (s_is_a ? mvalid : nvalid) - s_row ? (uint32_t)lane * (uint32_t)s_ld : kOob;
+  const uint32_t s_dst = lds_addr(s_lds) + part * 1024;
   auto copy_tile = [&](int t, auto group) __attribute__((always_inline)) {
-    if (decltype(group)::value == 1 && t % GROUP == 0 && t < nk) {
-      copy_scales(t / GROUP, wave - 4);
-      if (SC_A + SC_B > 4) copy_scales(t / GROUP, wave);
-    }
+    if (decltype(group)::value == 1 && t % GROUP == 0 && t < nk)
+      dma_to_lds(make_rsrc(s_base + (int64_t)(t / GROUP) * 16, kMaxRange), s_dst + (t / GROUP % SLOTS) * SG_BYTES, s_off);
     const int4v ra = opa.rsrc(t, nk, nk), rb = opb.rsrc(t, nk, nk);
     const int slot = t % STAGES;
     const bool last = t == nk - 1;
 #pragma unroll
-    for (int j = 0; j < OpA::LD; ++j)
-      dma_to_lds(ra, a_lds0 + slot * A_BYTES + j * NW * 1024, last ? opa.off_last[j] : opa.off[j]);
+    for (int j = 0; j < LD; ++j) dma_to_lds(ra, a_lds0 + slot * SLOT + j * NW * 1024, last ? opa.off_last[j] : opa.off[j]);
 #pragma unroll
-    for (int j = 0; j < OpB::LD; ++j)
-      dma_to_lds(rb, b_lds0 + slot * B_BYTES + j * NW * 1024, last ? opb.off_last[j] : opb.off[j]);
+    for (int j = 0; j < LD; ++j) dma_to_lds(rb, b_lds0 + slot * SLOT + j * NW * 1024, last ? opb.off_last[j] : opb.off[j]);
   };
 
-  const int wm = wave / WN, wn = wave % WN, lrow = lane & 15, lblk = lane >> 4;
-  opa.init_frags(wm * WTM, lane);
-  opb.init_frags(wn * WTN, lane);
-  const char* const sa_lds = s_lds + (wm * WTM + lrow) * 16;
-  const char* const sb_lds = s_lds + (BM + wn * WTN + lrow) * 16;
-
-  half8 fa[KS][FM], fb[KS][FN];
-  int sa[KS][FM], sb[KS][FN];
+  const int wm = part >> 1, wn = part & 1, lrow = lane & 15, lblk = lane >> 4;
+  opa.init_frags(wm * WT, lane);
+  opb.init_frags(wn * WT, lane);
+  const char* const sa_lds = s_lds + (wm * WT + lrow) * 16;
+  const char* const sb_lds = s_lds + (BM + wn * WT + lrow) * 16;
+  half8 fa[FM], fb[FN];
+  int sa[FM], sb[FN];
   auto read_tile = [&](int t) __attribute__((always_inline)) {
-    const char* const As = a_lds + (t % STAGES) * A_BYTES;
-    const char* const Bs = b_lds + (t % STAGES) * B_BYTES;
-    const int group = (t / GROUP % SLOTS) * SG_BYTES + TB * (t % GROUP);
+    const char* const As = a_lds + (t % STAGES) * SLOT;
+    const char* const Bs = b_lds + (t % STAGES) * SLOT;
+    // (a lane whose block lies past KB takes the last block's scale)
+    const int off = (t / GROUP % SLOTS) * SG_BYTES + TB * (t % GROUP) + max(min(4 * grp + lblk, g.KB - 1 - TB * t), 0);
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const int off = group + max(min(4 * ks + lblk, g.KB - 1 - TB * t), 0);
+    for (int fn = 0; fn < FN; ++fn) {
+      fb[fn] = opb.frag(Bs, fn, grp);
+      sb[fn] = *(const TG_LDS uint8_t*)(sb_lds + off + fn * 256);
+    }
 #pragma unroll
-      for (int fn = 0; fn < FN; ++fn) {
-        fb[ks][fn] = opb.frag(Bs, fn, ks);
-        sb[ks][fn] = *(const TG_LDS uint8_t*)(sb_lds + off + fn * 256);
-      }
-#pragma unroll
-      for (int fm = 0; fm < FM; ++fm) {
-        fa[ks][fm] = opa.frag(As, fm, ks);
-        sa[ks][fm] = *(const TG_LDS uint8_t*)(sa_lds + off + fm * 256);
-      }
+    for (int fm = 0; fm < FM; ++fm) {
+      fa[fm] = opa.frag(As, fm, grp);
+      sa[fm] = *(const TG_LDS uint8_t*)(sa_lds + off + fm * 256);
     }
   };
-
-  float4v acc[FM][FN];
+  float4v sum[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < FN; ++j) sum[i][j] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
   auto wide = [](const half8& h) {
     const int4v v = __builtin_bit_cast(int4v, h);
     return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
@@ -373,18 +347,188 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_mxfp4_pp(MxGemmArgs g) {
   // Operands go in as (B fragment, A fragment), so a lane holds four consecutive columns.
   auto mma_tile = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
+    for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
-      for (int fm = 0; fm < FM; ++fm)
-#pragma unroll
-        for (int fn = 0; fn < FN; ++fn)
-          acc[fm][fn] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(fb[ks][fn]), wide(fa[ks][fm]), acc[fm][fn], 4, 4, 0,
-                                                                        sb[ks][fn], 0, sa[ks][fm]);
+      for (int fn = 0; fn < FN; ++fn)
+        sum[fm][fn] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(fb[fn]), wide(fa[fm]), sum[fm][fn], 4, 4, 0, sb[fn], 0, sa[fm]);
   };
-  pingpong_schedule<STAGES, PT, PT, false>(wave / 4, nk, copy_tile, read_tile, mma_tile);
+  pingpong_schedule<STAGES, 2 * LD, 2 * LD, false>(grp, nk, copy_tile, read_tile, mma_tile);
+
+  __syncthreads();
+  float4v acc[FM / 2][FN];
+  join_k_groups<FM, FN>(smem, sum, acc, wave, lane);
+  using ST = StagedTile<WT / 2, WT>;
+  char* const stage = smem + wave * ST::BYTES;
+  if (g.relu != 0)
+    ST::template stage<true>(stage, acc, lane);
+  else
+    ST::template stage<false>(stage, acc, lane);
+  ST::wave_fence();
+  const int r0 = wm * WT + grp * (WT / 2), c0 = wn * WT;
+  store_staged<ST, WT / 2>(stage, lane, g.C + (int64_t)(row0 + r0) * g.ldc + col0 + c0, g.ldc, mvalid - r0, nvalid - c0, g.vec_c);
+}
+
+constexpr int kMx128Lds = 4 * 2 * 128 * 128 + 4 * 256 * 16;
+
+// ------------------------------------------------------------------------------------
+// 256 x 256 tiles: two slots of k-tiles. A wave reads all fragments of a k-tile (96 registers)
+// and runs its 64 MFMAs from them, so a slot is free again as soon as both groups have read it
+// (four slots of 128 codes and the binary16 kernel's schedule: 8192^3 in 285 us against 260).
+// Interval kt (between barriers kt - 1 and kt; tile t in slot t % 2):
+//   group 0: reads tile kt; its copies of tile kt + 1; MFMAs of tile kt; waits for the copies;
+//   group 1: its copies of tile kt + 1; MFMAs of tile kt - 1; reads tile kt; waits likewise.
+// Tile kt + 1 goes to the slot of tile kt - 1, which both groups read before barrier kt - 1, and
+// is complete for everyone after barrier kt. Group 0, whose reads come first, makes more of the
+// copies (all of A, B but for the last CB per wave), so that neither group's interval is longer.
+// Scales: 16 blocks (two k-tiles) a row per 16-byte copy, three slots; tile t brings A's
+// (t even) or B's (t odd) next group t / 2 + 1, whose slot held group t / 2 - 2. A lane's MFMA
+// ks takes block 2 (l / 16) + ks of the k-tile on both sides, so its two scales of a row are
+// neighbouring bytes: one 2-byte read, the MFMA picks the byte. Blocks past KB: zero codes, and
+// the scale bytes (whatever the padding holds) are cleared.
+template <int PANEL, int CB>
+__global__ __launch_bounds__(512) void gemm_mxfp4_pp256(MxGemmArgs g) {
+  constexpr int BM = 256, BN = 256, WM = 2, WN = 4, NC = 4, WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
+  using Op = PpOperand<256, 64, 16, true, NC>;  // both operands; the copies of four waves
+  constexpr int SLOT = Op::BYTES, LD = Op::LD, TB = 8, SG_BYTES = (BM + BN) * 16;
+  static_assert(LD == 8 && CB >= 0 && CB <= LD && Op::CPR == 8, "copies");
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  char* const a_lds = smem;
+  char* const b_lds = smem + 2 * SLOT;
+  char* const s_lds = b_lds + 2 * SLOT;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int grp = wave / NC, cw = wave % NC;
+  int64_t tm, tn;
+  tile_of(blockIdx.x, g.tiles_m, g.tiles_n, PANEL, 1, &tm, &tn);
+  const int row0 = (int)tm * BM, col0 = (int)tn * BN;
+  const int mvalid = min(BM, g.M - row0), nvalid = min(BN, g.N - col0);
+  const int nk = (g.KB + TB - 1) / TB;
+  const int kin_last = (g.KB - (nk - 1) * TB) * (kMxBlockBytes / 2);  // in halves
+
+  Op opa, opb;
+  opa.init_copies((const _Float16*)g.A, g.lda / 2, row0, mvalid, kin_last, cw, lane);
+  opb.init_copies((const _Float16*)g.B, g.ldb / 2, col0, nvalid, kin_last, cw, lane);
+  // Copy j of a thread lies RSTEP rows after copy 0, a multiple of the swizzle period, so its
+  // offset is copy 0's plus j RSTEP rows; an out-of-range offset stays out of range and below
+  // 2^32 (row strides are at most 2^23 bytes). Two registers per operand instead of 2 LD.
+  constexpr int RSTEP = NC * 64 / Op::CPR;
+  static_assert(RSTEP % 16 == 0 && (LD - 1) * RSTEP < 256, "copy rows");
+  const uint32_t a_rstep = (uint32_t)RSTEP * (uint32_t)g.lda, b_rstep = (uint32_t)RSTEP * (uint32_t)g.ldb;
+  const uint32_t a_off = opa.off[0], a_off_last = opa.off_last[0], b_off = opb.off[0], b_off_last = opb.off_last[0];
+  const uint32_t a_dst = lds_addr(a_lds) + cw * 1024, b_dst = lds_addr(b_lds) + cw * 1024;
+  auto copy_a = [&](int t) __attribute__((always_inline)) {
+    const int4v r = opa.rsrc(t, nk, nk);
+    const uint32_t o = t == nk - 1 ? a_off_last : a_off, d = a_dst + (t & 1) * SLOT;
+#pragma unroll
+    for (int j = 0; j < LD; ++j) dma_to_lds(r, d + j * NC * 1024, o + j * a_rstep);
+  };
+  auto copy_b = [&](int t, int lo, int hi) __attribute__((always_inline)) {
+    const int4v r = opb.rsrc(t, nk, nk);
+    const uint32_t o = t == nk - 1 ? b_off_last : b_off, d = b_dst + (t & 1) * SLOT;
+#pragma unroll
+    for (int j = lo; j < hi; ++j) dma_to_lds(r, d + j * NC * 1024, o + j * b_rstep);
+  };
+  // Scale group sg of A's (is_a) or B's rows 64 cw .. + 63.
+  auto copy_scales = [&](int sg, bool is_a) __attribute__((always_inline)) {
+    const int64_t ld = is_a ? g.ldsa : g.ldsb;
+    const uint8_t* const base = is_a ? g.SA + (int64_t)(row0 + cw * 64) * ld : g.SB + (int64_t)(col0 + cw * 64) * ld;
+    const int left = (is_a ? mvalid : nvalid) - cw * 64;
+    dma_to_lds(make_rsrc(base + (int64_t)sg * 16, 2 * sg < nk ? kMaxRange : 0u),
+               lds_addr(s_lds) + (sg % 3) * SG_BYTES + (is_a ? 0 : BM * 16) + cw * 1024,
+               lane < left ? (uint32_t)lane * (uint32_t)ld : kOob);
+  };
+
+  const int wm = wave / WN, wn = wave % WN, lrow = lane & 15, lblk = lane >> 4;
+  // Fragment f, substep ks: chunk 2 lblk + ks of row 16 f + lrow.
+  const int sw = Op::swz(lrow);
+  const char* const a_rd[2] = {a_lds + (wm * WTM + lrow) * 128 + (((2 * lblk) ^ sw) << 4),
+                               a_lds + (wm * WTM + lrow) * 128 + (((2 * lblk + 1) ^ sw) << 4)};
+  const char* const b_rd[2] = {b_lds + (wn * WTN + lrow) * 128 + (((2 * lblk) ^ sw) << 4),
+                               b_lds + (wn * WTN + lrow) * 128 + (((2 * lblk + 1) ^ sw) << 4)};
+  const char* const sa_rd = s_lds + (wm * WTM + lrow) * 16 + 2 * lblk;
+  const char* const sb_rd = s_lds + (BM + wn * WTN + lrow) * 16 + 2 * lblk;
+  int4v fa[2][FM], fb[2][FN];
+  uint32_t sa[FM], sb[FN];
+  auto read_tile = [&](int t) __attribute__((always_inline)) {
+    const int slot = (t & 1) * SLOT, so = (t / 2 % 3) * SG_BYTES + (t & 1) * 8;
+    const int left = g.KB - TB * t - 2 * lblk;  // blocks of this lane inside the matrix
+    const uint32_t mask = left >= 2 ? 0xFFFFu : left == 1 ? 0xFFu : 0u;
+#pragma unroll
+    for (int fn = 0; fn < FN; ++fn) sb[fn] = *(const TG_LDS uint16_t*)(sb_rd + so + fn * 256) & mask;
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm) sa[fm] = *(const TG_LDS uint16_t*)(sa_rd + so + fm * 256) & mask;
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn) fb[ks][fn] = *(const TG_LDS int4v*)(b_rd[ks] + slot + fn * 2048);
+#pragma unroll
+      for (int fm = 0; fm < FM; ++fm) fa[ks][fm] = *(const TG_LDS int4v*)(a_rd[ks] + slot + fm * 2048);
+    }
+  };
+  float4v acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
+  auto wide = [](const int4v& v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1); };
+  auto mma_tile = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn)
+        acc[fm][fn] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(fb[0][fn]), wide(fa[0][fm]), acc[fm][fn], 4, 4, 0, sb[fn], 0, sa[fm]);
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn)
+        acc[fm][fn] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(fb[1][fn]), wide(fa[1][fm]), acc[fm][fn], 4, 4, 1, sb[fn], 1, sa[fm]);
+  };
+
+  if (grp == 0) {
+    copy_scales(0, true);
+    copy_scales(0, false);
+    copy_scales(1, true);
+    copy_a(0);
+    copy_b(0, 0, LD - CB);
+  } else {
+    copy_b(0, LD - CB, LD);
+  }
+  wait_vmcnt<0>();
+  lds_barrier();
+  // sched_barrier(0) pins every phase: MFMAs only touch registers, so s_barrier does not order
+  // them.
+  if (grp == 0) {
+    for (int kt = 0; kt < nk; ++kt) {
+      __builtin_amdgcn_sched_barrier(0);
+      read_tile(kt);
+      copy_a(kt + 1);
+      copy_b(kt + 1, 0, LD - CB);
+      copy_scales((kt + 1) / 2 + 1, ((kt + 1) & 1) == 0);
+      __builtin_amdgcn_sched_barrier(0);
+      mma_tile();
+      __builtin_amdgcn_sched_barrier(0);
+      wait_vmcnt<0>();
+      lds_barrier();  // (barrier kt)
+    }
+  } else {
+    copy_b(1, LD - CB, LD);  // in interval 0
+    for (int kt = 0; kt < nk; ++kt) {
+      __builtin_amdgcn_sched_barrier(0);
+      read_tile(kt);
+      __builtin_amdgcn_sched_barrier(0);
+      wait_vmcnt<0>();
+      lds_barrier();  // (barrier kt)
+      __builtin_amdgcn_sched_barrier(0);
+      copy_b(kt + 2, LD - CB, LD);  // in interval kt + 1
+      __builtin_amdgcn_sched_barrier(0);
+      mma_tile();
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  wait_vmcnt<0>();
 
   using ST = StagedTile<WTM, WTN>;
-  static_assert(NW * ST::BYTES <= mx_lds_bytes<BM, BN, KS, STAGES>(), "staged tile fits in the ring");
+  static_assert(8 * ST::BYTES <= 4 * SLOT, "staged tile fits in the ring");
   __syncthreads();
   char* const stage = smem + wave * ST::BYTES;
   if (g.relu != 0)
@@ -395,6 +539,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_mxfp4_pp(MxGemmArgs g) {
   store_staged<ST, WTM>(stage, lane, g.C + (int64_t)(row0 + wm * WTM) * g.ldc + col0 + wn * WTN, g.ldc,
                         mvalid - wm * WTM, nvalid - wn * WTN, g.vec_c);
 }
+
+constexpr int kMx256Lds = 4 * 256 * 128 + 3 * 512 * 16;
 
 // ------------------------------------------------------------------------------------
 // Product of binary16 A with an MXFP4 weight, ping-pong kernel on k-tiles of 32 (one block):
@@ -743,14 +889,19 @@ hipError_t launch_big(K kern, int lds, std::atomic<uint64_t>& ready, const MxGem
   return hipGetLastError();
 }
 
-template <int BM, int BN, int KS, int STAGES>
-hipError_t launch_mx_pp(bool f16_a, const MxGemmArgs& g, hipStream_t s, int device) {
-  static std::atomic<uint64_t> ready[2];
-  if (f16_a) {
-    constexpr int ring = wq_lds_bytes<BM, BN, 2, 4, STAGES>(), st = 8 * StagedTile<BM / 2, BN / 4>::BYTES;
-    return launch_big(gemm_f16_mxfp4_pp<BM, BN, 2, 4, STAGES, 4>, ring > st ? ring : st, ready[1], g, s, device);
-  }
-  return launch_big(gemm_mxfp4_pp<BM, BN, KS, 2, 4, STAGES, 4>, mx_lds_bytes<BM, BN, KS, STAGES>(), ready[0], g, s, device);
+template <int BM>
+hipError_t launch_wq_pp(const MxGemmArgs& g, hipStream_t s, int device) {
+  static std::atomic<uint64_t> ready{0};
+  constexpr int ring = wq_lds_bytes<BM, BM, 2, 4, 4>(), st = 8 * StagedTile<BM / 2, BM / 4>::BYTES;
+  return launch_big(gemm_f16_mxfp4_pp<BM, BM, 2, 4, 4, 4>, ring > st ? ring : st, ready, g, s, device);
+}
+hipError_t launch_mx_128(const MxGemmArgs& g, hipStream_t s, int device) {
+  static std::atomic<uint64_t> ready{0};
+  return launch_big(gemm_mxfp4_pp128<4>, kMx128Lds, ready, g, s, device);
+}
+hipError_t launch_mx_256(const MxGemmArgs& g, hipStream_t s, int device) {
+  static std::atomic<uint64_t> ready{0};
+  return launch_big(gemm_mxfp4_pp256<4, 8>, kMx256Lds, ready, g, s, device);
 }
 
 template <int MT, int W, bool F16A>
@@ -785,8 +936,8 @@ hipError_t launch_mxfp4(int cfg, bool f16_a, const MxGemmArgs& args, hipStream_t
   g.tiles_n = (int)ceil_div(g.N, tile);
   switch (cfg) {
     case kMxSkinny: return f16_a ? launch_skinny<true>(g, s, device) : launch_skinny<false>(g, s, device);
-    case kMx128: return launch_mx_pp<128, 128, 2, 4>(f16_a, g, s, device);
-    case kMx256: return launch_mx_pp<256, 256, 1, 4>(f16_a, g, s, device);
+    case kMx128: return f16_a ? launch_wq_pp<128>(g, s, device) : launch_mx_128(g, s, device);
+    case kMx256: return f16_a ? launch_wq_pp<256>(g, s, device) : launch_mx_256(g, s, device);
     default: break;
   }
   const dim3 grid((unsigned)((int64_t)g.tiles_m * g.tiles_n));

@@ -130,23 +130,33 @@ struct OrthStep {
   int in, last;  // which of the two iterate buffers is read; the final step writes the result
 };
 
-// k-tiles of 32, or of 64 for the smaller tiles, whose few MFMAs per k-tile leave the barriers
-// and latencies between them in the open.
 template <int BM>
-constexpr int kOrthKs = BM == 128 ? 2 : 1;
+constexpr int kOrthKg = BM == 128 ? 2 : 1;
 
 template <int BM>
 constexpr int orth_lds_bytes() {
   // the operand ring, or the staged tiles of the epilogue (per wave, transposed with a 16-byte
   // pad per column), whichever is larger
-  constexpr int ring = 4 * 2 * BM * 64 * kOrthKs<BM>, st = 8 * (BM / 4) * (BM / 2 * 2 + 16);
+  constexpr int ring = 4 * 2 * BM * 64 * kOrthKg<BM>, st = 8 * (BM * kOrthKg<BM> / 4) * (BM / kOrthKg<BM> + 16);
   return ring > st ? ring : st;
+}
+
+template <bool JOINED, typename A, typename B>
+__device__ __forceinline__ auto& pick_sums(A& own, B& joined) {
+  if constexpr (JOINED)
+    return joined;
+  else
+    return own;
 }
 
 template <Product P, int BM, bool TALL>
 __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
-  constexpr int NW = 8, WM = 2, WN = 4, STAGES = 4, KS = kOrthKs<BM>, BK = 32 * KS;
-  constexpr int WTM = BM / WM, WTN = BM / WN, FM = WTM / 16, FN = WTN / 16;
+  // Wave tiles of BM / 2 x BM / WN. Smaller tiles (KG = 2): k-tiles of 64, of which each wave
+  // group takes one half on wave tiles of 64 x 64 -- a third fewer LDS reads than 64 x 32 tiles
+  // over the whole of it, and LDS is what bounds them.
+  constexpr int NW = 8, STAGES = 4, KG = kOrthKg<BM>, WN = 4 / KG, BK = 32 * KG;
+  constexpr int WTN = BM / WN, FM = BM / 32, FN = WTN / 16;
+  constexpr int WTM = BM / 2 / KG, FE = FM / KG;  // after the groups are joined
   // Gram: rows of the wide iterate, or columns of the tall one; Square: E is its own
   // transpose; Apply: P times the wide iterate (k along its rows), or the tall one times P.
   constexpr bool A_KMAJ = P != kGram || !TALL, B_KMAJ = P == kSquare || (P == kGram) != TALL;
@@ -209,41 +219,40 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
 #pragma unroll
     for (int j = 0; j < OpB::LD; ++j) dma_to_lds(rb, b_lds0 + slot * B_BYTES + j * NW * 1024, opb.off[j]);
   };
-  const int wm = wave / WN, wn = wave % WN, lrow = lane & 15, lkg = lane >> 4;
-  opa.init_frags(wm * WTM, lane);
+  const int kg = KG == 2 ? wave >> 2 : 0, wv = wave % (2 * WN), wm = wv / WN, wn = wv % WN;
+  const int lrow = lane & 15, lkg = lane >> 4;
+  opa.init_frags(wm * (BM / 2), lane);
   opb.init_frags(wn * WTN, lane);
-  half8 fa[KS][FM], fb[KS][FN];
+  half8 fa[FM], fb[FN];
   auto read_tile = [&](int kt) __attribute__((always_inline)) {
     const char* const As = a_lds + (kt % STAGES) * A_BYTES;
     const char* const Bs = b_lds + (kt % STAGES) * B_BYTES;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
+    for (int fm = 0; fm < FM; ++fm) fa[fm] = opa.frag(As, fm, kg);
 #pragma unroll
-      for (int fm = 0; fm < FM; ++fm) fa[ks][fm] = opa.frag(As, fm, ks);
-#pragma unroll
-      for (int fn = 0; fn < FN; ++fn) fb[ks][fn] = opb.frag(Bs, fn, ks);
-    }
+    for (int fn = 0; fn < FN; ++fn) fb[fn] = opb.frag(Bs, fn, kg);
   };
-  float4v acc[FM][FN];
+  float4v sum[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < FN; ++j) acc[i][j] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < FN; ++j) sum[i][j] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
   auto mma_tile = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
+    for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
-      for (int fm = 0; fm < FM; ++fm)
-#pragma unroll
-        for (int fn = 0; fn < FN; ++fn)
-          acc[fm][fn] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[ks][fn], fa[ks][fm], acc[fm][fn], 0, 0, 0);
+      for (int fn = 0; fn < FN; ++fn)
+        sum[fm][fn] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[fn], fa[fm], sum[fm][fn], 0, 0, 0);
   };
   pingpong_schedule<STAGES, PT, PT, (A_KMAJ && B_KMAJ && BM == 256)>(wave / 4, nk, copy_tile, read_tile, mma_tile);
   __syncthreads();  // the ring is free for staging
+  float4v joined_sum[KG == 2 ? FE : 1][FN];
+  if constexpr (KG == 2) join_k_groups<FM, FN>(smem, sum, joined_sum, wave, lane);
+  float4v(&acc)[FE][FN] = pick_sums<KG == 2>(sum, joined_sum);
 
   // Epilogue. The lane holds row r and columns c .. c + 3 of each 16 x 16 tile; the padded sizes
   // are multiples of 64, so a group of four lies inside the matrix or outside it.
-  const int wr0 = row0 + wm * WTM, wc0 = col0 + wn * WTN;
+  const int wr0 = row0 + wm * (BM / 2) + kg * WTM, wc0 = col0 + wn * WTN;
   using ST = StagedTile<WTM, WTN>;
   char* const stage = smem + wave * (orth_lds_bytes<BM>() / NW);
   static_assert(ST::BYTES <= orth_lds_bytes<BM>() / NW, "staged tile");
@@ -251,7 +260,7 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
 
   if constexpr (P == kApply) {
     // X' = diag(P) X + offdiag(P) hi(X). The old values of kAhead rows of tiles are in flight.
-    constexpr int kAhead = FM < 3 ? FM : 3;
+    constexpr int kAhead = FE < 3 ? FE : 3;
     half4 h[kAhead][FN], l[kAhead][FN];
     float dr[kAhead];
     auto fetch = [&](auto fm_c) __attribute__((always_inline)) {
@@ -271,7 +280,7 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
       for (int fn = 0; fn < FN; ++fn) dc[fn] = *(const float4v*)(DP + min(wc0 + 16 * fn + 4 * lkg, cols - 4));
     }
     static_for<kAhead>([&](auto i) __attribute__((always_inline)) { fetch(i); });
-    static_for<FM>([&](auto fm_c) __attribute__((always_inline)) {
+    static_for<FE>([&](auto fm_c) __attribute__((always_inline)) {
       constexpr int fm = decltype(fm_c)::value;
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -280,11 +289,11 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
         for (int e = 0; e < 4; ++e)
           acc[fm][fn][e] += (TALL ? dc[fn][e] : dr[fm % kAhead]) * joined(h[fm % kAhead][fn][e], l[fm % kAhead][fn][e]);
       __builtin_amdgcn_sched_barrier(0);
-      if constexpr (fm + kAhead < FM) fetch(std::integral_constant<int, fm + kAhead>{});
+      if constexpr (fm + kAhead < FE) fetch(std::integral_constant<int, fm + kAhead>{});
     });
     if (st.last) {
 #pragma unroll
-      for (int fm = 0; fm < FM; ++fm)
+      for (int fm = 0; fm < FE; ++fm)
 #pragma unroll
         for (int fn = 0; fn < FN; ++fn) acc[fm][fn] *= g.scale;
       ST::template stage<false>(stage, acc, lane);
@@ -299,7 +308,7 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
       store_staged<ST, WTM, false>(stage, lane, g.hi[st.in ^ 1] + o, ldx, rv, cv, 1);
       ST::wave_fence();
 #pragma unroll
-      for (int fm = 0; fm < FM; ++fm)
+      for (int fm = 0; fm < FE; ++fm)
 #pragma unroll
         for (int fn = 0; fn < FN; ++fn) {
           asm volatile("" : "+v"(acc[fm][fn]));  // round again: the rounded values kept from above would spill
@@ -333,7 +342,7 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
     };
     if constexpr (P == kSquare) {
       // P from E, D and E E; the E values of kAhead rows of tiles are in flight
-      constexpr int kAhead = FM < 3 ? FM : 3;
+      constexpr int kAhead = FE < 3 ? FE : 3;
       half4 x[kAhead][FN];
       float dr[kAhead];
       float4v dc[FN];
@@ -348,7 +357,7 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
 #pragma unroll
       for (int fn = 0; fn < FN; ++fn) dc[fn] = *(const float4v*)(D + min(wc0 + 16 * fn + 4 * lkg, cols - 4));
       static_for<kAhead>([&](auto i) __attribute__((always_inline)) { fetch(i); });
-      static_for<FM>([&](auto fm_c) __attribute__((always_inline)) {
+      static_for<FE>([&](auto fm_c) __attribute__((always_inline)) {
         constexpr int fm = decltype(fm_c)::value;
         __builtin_amdgcn_sched_barrier(0);
         const int r = wr0 + 16 * fm + lrow;
@@ -363,10 +372,10 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
           }
         split_diagonal(fm_c);
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (fm + kAhead < FM) fetch(std::integral_constant<int, fm + kAhead>{});
+        if constexpr (fm + kAhead < FE) fetch(std::integral_constant<int, fm + kAhead>{});
       });
     } else {
-      static_for<FM>([&](auto fm_c) __attribute__((always_inline)) { split_diagonal(fm_c); });
+      static_for<FE>([&](auto fm_c) __attribute__((always_inline)) { split_diagonal(fm_c); });
     }
     ST::template stage<false>(stage, acc, lane);
     ST::wave_fence();
@@ -378,7 +387,7 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
       static_assert(WTN * PITCH <= orth_lds_bytes<BM>() / NW, "transposed tile");
       ST::wave_fence();
 #pragma unroll
-      for (int fm = 0; fm < FM; ++fm)
+      for (int fm = 0; fm < FE; ++fm)
 #pragma unroll
         for (int fn = 0; fn < FN; ++fn)
 #pragma unroll

@@ -72,6 +72,31 @@ __device__ __forceinline__ void pingpong_schedule(int grp, int nk, Copy&& copy, 
   wait_vmcnt<0>();
 }
 
+// The two wave groups of a kernel that gives each group half of every k-tile hold partial sums
+// of the same wave tiles: wave w and w + 4. Each passes half of its rows of 16 x 16 tiles to the
+// other through LDS (16 bytes a lane, 2 KB FM per wave, all waves at the ring's place) and adds
+// what it gets to the half it keeps: group 0 rows 0 .. FM / 2 - 1, group 1 the others, in out.
+// Called by every wave once the ring is free.
+template <int FM, int FN, typename V>
+__device__ __forceinline__ void join_k_groups(char* smem, const V (&acc)[FM][FN], V (&out)[FM / 2][FN], int wave, int lane) {
+  constexpr int H = FM / 2, WAVE = H * FN * 64 * 16;
+  const bool second = wave >= 4;
+#pragma unroll
+  for (int i = 0; i < H; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const V give = second ? acc[i][j] : acc[i + H][j];
+      out[i][j] = second ? acc[i + H][j] : acc[i][j];
+      *(TG_LDS V*)(smem + wave * WAVE + ((i * FN + j) * 64 + lane) * 16) = give;
+    }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < H; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) out[i][j] += *(const TG_LDS V*)(smem + (wave ^ 4) * WAVE + ((i * FN + j) * 64 + lane) * 16);
+  __syncthreads();
+}
+
 // Stores a staged tile (StagedTile) to any C: 16-byte chunks where `vec` says that every
 // chunk of C is 16-byte aligned, single elements otherwise and in a chunk that N cuts. NT: the
 // result streams out (store_c); false for one that the next kernel reads.
