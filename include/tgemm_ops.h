@@ -113,6 +113,7 @@ TGEMM_API int orthogonalize_f16(int64_t batch, int64_t R, int64_t C, int dtype,
 #define TGEMM_MX_SKINNY 1
 #define TGEMM_MX_128 2
 #define TGEMM_MX_256 3
+#define TGEMM_MX_64 4   /* 64 x 128 tiles; not with binary16 A */
 TGEMM_API int mxfp4_gemm_cfg(int idx, int64_t M, int64_t N, int64_t K,
                              const void* A, int64_t lda, const void* scale_a, int64_t ldsa,
                              const void* B, int64_t ldb, const void* scale_b, int64_t ldsb,

@@ -27,7 +27,7 @@ def test_header_symbols_are_exported():
 
 def test_constants_match_header():
     text = header()
-    for name, value in (("GENERIC", tg.MX_GENERIC), ("SKINNY", tg.MX_SKINNY), ("128", tg.MX_128), ("256", tg.MX_256)):
+    for name, value in (("GENERIC", tg.MX_GENERIC), ("SKINNY", tg.MX_SKINNY), ("128", tg.MX_128), ("256", tg.MX_256), ("64", tg.MX_64)):
         assert re.search(rf"#define TGEMM_MX_{name} {value}\b", text)
     assert "(TGEMM_MAX_DIM - 512)" in text and tg.MX_MAX_DIM == (1 << 31) - 512
 
@@ -80,7 +80,7 @@ def gemm_f16(M=8, N=8, K=64, A=A16, lda=64, B=A16, ldb=32, SB=A16, ldsb=16, C=A1
     (dict(lda=31), tg.TGEMM_EINVAL_LD), (dict(ldb=31), tg.TGEMM_EINVAL_LD), (dict(ldsb=1), tg.TGEMM_EINVAL_LD),
     (dict(ldc=7), tg.TGEMM_EINVAL_LD), (dict(A=None), tg.TGEMM_ENULL), (dict(B=None), tg.TGEMM_ENULL),
     (dict(SB=None), tg.TGEMM_ENULL), (dict(C=None), tg.TGEMM_ENULL), (dict(C=A16 + 1), tg.TGEMM_EALIGN),
-    (dict(cfg=-1), tg.TGEMM_EINVAL_CFG), (dict(cfg=4), tg.TGEMM_EINVAL_CFG),
+    (dict(cfg=-1), tg.TGEMM_EINVAL_CFG), (dict(cfg=5), tg.TGEMM_EINVAL_CFG),
     (dict(cfg=tg.MX_SKINNY, M=65), tg.TGEMM_EINVAL_CFG), (dict(cfg=tg.MX_256, B=A16 + 4), tg.TGEMM_EINVAL_CFG),
     (dict(cfg=tg.MX_128, ldb=40), tg.TGEMM_EINVAL_CFG),
     (dict(M=0, A=None), tg.TGEMM_OK), (dict(N=0, B=None, C=None), tg.TGEMM_OK),
@@ -97,6 +97,7 @@ def test_gemm_more_refusals():
     assert gemm(SA=None) == tg.TGEMM_ENULL
     assert gemm_f16(lda=63) == tg.TGEMM_EINVAL_LD
     assert gemm_f16(A=A16 + 1) == tg.TGEMM_EALIGN
+    assert gemm_f16(cfg=tg.MX_64) == tg.TGEMM_EINVAL_CFG
     assert gemm_f16(cfg=tg.MX_128, lda=65) == tg.TGEMM_EINVAL_CFG
 
 

@@ -813,7 +813,7 @@ def fp8_block_scaled_linear(x, w_fp8, scale_w, block: int = 128, relu: bool = Fa
 
 # ---------------------------------------------------------------- the operators of tgemm_ops.h
 from . import mxfp4  # noqa: E402
-from .mxfp4 import (MX_128, MX_256, MX_BLOCK, MX_BLOCK_BYTES, MX_GENERIC, MX_MAX_DIM, MX_SKINNY,  # noqa: E402,F401
+from .mxfp4 import (MX_64, MX_128, MX_256, MX_BLOCK, MX_BLOCK_BYTES, MX_GENERIC, MX_MAX_DIM, MX_SKINNY,  # noqa: E402,F401
                     MX_SKINNY_ROWS, mxfp4_dequant, mxfp4_empty, mxfp4_gemm, mxfp4_gemm_f16, mxfp4_linear, mxfp4_quant,
                     mxfp4_select_config)
 from . import newton_schulz  # noqa: E402

@@ -41,7 +41,9 @@ struct MxGemmArgs {
 };
 
 // The kernels of a product, by index (tooling ABI: the _cfg entry points).
-enum MxConfig { kMxGeneric = 0, kMxSkinny = 1, kMx128 = 2, kMx256 = 3, kMxConfigs = 4 };
+enum MxConfig { kMxGeneric = 0, kMxSkinny = 1, kMx128 = 2, kMx256 = 3, kMx64 = 4, kMxConfigs = 5 };
+constexpr int mx_tile_m(int cfg) { return cfg == kMx256 ? 256 : cfg == kMx64 ? 64 : 128; }
+constexpr int mx_tile_n(int cfg) { return cfg == kMx256 ? 256 : 128; }
 constexpr int kMxSkinnyRows = 64;  // the skinny kernel's largest M
 hipError_t launch_mxfp4(int cfg, bool f16_a, const MxGemmArgs& g, hipStream_t s, int device);
 

@@ -260,24 +260,27 @@ __global__ __launch_bounds__(256) void dequant_mxfp4_rows(MxDequantArgs q) {
 // holds; they meet zero codes (out-of-range copies) and are replaced or cleared.
 // Requirements (host): A, B, SA, SB 16-byte aligned, their row strides multiples of 16.
 //
-// 128 x 128 tiles, for small output grids: the two-group ping-pong (tgemm_pingpong.h) over four
-// slots. Each group takes half of every k-tile on wave tiles of 64 x 64 (a third fewer LDS reads
-// than 64 x 32 tiles over the whole of it), and the groups' sums are joined at the end.
-template <int PANEL>
-__global__ __launch_bounds__(512) void gemm_mxfp4_pp128(MxGemmArgs g) {
-  constexpr int BM = 128, BN = 128, NW = 8, STAGES = 4, WT = 64, FM = WT / 16, FN = WT / 16;
-  using Op = PpOperand<128, 64, 16, true, NW>;  // both operands
-  constexpr int SLOT = Op::BYTES, LD = Op::LD;
+// Small output grids: the two-group ping-pong (tgemm_pingpong.h). Each group takes half of every
+// k-tile on wave tiles of 64 x 64 (128 x 128 tiles; a third fewer LDS reads than 64 x 32 tiles over
+// the whole of it) or 64 x 32 (64 x 128 tiles), and the groups' sums are joined at the end. What
+// bounds them is how many bytes a compute unit has on their way: 128 x 128 tiles have room for
+// four slots of 32 KB, 64 x 128 ones for six of 24 KB on twice the compute units.
+template <int BM, int STAGES, int PANEL>
+__global__ __launch_bounds__(512) void gemm_mxfp4_small(MxGemmArgs g) {
+  constexpr int BN = 128, NW = 8, WN = BM == 128 ? 2 : 4, WTN = BN / WN, FM = 4, FN = WTN / 16;
+  using OpA = PpOperand<BM, 64, 16, true, NW>;
+  using OpB = PpOperand<BN, 64, 16, true, NW>;
+  constexpr int A_SLOT = OpA::BYTES, B_SLOT = OpB::BYTES;
   constexpr int TB = 8, GROUP = 2;  // blocks per row of a k-tile, k-tiles per scale group
   // Group 1 copies scale group s with its first k-tile 2 s in iteration 2 s - STAGES + 1, when
-  // that k-tile's group s - 2 may still be read: three slots would do, four make it a mask.
-  constexpr int SLOTS = 4, SG_BYTES = (BM + BN) * 16;
-  static_assert(Op::REM == 0 && STAGES == 4, "copies");
+  // that k-tile may still be read: the slot's former group s - 4 ended with k-tile 2 s - 7.
+  constexpr int SLOTS = 4, SG_BYTES = (BM + BN) * 16, SC_A = BM / 64;
+  static_assert(OpA::REM == 0 && OpB::REM == 0 && STAGES <= 7 && SC_A + BN / 64 <= 4, "copies");
 
   extern __shared__ __attribute__((aligned(16))) char smem[];
   char* const a_lds = smem;
-  char* const b_lds = smem + STAGES * SLOT;
-  char* const s_lds = b_lds + STAGES * SLOT;
+  char* const b_lds = smem + STAGES * A_SLOT;
+  char* const s_lds = b_lds + STAGES * B_SLOT;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int grp = wave >> 2;
@@ -288,40 +291,41 @@ __global__ __launch_bounds__(512) void gemm_mxfp4_pp128(MxGemmArgs g) {
   const int nk = (g.KB + TB - 1) / TB;
   const int kin_last = (g.KB - (nk - 1) * TB) * (kMxBlockBytes / 2);  // in halves
 
-  Op opa, opb;
+  OpA opa;
+  OpB opb;
   opa.init_copies((const _Float16*)g.A, g.lda / 2, row0, mvalid, kin_last, wave, lane);
   opb.init_copies((const _Float16*)g.B, g.ldb / 2, col0, nvalid, kin_last, wave, lane);
   const uint32_t a_lds0 = lds_addr(a_lds) + wave * 1024, b_lds0 = lds_addr(b_lds) + wave * 1024;
-  // The scale copies (64 rows of A or B each) are group 1's, one per wave.
+  // The scale copies (64 rows of A or B each) are group 1's, at most one per wave.
   const int part = wave & 3;
-  const bool s_is_a = part < 2;
-  const int s_row = (part & 1) * 64;
+  const bool s_is_a = part < SC_A;
+  const int s_row = (s_is_a ? part : part - SC_A) * 64;
   const int64_t s_ld = s_is_a ? g.ldsa : g.ldsb;
   const uint8_t* const s_base = s_is_a ? g.SA + (int64_t)(row0 + s_row) * s_ld : g.SB + (int64_t)(col0 + s_row) * s_ld;
   const uint32_t s_off = lane < (s_is_a ? mvalid : nvalid) - s_row ? (uint32_t)lane * (uint32_t)s_ld : kOob;
   const uint32_t s_dst = lds_addr(s_lds) + part * 1024;
   auto copy_tile = [&](int t, auto group) __attribute__((always_inline)) {
-    if (decltype(group)::value == 1 && t % GROUP == 0 && t < nk)
+    if (decltype(group)::value == 1 && t % GROUP == 0 && t < nk && part < SC_A + BN / 64)
       dma_to_lds(make_rsrc(s_base + (int64_t)(t / GROUP) * 16, kMaxRange), s_dst + (t / GROUP % SLOTS) * SG_BYTES, s_off);
     const int4v ra = opa.rsrc(t, nk, nk), rb = opb.rsrc(t, nk, nk);
     const int slot = t % STAGES;
     const bool last = t == nk - 1;
 #pragma unroll
-    for (int j = 0; j < LD; ++j) dma_to_lds(ra, a_lds0 + slot * SLOT + j * NW * 1024, last ? opa.off_last[j] : opa.off[j]);
+    for (int j = 0; j < OpA::LD; ++j) dma_to_lds(ra, a_lds0 + slot * A_SLOT + j * NW * 1024, last ? opa.off_last[j] : opa.off[j]);
 #pragma unroll
-    for (int j = 0; j < LD; ++j) dma_to_lds(rb, b_lds0 + slot * SLOT + j * NW * 1024, last ? opb.off_last[j] : opb.off[j]);
+    for (int j = 0; j < OpB::LD; ++j) dma_to_lds(rb, b_lds0 + slot * B_SLOT + j * NW * 1024, last ? opb.off_last[j] : opb.off[j]);
   };
 
-  const int wm = part >> 1, wn = part & 1, lrow = lane & 15, lblk = lane >> 4;
-  opa.init_frags(wm * WT, lane);
-  opb.init_frags(wn * WT, lane);
-  const char* const sa_lds = s_lds + (wm * WT + lrow) * 16;
-  const char* const sb_lds = s_lds + (BM + wn * WT + lrow) * 16;
+  const int wm = part / WN, wn = part % WN, lrow = lane & 15, lblk = lane >> 4;
+  opa.init_frags(wm * 64, lane);
+  opb.init_frags(wn * WTN, lane);
+  const char* const sa_lds = s_lds + (wm * 64 + lrow) * 16;
+  const char* const sb_lds = s_lds + (BM + wn * WTN + lrow) * 16;
   half8 fa[FM], fb[FN];
   int sa[FM], sb[FN];
   auto read_tile = [&](int t) __attribute__((always_inline)) {
-    const char* const As = a_lds + (t % STAGES) * SLOT;
-    const char* const Bs = b_lds + (t % STAGES) * SLOT;
+    const char* const As = a_lds + (t % STAGES) * A_SLOT;
+    const char* const Bs = b_lds + (t % STAGES) * B_SLOT;
     // (a lane whose block lies past KB takes the last block's scale)
     const int off = (t / GROUP % SLOTS) * SG_BYTES + TB * (t % GROUP) + max(min(4 * grp + lblk, g.KB - 1 - TB * t), 0);
 #pragma unroll
@@ -352,23 +356,24 @@ __global__ __launch_bounds__(512) void gemm_mxfp4_pp128(MxGemmArgs g) {
       for (int fn = 0; fn < FN; ++fn)
         sum[fm][fn] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(fb[fn]), wide(fa[fm]), sum[fm][fn], 4, 4, 0, sb[fn], 0, sa[fm]);
   };
-  pingpong_schedule<STAGES, 2 * LD, 2 * LD, false>(grp, nk, copy_tile, read_tile, mma_tile);
+  pingpong_schedule<STAGES, OpA::LD + OpB::LD, OpA::LD + OpB::LD, false>(grp, nk, copy_tile, read_tile, mma_tile);
 
   __syncthreads();
   float4v acc[FM / 2][FN];
   join_k_groups<FM, FN>(smem, sum, acc, wave, lane);
-  using ST = StagedTile<WT / 2, WT>;
+  using ST = StagedTile<32, WTN>;
   char* const stage = smem + wave * ST::BYTES;
   if (g.relu != 0)
     ST::template stage<true>(stage, acc, lane);
   else
     ST::template stage<false>(stage, acc, lane);
   ST::wave_fence();
-  const int r0 = wm * WT + grp * (WT / 2), c0 = wn * WT;
-  store_staged<ST, WT / 2>(stage, lane, g.C + (int64_t)(row0 + r0) * g.ldc + col0 + c0, g.ldc, mvalid - r0, nvalid - c0, g.vec_c);
+  const int r0 = wm * 64 + grp * 32, c0 = wn * WTN;
+  store_staged<ST, 32>(stage, lane, g.C + (int64_t)(row0 + r0) * g.ldc + col0 + c0, g.ldc, mvalid - r0, nvalid - c0, g.vec_c);
 }
 
-constexpr int kMx128Lds = 4 * 2 * 128 * 128 + 4 * 256 * 16;
+template <int BM, int STAGES>
+constexpr int kMxSmallLds = STAGES * (BM + 128) * 128 + 4 * (BM + 128) * 16;
 
 // ------------------------------------------------------------------------------------
 // 256 x 256 tiles: two slots of k-tiles. A wave reads all fragments of a k-tile (96 registers)
@@ -895,9 +900,11 @@ hipError_t launch_wq_pp(const MxGemmArgs& g, hipStream_t s, int device) {
   constexpr int ring = wq_lds_bytes<BM, BM, 2, 4, 4>(), st = 8 * StagedTile<BM / 2, BM / 4>::BYTES;
   return launch_big(gemm_f16_mxfp4_pp<BM, BM, 2, 4, 4, 4>, ring > st ? ring : st, ready, g, s, device);
 }
-hipError_t launch_mx_128(const MxGemmArgs& g, hipStream_t s, int device) {
+template <int BM, int STAGES>
+hipError_t launch_mx_small(const MxGemmArgs& g, hipStream_t s, int device) {
   static std::atomic<uint64_t> ready{0};
-  return launch_big(gemm_mxfp4_pp128<4>, kMx128Lds, ready, g, s, device);
+  static_assert(kMxSmallLds<BM, STAGES> <= 160 * 1024, "LDS");
+  return launch_big(gemm_mxfp4_small<BM, STAGES, 4>, kMxSmallLds<BM, STAGES>, ready, g, s, device);
 }
 hipError_t launch_mx_256(const MxGemmArgs& g, hipStream_t s, int device) {
   static std::atomic<uint64_t> ready{0};
@@ -931,12 +938,12 @@ hipError_t launch_skinny(const MxGemmArgs& g, hipStream_t s, int device) {
 
 hipError_t launch_mxfp4(int cfg, bool f16_a, const MxGemmArgs& args, hipStream_t s, int device) {
   MxGemmArgs g = args;
-  const int tile = cfg == kMx256 ? 256 : 128;
-  g.tiles_m = (int)ceil_div(g.M, tile);
-  g.tiles_n = (int)ceil_div(g.N, tile);
+  g.tiles_m = (int)ceil_div(g.M, mx_tile_m(cfg));
+  g.tiles_n = (int)ceil_div(g.N, mx_tile_n(cfg));
   switch (cfg) {
     case kMxSkinny: return f16_a ? launch_skinny<true>(g, s, device) : launch_skinny<false>(g, s, device);
-    case kMx128: return f16_a ? launch_wq_pp<128>(g, s, device) : launch_mx_128(g, s, device);
+    case kMx128: return f16_a ? launch_wq_pp<128>(g, s, device) : launch_mx_small<128, 4>(g, s, device);
+    case kMx64: return f16_a ? hipErrorNotSupported : launch_mx_small<64, 6>(g, s, device);
     case kMx256: return f16_a ? launch_wq_pp<256>(g, s, device) : launch_mx_256(g, s, device);
     default: break;
   }

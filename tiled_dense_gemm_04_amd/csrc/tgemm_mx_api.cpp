@@ -77,10 +77,12 @@ int run(bool f16_a, int force, int64_t M, int64_t N, int64_t K, const void* A, i
   if (force >= 0 && cfg != kSelectZeroFill) {
     if (force != tgemm::kMxGeneric && cfg == tgemm::kMxGeneric) return TGEMM_EINVAL_CFG;
     if (force == tgemm::kMxSkinny && M > tgemm::kMxSkinnyRows) return TGEMM_EINVAL_CFG;
+    if (force == tgemm::kMx64 && f16_a) return TGEMM_EINVAL_CFG;
     cfg = force;
   }
-  const int64_t tile = cfg == tgemm::kMx256 ? 256 : 128;
-  const int64_t grid = cfg == tgemm::kMxSkinny ? tgemm::ceil_div(N, 16) : tgemm::ceil_div(M, tile) * tgemm::ceil_div(N, tile);
+  const int64_t grid = cfg == tgemm::kMxSkinny
+                           ? tgemm::ceil_div(N, 16)
+                           : tgemm::ceil_div(M, tgemm::mx_tile_m(cfg)) * tgemm::ceil_div(N, tgemm::mx_tile_n(cfg));
   if (grid >= kMaxGrid) return TGEMM_EINVAL_DIM;
   int dev = -1;
   const int d = tgemm::current_device(&dev);
