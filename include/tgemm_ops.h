@@ -66,8 +66,8 @@ TGEMM_API int mxfp4_gemm(int64_t M, int64_t N, int64_t K,
 
 /*
  * C = ReLU?(A @ W^T) of binary16 A (M x K, lda elements) and an MXFP4 weight (N x K) decoded to
- * binary16 as mxfp4_dequant does, accumulated in float32. Up to 64 rows (single tokens, small
- * batches) a kernel that reads the weight once. The fast kernels also need A 16-byte aligned, lda
+ * binary16 as mxfp4_dequant does, accumulated in float32. For few rows (single tokens, small
+ * batches) a kernel reads the weight once for every 64 rows. The fast kernels also need A 16-byte aligned, lda
  * and K multiples of 8 and lda at most TGEMM_FAST_MAX_LD. Otherwise as mxfp4_gemm.
  */
 TGEMM_API int mxfp4_gemm_f16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
@@ -107,7 +107,7 @@ TGEMM_API int orthogonalize_f16(int64_t batch, int64_t R, int64_t C, int dtype,
 
 /* MXFP4 tooling: the two products forced to kernel idx (TGEMM_MX_*; TGEMM_EINVAL_CFG for an
  * index out of range, a fast kernel that cannot take the arguments, or the skinny kernel with M
- * > 64), and the kernel a call takes (-100 / -101 as for tgemm_select_config; f16_a: the
+ * > 256), and the kernel a call takes (-100 / -101 as for tgemm_select_config; f16_a: the
  * product with binary16 A, scale_a ignored). */
 #define TGEMM_MX_GENERIC 0
 #define TGEMM_MX_SKINNY 1

@@ -121,7 +121,8 @@ def test_quant_nonfinite_and_strided(gpu):
 
 # Sizes around the 16-, 128- and 256-wide tiles, the k-tiles of 32 and 128 and the scale groups of 512.
 GEMM_SHAPES = [(1, 1, 1), (1, 16, 512), (2, 40, 33), (16, 17, 544), (17, 300, 2080), (33, 264, 1100), (64, 130, 96),
-               (65, 257, 128), (128, 128, 1056), (300, 513, 640), (257, 255, 160), (520, 392, 4128)]
+               (65, 257, 128), (128, 128, 1056), (300, 513, 640), (257, 255, 160), (520, 392, 4128),
+               (130, 40, 1000)]
 CONFIGS = [None, tg.MX_GENERIC, tg.MX_SKINNY, tg.MX_128, tg.MX_256, tg.MX_64]
 CONFIGS_F16 = CONFIGS[:-1]  # no 64 x 128 tiles with binary16 A
 

@@ -81,7 +81,7 @@ def gemm_f16(M=8, N=8, K=64, A=A16, lda=64, B=A16, ldb=32, SB=A16, ldsb=16, C=A1
     (dict(ldc=7), tg.TGEMM_EINVAL_LD), (dict(A=None), tg.TGEMM_ENULL), (dict(B=None), tg.TGEMM_ENULL),
     (dict(SB=None), tg.TGEMM_ENULL), (dict(C=None), tg.TGEMM_ENULL), (dict(C=A16 + 1), tg.TGEMM_EALIGN),
     (dict(cfg=-1), tg.TGEMM_EINVAL_CFG), (dict(cfg=5), tg.TGEMM_EINVAL_CFG),
-    (dict(cfg=tg.MX_SKINNY, M=65), tg.TGEMM_EINVAL_CFG), (dict(cfg=tg.MX_256, B=A16 + 4), tg.TGEMM_EINVAL_CFG),
+    (dict(cfg=tg.MX_SKINNY, M=tg.MX_SKINNY_ROWS + 1), tg.TGEMM_EINVAL_CFG), (dict(cfg=tg.MX_256, B=A16 + 4), tg.TGEMM_EINVAL_CFG),
     (dict(cfg=tg.MX_128, ldb=40), tg.TGEMM_EINVAL_CFG),
     (dict(M=0, A=None), tg.TGEMM_OK), (dict(N=0, B=None, C=None), tg.TGEMM_OK),
     (dict(M=1 << 30, N=1 << 30, ldc=1 << 30), tg.TGEMM_EINVAL_DIM),
@@ -107,7 +107,10 @@ def test_kernel_choice():
         assert sel(0, 8, 64, f16) == tg.SELECT_NOOP and sel(8, 8, 0, f16) == tg.SELECT_ZERO_FILL
         assert sel(1, 4096, 4096, f16) == tg.MX_SKINNY
         assert sel(8192, 8192, 8192, f16) == tg.MX_256
-        assert sel(1024, 512, 4096, f16) == tg.MX_128
+        assert sel(2048, 1024, 4096, f16) == (tg.MX_128 if f16 else tg.MX_64)
+        assert sel(64, 4096, 4096, f16) == tg.MX_SKINNY
+        assert sel(128, 2048, 96, f16) == (tg.MX_SKINNY if f16 else tg.MX_64)
+        assert sel(2048, 2048, 4096, f16) == tg.MX_128
         # any N, and scales or codes the copies cannot take
         assert sel(4095, 4097, 64, f16) == tg.MX_256
         assert sel(300, 300, 96, f16, ldsb=3) == tg.MX_GENERIC
@@ -119,7 +122,7 @@ def test_kernel_choice():
     assert sel(300, 300, 100, True) == tg.MX_GENERIC      # K no multiple of 8
     assert sel(300, 300, 96, True, lda=100) == tg.MX_GENERIC
     assert sel(300, 300, 96, True, A=A16 + 2) == tg.MX_GENERIC
-    assert sel(300, 300, 100, False) == tg.MX_128         # codes are whole blocks: any K
+    assert sel(300, 300, 100, False) == tg.MX_64         # codes are whole blocks: any K
 
 
 def test_python_refusals():

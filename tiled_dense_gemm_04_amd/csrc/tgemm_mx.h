@@ -44,7 +44,8 @@ struct MxGemmArgs {
 enum MxConfig { kMxGeneric = 0, kMxSkinny = 1, kMx128 = 2, kMx256 = 3, kMx64 = 4, kMxConfigs = 5 };
 constexpr int mx_tile_m(int cfg) { return cfg == kMx256 ? 256 : cfg == kMx64 ? 64 : 128; }
 constexpr int mx_tile_n(int cfg) { return cfg == kMx256 ? 256 : 128; }
-constexpr int kMxSkinnyRows = 64;  // the skinny kernel's largest M
+constexpr int kMxSkinnyTile = 64;   // rows of A per workgroup of the skinny kernel
+constexpr int kMxSkinnyRows = 256;  // its largest M
 hipError_t launch_mxfp4(int cfg, bool f16_a, const MxGemmArgs& g, hipStream_t s, int device);
 
 // The current device, if it is one the library runs on (tgemm_api.cpp).

@@ -661,8 +661,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f16_mxfp4_pp(MxGemmArgs g) 
 }
 
 // ------------------------------------------------------------------------------------
-// Few rows (M <= 64: single tokens and small batches): bound by reading the weight once. A
-// workgroup owns 16 rows of the weight and splits K over its W waves in runs of 512 (16 blocks:
+// Few rows (single tokens and small batches): bound by reading the weight once for every 64 rows
+// of A. A workgroup owns 16 rows of the weight and up to 64 of A and splits K over its W waves in runs of 512 (16 blocks:
 // one 16-byte load of scales per row, four loads of codes), so all of a wave's loads of a run
 // are in flight at once; the waves' partial sums are added in wave order. Lane l of the weight's
 // fragment holds block l / 16 (of four) of row l % 16, 32 codes.
@@ -672,7 +672,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f16_mxfp4_pp(MxGemmArgs g) 
 // of its own for 16 bytes of it (13 us for 37 x 3000 x 4096, against 9); so the rows of A are
 // loaded 256 contiguous bytes each, four rows per load, and pass through a part of LDS that
 // belongs to the wave (no barrier; chunk c of row r at place c ^ r, free of bank conflicts).
-template <int MT, int W, bool F16A>
+// LR: loads that cover the rows of A (4 MT, or one for up to four rows, the others zeros).
+template <int MT, int W, int LR, bool F16A>
 __global__ __launch_bounds__(64 * W) void gemm_mxfp4_skinny(MxGemmArgs g) {
   constexpr int A_BYTES = F16A ? MT * 16 * 256 : 0;              // per wave: 16 MT rows of 128 k
   constexpr int P_BYTES = W * MT * 64 * 16;                      // partial sums, in the same place
@@ -681,7 +682,8 @@ __global__ __launch_bounds__(64 * W) void gemm_mxfp4_skinny(MxGemmArgs g) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lrow = lane & 15, lblk = lane >> 4;
-  const int n0 = (int)blockIdx.x * 16;
+  const int n0 = (int)blockIdx.x * 16, m0 = (int)blockIdx.y * kMxSkinnyTile;
+  const int rows = min(g.M - m0, MT * 16);
   const int n = min(n0 + lrow, g.N - 1);  // rows past N read the last one, their sums are dropped
   const uint8_t* const brow = g.B + (int64_t)n * g.ldb + lblk * kMxBlockBytes;
   const uint8_t* const srow = g.SB + (int64_t)n * g.ldsb;
@@ -691,6 +693,10 @@ __global__ __launch_bounds__(64 * W) void gemm_mxfp4_skinny(MxGemmArgs g) {
 #pragma unroll
   for (int i = 0; i < MT; ++i) acc[i] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
 
+  if constexpr (F16A) {
+    const half8 zero = {0, 0, 0, 0, 0, 0, 0, 0};
+    for (int i = LR; i < 4 * MT; ++i) *(TG_LDS half8*)(a_lds + i * 1024 + lane * 16) = zero;
+  }
   for (int r = wave; r < runs; r += W) {
     const int kb0 = r * 16;
     uint4v w[4];
@@ -706,14 +712,14 @@ __global__ __launch_bounds__(64 * W) void gemm_mxfp4_skinny(MxGemmArgs g) {
       // rows 4 i + lane / 16 of A, 16 bytes per lane: AHEAD chunks are loaded before they are used
       // (all four of a run for up to 16 rows)
       constexpr int AHEAD = MT == 1 ? 4 : MT == 2 ? 2 : 1;
-      half8 x[AHEAD][4 * MT];
+      half8 x[AHEAD][LR];
       auto fetch = [&](int c) __attribute__((always_inline)) {
         const int k = (kb0 + 4 * c) * kMxBlock + 8 * lrow;
 #pragma unroll
-        for (int i = 0; i < 4 * MT; ++i) {
+        for (int i = 0; i < LR; ++i) {
           x[c % AHEAD][i] = (half8){0, 0, 0, 0, 0, 0, 0, 0};
           const int m = 4 * i + lblk;
-          if (m < g.M && k < g.K) x[c % AHEAD][i] = *(const half8*)((const _Float16*)g.A + (int64_t)m * g.lda + k);
+          if (m < rows && k < g.K) x[c % AHEAD][i] = *(const half8*)((const _Float16*)g.A + (int64_t)(m0 + m) * g.lda + k);
         }
       };
 #pragma unroll
@@ -721,7 +727,7 @@ __global__ __launch_bounds__(64 * W) void gemm_mxfp4_skinny(MxGemmArgs g) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
 #pragma unroll
-        for (int i = 0; i < 4 * MT; ++i) {
+        for (int i = 0; i < LR; ++i) {
           const int m = 4 * i + lblk;
           *(TG_LDS half8*)(a_lds + m * 256 + ((lrow ^ (m & 15)) << 4)) = x[c % AHEAD][i];
         }
@@ -742,7 +748,7 @@ __global__ __launch_bounds__(64 * W) void gemm_mxfp4_skinny(MxGemmArgs g) {
     } else {
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        const int m = min(16 * i + lrow, g.M - 1);  // rows past M read the last one
+        const int m = m0 + min(16 * i + lrow, rows - 1);  // rows past M read the last one
         const uint8_t* const arow = (const uint8_t*)g.A + (int64_t)m * g.lda + (int64_t)(kb0 + lblk) * kMxBlockBytes;
         const uint4v sa = load_any<uint4v>(g.SA + (int64_t)m * g.ldsa + kb0);
         uint4v a[4];
@@ -771,10 +777,10 @@ __global__ __launch_bounds__(64 * W) void gemm_mxfp4_skinny(MxGemmArgs g) {
 #pragma unroll
     for (int w = 1; w < W; ++w) s += *(const TG_LDS float4v*)(part + (w * MT + i) * 64 + lane);
     const int m = 16 * i + lrow, c = n0 + 4 * lblk;
-    if (m >= g.M) continue;
+    if (m >= rows) continue;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (c + e < g.N) g.C[(int64_t)m * g.ldc + c + e] = (_Float16)(g.relu ? relu_f(s[e]) : s[e]);
+      if (c + e < g.N) g.C[(int64_t)(m0 + m) * g.ldc + c + e] = (_Float16)(g.relu ? relu_f(s[e]) : s[e]);
   }
 }
 
@@ -883,15 +889,19 @@ __global__ __launch_bounds__(256) void gemm_mxfp4_generic(MxGemmArgs g) {
 // kernel and device.
 template <typename K>
 hipError_t launch_big(K kern, int lds, std::atomic<uint64_t>& ready, const MxGemmArgs& g, hipStream_t s, int device,
-                      int threads = 512) {
+                      dim3 grid, int threads) {
   const uint64_t bit = 1ull << (device & 63);
   if (!(ready.load(std::memory_order_acquire) & bit)) {
     const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
     ready.fetch_or(bit, std::memory_order_acq_rel);
   }
-  hipLaunchKernelGGL(kern, dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n)), dim3(threads), lds, s, g);
+  hipLaunchKernelGGL(kern, grid, dim3(threads), lds, s, g);
   return hipGetLastError();
+}
+template <typename K>
+hipError_t launch_big(K kern, int lds, std::atomic<uint64_t>& ready, const MxGemmArgs& g, hipStream_t s, int device) {
+  return launch_big(kern, lds, ready, g, s, device, dim3((unsigned)((int64_t)g.tiles_m * g.tiles_n)), 512);
 }
 
 template <int BM>
@@ -911,22 +921,22 @@ hipError_t launch_mx_256(const MxGemmArgs& g, hipStream_t s, int device) {
   return launch_big(gemm_mxfp4_pp256<4, 8>, kMx256Lds, ready, g, s, device);
 }
 
-template <int MT, int W, bool F16A>
+template <int MT, int W, bool F16A, int LR = 4 * MT>
 hipError_t launch_skinny_tile(const MxGemmArgs& g, hipStream_t s, int device) {
   static std::atomic<uint64_t> ready{0};
   constexpr int lds = W * MT * (F16A ? 4096 : 1024);
-  MxGemmArgs a = g;
-  a.tiles_m = 1;
-  a.tiles_n = (int)ceil_div(g.N, 16);
-  return launch_big(gemm_mxfp4_skinny<MT, W, F16A>, lds, ready, a, s, device, 64 * W);
+  const dim3 grid((unsigned)ceil_div(g.N, 16), (unsigned)ceil_div(g.M, kMxSkinnyTile));
+  return launch_big(gemm_mxfp4_skinny<MT, W, LR, F16A>, lds, ready, g, s, device, grid, 64 * W);
 }
 
 // Eight waves, or sixteen for up to 16 rows where K has more than eight runs of 512 (every run
 // of a wave after its first waits for memory again; more rows need the registers).
 template <bool F16A>
 hipError_t launch_skinny(const MxGemmArgs& g, hipStream_t s, int device) {
-  switch ((g.M + 15) / 16) {
+  switch (g.M >= kMxSkinnyTile ? 4 : (g.M + 15) / 16) {
     case 1:
+      if (F16A && g.M <= 4)
+        return g.KB > 8 * 16 ? launch_skinny_tile<1, 16, F16A, 1>(g, s, device) : launch_skinny_tile<1, 8, F16A, 1>(g, s, device);
       return g.KB > 8 * 16 ? launch_skinny_tile<1, 16, F16A>(g, s, device) : launch_skinny_tile<1, 8, F16A>(g, s, device);
     case 2: return launch_skinny_tile<2, 8, F16A>(g, s, device);
     case 3: return launch_skinny_tile<3, 8, F16A>(g, s, device);

@@ -47,12 +47,26 @@ bool fast_eligible(bool f16_a, int64_t K, const void* A, int64_t lda, const void
   return aligned16(A) && aligned16(SA) && lda % 16 == 0 && ldsa % 16 == 0 && lda <= cap && ldsa <= cap;
 }
 
-// Kernel choice of a fast-eligible call: the skinny kernel up to 64 rows (each workgroup reads
-// its weight rows once), then 256 x 256 tiles when they fill at least half of the 256 compute
-// units, else 128 x 128.
-int choose(int64_t M, int64_t N) {
-  if (M <= tgemm::kMxSkinnyRows) return tgemm::kMxSkinny;
-  return tgemm::ceil_div(M, 256) * tgemm::ceil_div(N, 256) >= 128 ? tgemm::kMx256 : tgemm::kMx128;
+// Kernel choice of a fast-eligible call, by rounds of workgroups over the 256 compute units. One
+// round at K = 4096 measured (microseconds beyond the launch; all scale with K):
+//   A in MXFP4:    skinny 4 (up to 16 rows), 5 (48), 8 (64); 64 x 128 tiles 11 to 13; 128 x 128
+//                  14 to 15; 256 x 256 28 to 36;
+//   A in binary16: skinny 5, 9, 12; 128 x 128 tiles 42; 256 x 256 84 to 100.
+// The skinny kernel takes 64 rows of A by 16 of the weight per workgroup.
+int choose(bool f16_a, int64_t M, int64_t N) {
+  const int64_t skinny = tgemm::ceil_div(M, tgemm::kMxSkinnyTile) * tgemm::ceil_div(N, 16);
+  const int64_t t128 = tgemm::ceil_div(M, 128) * tgemm::ceil_div(N, 128);
+  const int64_t t64 = tgemm::ceil_div(M, 64) * tgemm::ceil_div(N, 128);
+  if (M <= 32) return tgemm::kMxSkinny;
+  if (f16_a) {
+    // up to three rounds of the skinny kernel cost less than one of 128 x 128 tiles, and two
+    // rounds of those about one of 256 x 256 (512 tiles: 80 against 85 us; 576: 88 against 67)
+    if (M <= tgemm::kMxSkinnyRows && skinny <= 3 * 256) return tgemm::kMxSkinny;
+    return t128 <= 512 ? tgemm::kMx128 : tgemm::kMx256;
+  }
+  if (M <= tgemm::kMxSkinnyTile && skinny <= 256) return tgemm::kMxSkinny;
+  if (t64 <= 256) return tgemm::kMx64;
+  return t128 <= 256 ? tgemm::kMx128 : tgemm::kMx256;
 }
 
 constexpr int kSelectNoop = -100, kSelectZeroFill = -101;
@@ -64,7 +78,7 @@ int select(bool f16_a, int64_t M, int64_t N, int64_t K, const void* A, int64_t l
   if (M == 0 || N == 0) return kSelectNoop;
   if (K == 0) return kSelectZeroFill;
   if (!fast_eligible(f16_a, K, A, lda, SA, ldsa, B, ldb, SB, ldsb)) return tgemm::kMxGeneric;
-  return choose(M, N);
+  return choose(f16_a, M, N);
 }
 
 // Runs the product; force: a kernel index, or -1 for the choice.

@@ -16,7 +16,7 @@ MX_BLOCK = 32
 MX_BLOCK_BYTES = 16
 MX_MAX_DIM = (1 << 31) - 512         # TGEMM_MX_MAX_DIM
 MX_GENERIC, MX_SKINNY, MX_128, MX_256, MX_64 = range(5)   # TGEMM_MX_*
-MX_SKINNY_ROWS = 64
+MX_SKINNY_ROWS = 256
 
 _i64, _p, _i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
 _GEMM = [_i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i32, _p]
