@@ -156,7 +156,7 @@ def test_gemm_f16(gpu, cfg):
     for i, (M, N, K) in enumerate(GEMM_SHAPES):
         if cfg == tg.MX_SKINNY and M > tg.MX_SKINNY_ROWS:
             continue
-        if cfg not in (None, tg.MX_GENERIC):
+        if cfg not in (None, tg.MX_GENERIC, tg.MX_SKINNY):
             K = -(-K // 8) * 8
         a, B, sb = f16_case(M, N, K, 700 + i)
         for relu in (False, True):
@@ -233,15 +233,16 @@ def test_unaligned_operands_take_the_generic_kernel(gpu):
     for off, ldq, lds in ((1, 113, 7), (0, 112, 7), (16, 112, 16), (5, 130, 9)):
         c = tg.mxfp4_gemm(shifted(A, off, ldq), shifted(sa, off, lds), shifted(B, off, ldq), shifted(sb, off, lds))
         mx.check(c.cpu().numpy(), ref, tol, f"offset {off} strides {ldq} {lds}")
-    a, _, _ = f16_case(M, N, K, 42)
     w = mx.to_half(mx.values(B, sb)[:, :K]).astype(np.float64)
-    ref, tol = mx.product(a.astype(np.float64), w)
-    for off, ld in ((1, 200), (0, 203), (8, 208)):
+    cases = [(M, *f16_case(M, N, K, 42)[:1], off, ld) for M in (70, 300) for off, ld in ((1, 200), (0, 203), (8, 208))]
+    for M, a, off, ld in cases:
+        ref, tol = mx.product(a.astype(np.float64), w)
         buf = gpu.full((off + M * ld,), float("nan"), dtype=gpu.float16, device="cuda")
         ad = buf[off:].as_strided((M, K), (ld, 1))
         ad.copy_(to_dev(a))
-        c = tg.mxfp4_gemm_f16(ad, *dev_matrix(B, sb))
-        mx.check(c.cpu().numpy(), ref, tol, f"a at {off}, stride {ld}")
+        for kernel in (None, tg.MX_GENERIC):
+            c = tg.mxfp4_gemm_f16(ad, *dev_matrix(B, sb), cfg=kernel)
+            mx.check(c.cpu().numpy(), ref, tol, f"{M} rows of a at {off}, stride {ld}, kernel {kernel}")
 
 
 def test_degenerate_sizes(gpu):
@@ -373,7 +374,7 @@ def test_linear_gradients_of_plain_values(gpu):
     mx.check(gpu.autograd.grad(y, wt, to_dev(dy))[0].cpu().numpy(), *mx.product(q(dy.T), q(x.T)))
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 40, 64), (50, 96, 257), (130, 72, 100)])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 64), (50, 96, 257), (130, 72, 100), (300, 77, 330)])
 def test_weight_gradients(gpu, M, N, K):
     rng = np.random.default_rng(K)
     a, B, sb = f16_case(M, N, K, K, 118, 126)
@@ -426,8 +427,10 @@ def test_strides_past_32_bits(gpu):
     a = rng.standard_normal((M, K)).astype(np.float16)
     ad = buf.as_strided((M, K), (ld, 1))
     ad.copy_(to_dev(a))
-    assert tg.mxfp4_select_config(M, N, K, True, lda=ld) == tg.MX_GENERIC
-    mx.check(tg.mxfp4_gemm_f16(ad, *dev_matrix(B, sb)).cpu().numpy(), *mx.product(a.astype(np.float64), mx.values(B, sb)))
+    assert tg.mxfp4_select_config(M, N, K, True, lda=ld) == tg.MX_SKINNY
+    for cfg in (None, tg.MX_GENERIC):
+        c = tg.mxfp4_gemm_f16(ad, *dev_matrix(B, sb), cfg=cfg)
+        mx.check(c.cpu().numpy(), *mx.product(a.astype(np.float64), mx.values(B, sb)))
     q, s, qt, st = tg.mxfp4_quant(ad, "both")
     assert np.array_equal(q.cpu().numpy(), mx.quant(a)[0]) and np.array_equal(qt.cpu().numpy(), mx.quant(a.T.copy())[0])
     out = tg.mxfp4_dequant(q, s, K, out=ad)

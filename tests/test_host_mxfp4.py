@@ -99,6 +99,8 @@ def test_gemm_more_refusals():
     assert gemm_f16(A=A16 + 1) == tg.TGEMM_EALIGN
     assert gemm_f16(cfg=tg.MX_64) == tg.TGEMM_EINVAL_CFG
     assert gemm_f16(cfg=tg.MX_128, lda=65) == tg.TGEMM_EINVAL_CFG
+    assert gemm_f16(cfg=tg.MX_256, A=A16 + 2) == tg.TGEMM_EINVAL_CFG
+    assert gemm_f16(cfg=tg.MX_SKINNY, B=A16 + 8) == tg.TGEMM_EINVAL_CFG
 
 
 def test_kernel_choice():
@@ -120,6 +122,7 @@ def test_kernel_choice():
     assert sel(300, 300, 96, False, ldsa=3) == tg.MX_GENERIC
     assert sel(300, 300, 96, False, SA=A16 + 1) == tg.MX_GENERIC
     assert sel(300, 300, 100, True) == tg.MX_GENERIC      # K no multiple of 8
+    assert sel(100, 300, 101, True, A=A16 + 2, lda=107) == tg.MX_SKINNY
     assert sel(300, 300, 96, True, lda=100) == tg.MX_GENERIC
     assert sel(300, 300, 96, True, A=A16 + 2) == tg.MX_GENERIC
     assert sel(300, 300, 100, False) == tg.MX_64         # codes are whole blocks: any K

@@ -719,7 +719,8 @@ __global__ __launch_bounds__(64 * W) void gemm_mxfp4_skinny(MxGemmArgs g) {
         for (int i = 0; i < LR; ++i) {
           x[c % AHEAD][i] = (half8){0, 0, 0, 0, 0, 0, 0, 0};
           const int m = 4 * i + lblk;
-          if (m < rows && k < g.K) x[c % AHEAD][i] = *(const half8*)((const _Float16*)g.A + (int64_t)(m0 + m) * g.lda + k);
+          if (m < rows && k < g.K)  // (any alignment of A, any K)
+            x[c % AHEAD][i] = __builtin_bit_cast(half8, load8((const _Float16*)g.A + (int64_t)(m0 + m) * g.lda + k, g.K - k));
         }
       };
 #pragma unroll

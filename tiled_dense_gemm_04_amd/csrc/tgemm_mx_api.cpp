@@ -38,13 +38,14 @@ int validate(bool f16_a, int64_t M, int64_t N, int64_t K, const void* A, int64_t
 }
 
 // The fast kernels copy 16-byte chunks (a whole MX block, 16 scales, 8 binary16 values) and
-// address a 256-row operand tile through a 32-bit buffer range.
-bool fast_eligible(bool f16_a, int64_t K, const void* A, int64_t lda, const void* SA, int64_t ldsa, const void* B,
-                   int64_t ldb, const void* SB, int64_t ldsb) {
+// address a 256-row operand tile through a 32-bit buffer range. The skinny kernel takes binary16
+// A of any alignment.
+bool mx_eligible(const void* Q, int64_t ldq, const void* S, int64_t lds) {
   const int64_t cap = 2 * TGEMM_FAST_MAX_LD;  // bytes
-  if (!aligned16(B) || !aligned16(SB) || ldb % 16 != 0 || ldsb % 16 != 0 || ldb > cap || ldsb > cap) return false;
-  if (f16_a) return aligned16(A) && lda % 8 == 0 && K % 8 == 0 && lda <= TGEMM_FAST_MAX_LD;
-  return aligned16(A) && aligned16(SA) && lda % 16 == 0 && ldsa % 16 == 0 && lda <= cap && ldsa <= cap;
+  return aligned16(Q) && aligned16(S) && ldq % 16 == 0 && lds % 16 == 0 && ldq <= cap && lds <= cap;
+}
+bool f16_eligible(int64_t K, const void* A, int64_t lda) {
+  return aligned16(A) && lda % 8 == 0 && K % 8 == 0 && lda <= TGEMM_FAST_MAX_LD;
 }
 
 // Kernel choice of a fast-eligible call, by rounds of workgroups over the 256 compute units. One
@@ -77,8 +78,9 @@ int select(bool f16_a, int64_t M, int64_t N, int64_t K, const void* A, int64_t l
   if (v != TGEMM_OK) return v;
   if (M == 0 || N == 0) return kSelectNoop;
   if (K == 0) return kSelectZeroFill;
-  if (!fast_eligible(f16_a, K, A, lda, SA, ldsa, B, ldb, SB, ldsb)) return tgemm::kMxGeneric;
-  return choose(f16_a, M, N);
+  if (!mx_eligible(B, ldb, SB, ldsb) || (!f16_a && !mx_eligible(A, lda, SA, ldsa))) return tgemm::kMxGeneric;
+  const int cfg = choose(f16_a, M, N);
+  return f16_a && cfg != tgemm::kMxSkinny && !f16_eligible(K, A, lda) ? tgemm::kMxGeneric : cfg;
 }
 
 // Runs the product; force: a kernel index, or -1 for the choice.
@@ -89,9 +91,11 @@ int run(bool f16_a, int force, int64_t M, int64_t N, int64_t K, const void* A, i
   if (cfg == kSelectNoop) return TGEMM_OK;
   if (cfg < 0 && cfg != kSelectZeroFill) return cfg;
   if (force >= 0 && cfg != kSelectZeroFill) {
-    if (force != tgemm::kMxGeneric && cfg == tgemm::kMxGeneric) return TGEMM_EINVAL_CFG;
-    if (force == tgemm::kMxSkinny && M > tgemm::kMxSkinnyRows) return TGEMM_EINVAL_CFG;
-    if (force == tgemm::kMx64 && f16_a) return TGEMM_EINVAL_CFG;
+    if (force != tgemm::kMxGeneric) {
+      if (!mx_eligible(B, ldb, SB, ldsb) || (!f16_a && !mx_eligible(A, lda, SA, ldsa))) return TGEMM_EINVAL_CFG;
+      if (force == tgemm::kMxSkinny ? M > tgemm::kMxSkinnyRows : f16_a && !f16_eligible(K, A, lda)) return TGEMM_EINVAL_CFG;
+      if (force == tgemm::kMx64 && f16_a) return TGEMM_EINVAL_CFG;
+    }
     cfg = force;
   }
   const int64_t grid = cfg == tgemm::kMxSkinny

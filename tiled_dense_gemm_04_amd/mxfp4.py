@@ -171,10 +171,31 @@ def mxfp4_gemm(a, scale_a, b, scale_b, c=None, relu: bool = False, stream=None, 
     return c
 
 
+def _padded_rows(x):
+    """x (M, K) with zeros to a multiple of 8 columns, in rows of that length."""
+    import torch
+    M, K = x.shape
+    y = torch.empty((M, -(-K // 8) * 8), dtype=x.dtype, device=x.device)
+    y[:, :K] = x
+    if K % 8:
+        y[:, K:] = 0
+    return y
+
+
 def mxfp4_gemm_f16(a, b, scale_b, c=None, relu: bool = False, stream=None, cfg: int | None = None, library=None):
     """C = ReLU?(a @ W^T) of fp16 a (M, K) and an MXFP4 weight W (N x K values decoded to
-    fp16); c: (M, N) fp16 (allocated if None). ``cfg`` forces a kernel (MX_*)."""
+    fp16); c: (M, N) fp16 (allocated if None). ``cfg`` forces a kernel (MX_*). More than
+    MX_SKINNY_ROWS rows that the fast kernels cannot take (K or the row stride no multiple of 8,
+    a base off 16 bytes) are copied once to rows they can, which costs far less than the generic
+    kernel."""
     M, K, lda = _operand(a, "a")
+    if M > MX_SKINNY_ROWS and cfg is None and K and (K % 8 or lda % 8 or a.data_ptr() % 16):
+        if stream is None:
+            a = _padded_rows(a)
+        else:
+            with _allocating(stream, a.device):
+                a = _padded_rows(a)
+        M, K, lda = _operand(a, "a")
     N, kb, ldb, ldsb, device = _matrix(b, scale_b, "b")
     if -(-K // MX_BLOCK) != kb:
         raise ValueError(f"inner dimensions differ: a has {K} columns, b rows of {kb} blocks")
@@ -230,23 +251,32 @@ def _once():
         raise RuntimeError("the MXFP4 functions have no second derivative (create_graph=True)")
 
 
-def _times_weight(dy, w):
-    """dy @ w (M x N by N x K, rows contiguous) through gemm_f16_ws, as ``matmul`` runs it."""
+def _times_weight(dy, codes, scale, k):
+    """dy @ W (M x N by N x k) with W decoded to fp16, through gemm_f16_ws as ``matmul`` runs it.
+    Sizes that are no multiples of 8 are padded to ones, which the fast GEMM kernels take: W's rows
+    to whole blocks (zero codes) and N with zeros; the result is the part of a wider buffer."""
     import torch
-    (M, N), K, device = dy.shape, w.shape[1], dy.device
-    dx = torch.empty((M, K), dtype=torch.float16, device=device)
+    (M, N), device = dy.shape, dy.device
+    width, n8 = codes.shape[1] * 2, -(-N // 8) * 8
+    if n8 != N or dy.data_ptr() % 16 or (M > 1 and dy.stride(0) % 8):
+        dy = _padded_rows(dy)
+    w = torch.empty((n8, width), dtype=torch.float16, device=device)
+    mxfp4_dequant(codes, scale, width, out=w[:N])
+    if n8 != N:
+        w[N:] = 0
+    dx = torch.empty((M, width), dtype=torch.float16, device=device)
     L, stream = lib(), _stream(None, device)
-    need = L.tgemm_workspace_bytes(0, 0, M, K, N)
+    need = L.tgemm_workspace_bytes(0, 0, M, width, n8)
     ws = None
     if need:  # a captured graph gets a (zeroed) workspace of its own: its replays may overlap other calls
         ws = (torch.zeros(need, dtype=torch.uint8, device=device) if torch.cuda.is_current_stream_capturing()
               else workspace_for(need, device, stream))
-    rc = _call("gemm_f16_ws", (0, 0, M, K, N, dy.data_ptr(), dy.stride(0) if M > 1 else max(1, N), w.data_ptr(),
-                               max(1, K), dx.data_ptr(), max(1, K), 0, ws.data_ptr() if need else None,
+    rc = _call("gemm_f16_ws", (0, 0, M, width, n8, dy.data_ptr(), dy.stride(0) if M > 1 else n8 or 1, w.data_ptr(),
+                               width or 1, dx.data_ptr(), width or 1, 0, ws.data_ptr() if need else None,
                                ws.numel() if need else 0, stream), device)
     if rc != TGEMM_OK:
         raise TgemmError(rc, "gemm_f16_ws")
-    return dx
+    return dx if width == k else dx[:, :k]
 
 
 class _Packed:
@@ -350,6 +380,6 @@ def autograd_functions():
         def backward(ctx, dy):
             _once()
             codes, scale = ctx.saved_tensors
-            return _times_weight(_row_major(dy, "dy"), mxfp4_dequant(codes, scale, ctx.k)), None, None
+            return _times_weight(_row_major(dy, "dy"), codes, scale, ctx.k), None, None
 
     return {"Mxfp4LinearFunction": Mxfp4LinearFunction, "Mxfp4WeightFunction": Mxfp4WeightFunction}
