@@ -10,6 +10,31 @@
 namespace tgemm {
 namespace {
 
+// The descriptors of an operand's k-tiles, one after another: a pointer that moves by a tile (no
+// 64-bit product per tile: the scalar instructions around a copy are what small tiles wait for).
+struct TileStream {
+  const char* p;
+  int64_t step;
+  uint32_t full, last;
+  int left;  // tiles from this one on
+  template <typename Op>
+  __device__ __forceinline__ void init(const Op& op, int nk) {
+    p = op.base;
+    step = op.step;
+    full = op.rng_full;
+    last = op.rng_last;
+    left = nk;
+  }
+  __device__ __forceinline__ bool at_last() const { return left == 1; }
+  // The tile's descriptor (an empty range past the last tile, where p may lie behind the matrix).
+  __device__ __forceinline__ int4v next() {
+    const int4v r = make_rsrc(p, left > 1 ? full : left == 1 ? last : 0u);
+    p += step;
+    --left;
+    return r;
+  }
+};
+
 // 8 waves in two groups of four (one wave of each per SIMD) over a ring of STAGES LDS slots;
 // tile t lives in slot t % STAGES. In every interval between two barriers one group issues
 // MFMAs from registers while the other reads LDS and issues copies:
@@ -20,7 +45,7 @@ namespace {
 //                          by both groups before barrier kt-1); wait for its copies of tile
 //                          kt+1; barrier; MFMAs of tile kt.
 // copy(t, group) issues at least PT0 (group 0) or PT1 (group 1) vector-memory copies of tile t
-// in every call, also past the last tile (empty ranges), so with PT * (STAGES - 2) operations
+// in every call (t = 0, 1, 2, ...), also past the last tile (empty ranges), so with PT * (STAGES - 2) operations
 // left in flight everything a thread copied for tile kt+1 has landed; more copies in a call
 // only make that wait longer. MID adds a barrier between the phases, which measured faster
 // for 256 x 256 tiles with both operands k-contiguous in the binary16 kernel.
