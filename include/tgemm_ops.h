@@ -21,7 +21,7 @@ extern "C" {
  *                E2M1 codes along k, two a byte, the even k in the low half. E2M1 has a sign, two
  *                exponent bits (bias 1) and a fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6. Codes past
  *                K in a row's last block are zero (mxfp4_quant writes them so; the products sum
- *                whole blocks, and it is enough if either operand holds zeros there);
+ *                whole blocks);
  *   scale, lds : R rows of KB bytes (lds >= max(1, KB) bytes), one E8M0 scale per block: byte s
  *                stands for 2^(s - 127), 255 for NaN.
  * The fast kernels take codes and scales 16-byte aligned, with ldq and lds multiples of 16, at
@@ -39,7 +39,8 @@ extern "C" {
  * whose largest magnitude is amax: scale 2^(floor(log2 amax) - 2) (1 for a block of zeros), codes
  * x / scale rounded to nearest, ties to the even code, saturated at 6. A block that holds an
  * infinity or a NaN gets scale byte 255 and zero codes. R == 0 or K == 0 is a no-op. X must be
- * 2-byte aligned; no other alignment is needed. R * ceil(K/32) must be below 2^32.
+ * 2-byte aligned; no other alignment is needed. R * ceil(K/32) may be at
+ * most 2^31 - 128 (also of mxfp4_dequant).
  */
 TGEMM_API int mxfp4_quant(int64_t R, int64_t K, const void* X, int64_t ldx,
                           void* Q, int64_t ldq, void* scale, int64_t lds,
@@ -57,7 +58,8 @@ TGEMM_API int mxfp4_dequant(int64_t R, int64_t K, const void* Q, int64_t ldq, co
  * C = ReLU?(A @ B^T) of two MXFP4 matrices, A (M x K) and B (N x K, a linear layer's weight):
  *   C[i,j] = ReLU?( sum_kb 2^(sa + sb - 254) sum_{k in kb} a[i,k] * b[j,k] ),
  * accumulated in float32 and rounded to binary16 once. M == 0 or N == 0 is a no-op, K == 0 writes
- * C = 0. A NaN scale makes its row (A) or column (B) of C NaN (+0 with relu).
+ * C = 0. A NaN scale makes its row (A) or column (B) of C NaN (+0 with relu). A product of more
+ * than 2^23 - 1 tiles (128 x 128 at the smallest but for up to 256 rows) is TGEMM_EINVAL_DIM.
  */
 TGEMM_API int mxfp4_gemm(int64_t M, int64_t N, int64_t K,
                          const void* A, int64_t lda, const void* scale_a, int64_t ldsa,
@@ -93,7 +95,7 @@ TGEMM_API int mxfp4_gemm_f16(int64_t M, int64_t N, int64_t K, const void* A, int
  *               contents; calls that may overlap in time need different ones.
  * X may be G (same strides, binary16), no other overlap. min(R, C) is at most 32768, max(R, C) at
  * most TGEMM_FAST_MAX_LD, steps 1 .. 64 (else TGEMM_EINVAL_DIM, as for an unknown dtype); stride_x
- * must keep the results apart (TGEMM_EINVAL_LD). An empty batch or matrix is a no-op; a matrix of
+ * is at least (R - 1) * ldx + C (TGEMM_EINVAL_LD). An empty batch or matrix is a no-op; a matrix of
  * zeros gives zeros; one that holds an infinity or a NaN gives NaN in that matrix. X must be
  * 2-byte and G aligned to its type.
  */

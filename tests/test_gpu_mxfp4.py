@@ -443,3 +443,54 @@ def test_no_second_derivative(gpu):
     for y in (tg.Mxfp4LinearFunction.apply(x, w), tg.Mxfp4WeightFunction.apply(x, *tg.mxfp4_quant(w.detach()))):
         with pytest.raises(RuntimeError, match="second derivative"):
             gpu.autograd.grad(y.sum(), x, create_graph=True)
+
+
+@pytest.mark.parametrize("form", ["linear", "weight"])
+def test_captured_step(gpu, form):
+    """Output and gradients captured once (leaves of the capture's own) and replayed on new
+    inputs, with the eager step between the replays."""
+    rng = np.random.default_rng(41)
+    M, N, K = 100, 264, 200
+    wq = tg.mxfp4_quant(to_dev(spread(rng, N, K, -6, 0)))
+
+    def step(x, w, dy):
+        if form == "linear":
+            y = tg.Mxfp4LinearFunction.apply(x, w)
+            return (y.detach(), *gpu.autograd.grad(y, (x, w), dy))
+        y = tg.Mxfp4WeightFunction.apply(x, *wq)
+        return (y.detach(), *gpu.autograd.grad(y, (x,), dy))
+
+    def leaves():
+        return [gpu.zeros(sh, dtype=gpu.float16, device="cuda").requires_grad_(grad)
+                for sh, grad in (((M, K), True), ((N, K), True), ((M, N), False))]
+
+    static = leaves()
+    side = gpu.cuda.Stream()
+    side.wait_stream(gpu.cuda.current_stream())
+    with gpu.cuda.stream(side):
+        step(*leaves())
+    side.synchronize()
+    g = gpu.cuda.CUDAGraph()
+    with gpu.cuda.graph(g, stream=side):
+        out = step(*static)
+    for _ in range(4):
+        eager = leaves()
+        for s, e in zip(static, eager):
+            v = to_dev(spread(rng, *s.shape, -3, 1))
+            s.detach().copy_(v)
+            e.detach().copy_(v)
+        g.replay()
+        gpu.cuda.synchronize()
+        for got, ref in zip(out, step(*eager)):
+            assert gpu.equal(got, ref)
+
+
+def test_weight_of_many_rows(gpu):
+    """More rows than the skinny kernel's launch holds take other tiles."""
+    N = 16 * ((1 << 22) - 1) + 1
+    codes = gpu.full((N, 16), 0x22, dtype=gpu.uint8, device="cuda")            # every value 1
+    scale = gpu.full((N, 16), 127, dtype=gpu.uint8, device="cuda")[:, :1]
+    x = gpu.full((1, 32), 0.5, dtype=gpu.float16, device="cuda")
+    scale[-1] = 128
+    for y in (tg.mxfp4_gemm_f16(x, codes, scale), tg.mxfp4_gemm(*tg.mxfp4_quant(x), codes, scale)):
+        assert bool((y[:, :-1] == 16).all()) and y[0, -1].item() == 32

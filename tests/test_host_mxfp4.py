@@ -141,3 +141,20 @@ def test_python_refusals():
         tg.mxfp4_gemm(q, s, q, s)
     with pytest.raises(TypeError):
         tg.mxfp4_dequant(q.float(), s, 70)
+
+
+def test_launch_limits():
+    """Fewer than 2^32 threads in a launch: 128 blocks per workgroup of 256 threads, 16 rows of
+    the weight per skinny workgroup of up to 1024, tiles of 512 threads."""
+    most = (1 << 31) - 128   # blocks
+    assert quant(R=1 << 26, K=1024, ldx=1024, ldq=512, lds=32) == tg.TGEMM_EINVAL_DIM
+    assert dequant(R=1 << 26, K=1024, ldx=1024, ldq=512, lds=32) == tg.TGEMM_EINVAL_DIM
+    assert (1 << 26) * 32 > most
+    wide = 16 * ((1 << 22) - 1)   # columns of the skinny kernel
+    for f16 in (False, True):
+        assert tg.mxfp4_select_config(1, wide, 32, f16) == tg.MX_SKINNY
+        assert tg.mxfp4_select_config(1, wide + 1, 32, f16) not in (tg.MX_SKINNY, tg.MX_GENERIC)
+    for product in (gemm, gemm_f16):
+        assert product(N=wide + 1, ldc=wide + 1, cfg=tg.MX_SKINNY) == tg.TGEMM_EINVAL_CFG
+        # 2^24 tiles of 128 x 128
+        assert product(M=33, N=(1 << 31) - 1024, ldc=1 << 31, cfg=tg.MX_128) == tg.TGEMM_EINVAL_DIM

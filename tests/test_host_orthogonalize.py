@@ -50,3 +50,12 @@ def test_python_refusals():
         tg.orthogonalize(torch.zeros(4, 4, dtype=torch.bfloat16))
     with pytest.raises(ValueError, match="2-D"):
         tg.orthogonalize(torch.zeros(4, dtype=torch.float16))
+
+
+def test_batch_limits():
+    """Fewer than 2^32 threads in a launch: 512 per 4096 padded values, and the batch itself."""
+    assert tg.orthogonalize_workspace_bytes((1 << 22) - 1, 8, 8) > 0
+    for bad in ((1 << 22, 8, 8), (1 << 21, 256, 256)):
+        with pytest.raises(tg.TgemmError) as e:
+            tg.orthogonalize_workspace_bytes(*bad)
+        assert e.value.code == tg.TGEMM_EINVAL_DIM

@@ -13,7 +13,11 @@ using tgemm::MxGemmArgs;
 
 // The kernels index rows and columns of a tile past the matrix's edge in 32 bits.
 constexpr int64_t kMaxDim = TGEMM_MX_MAX_DIM;
-constexpr int64_t kMaxGrid = (int64_t)1 << 31;
+// The runtime takes fewer than 2^32 threads per launch; the widest kernels here have 512 a
+// workgroup (the skinny one up to 1024).
+constexpr int64_t kMaxGrid = ((int64_t)1 << 23) - 1, kMaxSkinnyN = 16 * (((int64_t)1 << 22) - 1);
+// Blocks along the rows of a matrix that is quantised or decoded: 128 per workgroup of 256 threads.
+constexpr int64_t kMaxBlocks = ((int64_t)1 << 31) - 128;
 
 uintptr_t addr(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 bool aligned16(const void* p) { return (addr(p) & 15u) == 0; }
@@ -58,7 +62,8 @@ int choose(bool f16_a, int64_t M, int64_t N) {
   const int64_t skinny = tgemm::ceil_div(M, tgemm::kMxSkinnyTile) * tgemm::ceil_div(N, 16);
   const int64_t t128 = tgemm::ceil_div(M, 128) * tgemm::ceil_div(N, 128);
   const int64_t t64 = tgemm::ceil_div(M, 64) * tgemm::ceil_div(N, 128);
-  if (M <= 32) return tgemm::kMxSkinny;
+  const bool narrow = N <= kMaxSkinnyN;
+  if (M <= 32 && narrow) return tgemm::kMxSkinny;
   if (f16_a) {
     // up to three rounds of the skinny kernel cost less than one of 128 x 128 tiles, and two
     // rounds of those about one of 256 x 256 (512 tiles: 80 against 85 us; 576: 88 against 67)
@@ -93,15 +98,14 @@ int run(bool f16_a, int force, int64_t M, int64_t N, int64_t K, const void* A, i
   if (force >= 0 && cfg != kSelectZeroFill) {
     if (force != tgemm::kMxGeneric) {
       if (!mx_eligible(B, ldb, SB, ldsb) || (!f16_a && !mx_eligible(A, lda, SA, ldsa))) return TGEMM_EINVAL_CFG;
-      if (force == tgemm::kMxSkinny ? M > tgemm::kMxSkinnyRows : f16_a && !f16_eligible(K, A, lda)) return TGEMM_EINVAL_CFG;
+      if (force == tgemm::kMxSkinny ? M > tgemm::kMxSkinnyRows || N > kMaxSkinnyN : f16_a && !f16_eligible(K, A, lda)) return TGEMM_EINVAL_CFG;
       if (force == tgemm::kMx64 && f16_a) return TGEMM_EINVAL_CFG;
     }
     cfg = force;
   }
-  const int64_t grid = cfg == tgemm::kMxSkinny
-                           ? tgemm::ceil_div(N, 16)
-                           : tgemm::ceil_div(M, tgemm::mx_tile_m(cfg)) * tgemm::ceil_div(N, tgemm::mx_tile_n(cfg));
-  if (grid >= kMaxGrid) return TGEMM_EINVAL_DIM;
+  if (cfg != tgemm::kMxSkinny && cfg != kSelectZeroFill &&
+      tgemm::ceil_div(M, tgemm::mx_tile_m(cfg)) * tgemm::ceil_div(N, tgemm::mx_tile_n(cfg)) > kMaxGrid)
+    return TGEMM_EINVAL_DIM;
   int dev = -1;
   const int d = tgemm::current_device(&dev);
   if (d != TGEMM_OK) return d;
@@ -146,8 +150,7 @@ int mxfp4_quant(int64_t R, int64_t K, const void* X, int64_t ldx, void* Q, int64
   if (X == nullptr || (!rows && !cols)) return TGEMM_ENULL;
   if ((rows && (Q == nullptr || scale == nullptr)) || (cols && (QT == nullptr || scale_t == nullptr))) return TGEMM_ENULL;
   if (addr(X) & 1u) return TGEMM_EALIGN;
-  // blocks along the rows are numbered in 32 bits
-  if (R * blocks(K) >= ((int64_t)1 << 32)) return TGEMM_EINVAL_DIM;
+  if (R * blocks(K) > kMaxBlocks) return TGEMM_EINVAL_DIM;
   int dev = -1;
   const int d = tgemm::current_device(&dev);
   if (d != TGEMM_OK) return d;
@@ -174,7 +177,7 @@ int mxfp4_dequant(int64_t R, int64_t K, const void* Q, int64_t ldq, const void* 
   if (R == 0 || K == 0) return TGEMM_OK;
   if (X == nullptr || Q == nullptr || scale == nullptr) return TGEMM_ENULL;
   if (addr(X) & 1u) return TGEMM_EALIGN;
-  if (R * blocks(K) >= ((int64_t)1 << 32)) return TGEMM_EINVAL_DIM;
+  if (R * blocks(K) > kMaxBlocks) return TGEMM_EINVAL_DIM;
   int dev = -1;
   const int d = tgemm::current_device(&dev);
   if (d != TGEMM_OK) return d;

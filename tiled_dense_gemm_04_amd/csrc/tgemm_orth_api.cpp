@@ -23,10 +23,11 @@ int check_sizes(int64_t batch, int64_t R, int64_t C) {
   if (batch == 0 || R == 0 || C == 0) return TGEMM_OK;
   const int64_t m = round_up(R < C ? R : C, tgemm::kOrthPad), n = round_up(R < C ? C : R, tgemm::kOrthPad);
   if (m > kMaxM || n > TGEMM_FAST_MAX_LD) return TGEMM_EINVAL_DIM;
-  // chunks of eight values of a matrix are numbered in 32 bits, workgroups of a launch in 31
-  const int64_t grid = batch * (m * n / (8 * 512) + 1 + tgemm::kOrthParts);
-  return m * n / 8 >= ((int64_t)1 << 31) || batch >= ((int64_t)1 << 24) || grid >= ((int64_t)1 << 31) ? TGEMM_EINVAL_DIM
-                                                                                                   : TGEMM_OK;
+  // Chunks of eight values of a matrix are numbered in 32 bits; the runtime takes fewer than 2^32
+  // threads per launch (512 a workgroup: orth_start's groups bound the products' tiles, and the
+  // norm has at most 1024 + batch workgroups).
+  if (m * n / 8 >= ((int64_t)1 << 31) || batch >= ((int64_t)1 << 22)) return TGEMM_EINVAL_DIM;
+  return batch * tgemm::ceil_div(m * n, 8 * 512) >= ((int64_t)1 << 23) ? TGEMM_EINVAL_DIM : TGEMM_OK;
 }
 
 // Places the workspace's arrays (each on a 256-byte boundary) from base on; returns its bytes.
