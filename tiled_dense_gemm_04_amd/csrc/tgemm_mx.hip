@@ -100,7 +100,8 @@ __device__ __forceinline__ uint4v load8(const _Float16* p, int n) {
 // Quantiser along the rows. Four lanes per block, eight values (16 bytes) each, NB blocks per
 // group of lanes with all loads issued first; block b of the matrix is block b % KB of row
 // b / KB, so consecutive groups of lanes read consecutive memory. Bound by memory: 2 bytes
-// read and 17/32 written per value.
+// read and 17/32 written per value; 16384 x 4096 takes 30.8 us, 5.5 TB/s, the rate of a plain
+// copy.
 template <int NB>
 __global__ __launch_bounds__(256) void quant_mxfp4_rows(MxQuantArgs q) {
   const uint32_t KB = (uint32_t)((q.K - 1) / kMxBlock + 1);
@@ -137,7 +138,9 @@ __global__ __launch_bounds__(256) void quant_mxfp4_rows(MxQuantArgs q) {
 // rows and two lane swaps, and a row block's one over four neighbouring lanes. The codes of
 // X^T cross the workgroup through LDS ([128 columns][8 blocks of 16 bytes], block j of column
 // c at place j ^ (c / 8) % 8, which spreads the sixteen columns groups written at once over
-// the banks) and leave as 128 contiguous bytes per column.
+// the banks) and leave as 128 contiguous bytes per column. Bound by memory and by the strided
+// rows and columns it is reached through: 16384 x 4096 along the columns 38 us (4.5 TB/s), along
+// both axes 50.5 us (4.1 TB/s; two passes would read X twice and take 69).
 template <bool ROWS>
 __global__ __launch_bounds__(256) void quant_mxfp4_cols(MxQuantArgs q) {
   __shared__ __attribute__((aligned(16))) uint8_t codes[128 * 128];
@@ -221,7 +224,8 @@ __global__ __launch_bounds__(256) void quant_mxfp4_cols(MxQuantArgs q) {
 // Codes and scales to binary16 values, each rounded to nearest even (only scales outside
 // 2^-23 .. 2^13 make values that binary16 does not hold; those past its range become
 // infinite, a scale byte of 255 gives NaN). Four lanes per block, eight values (16 bytes
-// written) each, NB blocks per group of lanes. Bound by memory.
+// written) each, NB blocks per group of lanes. Bound by memory: 16384 x 4096 in 31 to 35 us
+// (4.9 to 5.5 TB/s).
 __device__ __forceinline__ half8 decode8(uint32_t w, uint32_t sb) {
   const float s = scale_f32(sb);
   const half2v a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 0), b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, s, 1);
@@ -278,7 +282,9 @@ __global__ __launch_bounds__(256) void dequant_mxfp4_rows(MxDequantArgs q) {
 // k-tile on wave tiles of 64 x 64 (128 x 128 tiles; a third fewer LDS reads than 64 x 32 tiles over
 // the whole of it) or 64 x 32 (64 x 128 tiles), and the groups' sums are joined at the end. What
 // bounds them is how many bytes a compute unit has on their way: 128 x 128 tiles have room for
-// four slots of 32 KB, 64 x 128 ones for six of 24 KB on twice the compute units.
+// four slots of 32 KB, 64 x 128 ones for six of 24 KB on twice the compute units. 512 x 4096 x
+// 4096: 12.7 us on 64 x 128 tiles (14.6 on 128 x 128); 2048 x 2048 x 4096: 15.4 us on 128 x 128
+// (22.9 on 64 x 128), 2.2 PFLOP/s.
 template <int BM, int STAGES, int PANEL>
 __global__ __launch_bounds__(512) void gemm_mxfp4_small(MxGemmArgs g) {
   constexpr int BN = 128, NW = 8, WN = BM == 128 ? 2 : 4, WTN = BN / WN, FM = 4, FN = WTN / 16;
@@ -410,6 +416,10 @@ constexpr int kMxSmallLds = STAGES * (BM + 128) * 128 + 4 * (BM + 128) * 16;
 // ks takes block 2 (l / 16) + ks of the k-tile on both sides, so its two scales of a row are
 // neighbouring bytes: one 2-byte read, the MFMA picks the byte. Blocks past KB: zero codes, and
 // the scale bytes (whatever the padding holds) are cleared.
+// 8192^3 in 242 us (4.55 PFLOP/s), 4096^3 in 35 to 39. Its MFMAs alone, from registers, take 169
+// us for 8192^3 (power holds the clock at 1.74 GHz), with the loop's barriers 182, the copies and
+// reads alone 150: what bounds it is the matrix pipe's power and the part of the reads that the
+// other group's MFMAs do not cover.
 template <int PANEL>
 __global__ __launch_bounds__(512) void gemm_mxfp4_pp256(MxGemmArgs g) {
   constexpr int BM = 256, BN = 256, WM = 2, WN = 4, NC = 4, WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
@@ -576,7 +586,9 @@ constexpr int kMx256Lds = 4 * 256 * 128 + 3 * 512 * 16;
 // x 32 MFMA needs k 8 (l / 16) .. + 7 of weight row l % 16: one 4-byte LDS read (16 rows of
 // 16 bytes: every bank once) and four conversions with the block's scale, done in the phase
 // in which the other group's MFMAs keep the matrix pipe busy. Scales come 16 bytes a row, which
-// covers 16 k-tiles, in two slots.
+// covers 16 k-tiles, in two slots. 4096^3 in 103 to 110 us on 256 x 256 tiles (8192^3: 798 us,
+// 1.38 PFLOP/s, the rate of the binary16 kernels, which MFMA issue and power bound); 512 x 4096 x
+// 4096 in 41.5 us on 128 x 128 tiles, which wait for their copies.
 // Requirements (host): A, B, SB 16-byte aligned, lda and K multiples of 8, ldb, ldsb of 16.
 template <int BM, int BN, int WM, int WN, int STAGES>
 constexpr int wq_lds_bytes() {
@@ -686,10 +698,13 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f16_mxfp4_pp(MxGemmArgs g) 
 
 // ------------------------------------------------------------------------------------
 // Few rows (single tokens and small batches): bound by reading the weight once for every 64 rows
-// of A. A workgroup owns 16 rows of the weight and up to 64 of A and splits K over its W waves in runs of 512 (16 blocks:
-// one 16-byte load of scales per row, four loads of codes), so all of a wave's loads of a run
-// are in flight at once; the waves' partial sums are added in wave order. Lane l of the weight's
-// fragment holds block l / 16 (of four) of row l % 16, 32 codes.
+// of A, and at these sizes by the latency of a launch and of two dependent trips to memory. A
+// workgroup owns 16 rows of the weight and up to 64 of A and splits K over its W waves in runs of
+// 512 (16 blocks: one 16-byte load of scales per row, four loads of codes), so all of a wave's
+// loads of a run are in flight at once; the waves' partial sums are added in wave order. Lane l of
+// the weight's fragment holds block l / 16 (of four) of row l % 16, 32 codes.
+// 1 x 8192 x 4096: 5.9 us with MXFP4 A, 6.7 with binary16 (a weight of 17.8 MB: 3.0 and 2.7 TB/s,
+// launch included); 1 x 8192 x 8192: 9.3 and 12.2.
 // Codes of A come the same way. Binary16 A meets a block's codes in four MFMAs of 8 k per lane,
 // step j taking k 32 (l / 16) + 8 j .. + 7 on both sides (any order of k will do that both
 // operands share). Loaded straight into that layout, every lane would touch a 64-byte segment
@@ -813,7 +828,9 @@ __global__ __launch_bounds__(64 * W) void gemm_mxfp4_skinny(MxGemmArgs g) {
 // Any alignment, stride and K: 128 x 128 tiles, four waves of 64 x 64, one block of 32 k at a
 // time through a double-buffered LDS tile filled through registers (unaligned loads). Codes of
 // A are decoded without their scale, which multiplies the block's product in float32 together
-// with B's (E8M0 scales leave binary16's range); a binary16 A meets the decoded weight.
+// with B's (E8M0 scales leave binary16's range); a binary16 A meets the decoded weight. Bound by
+// the loads through registers, whose latency one block does not cover: 4096^3 takes 377 us with
+// MXFP4 A and 301 with binary16.
 template <bool F16A>
 __global__ __launch_bounds__(256) void gemm_mxfp4_generic(MxGemmArgs g) {
   constexpr int ROW = 40;  // halves per LDS row: 16-byte aligned, rows spread over the banks

@@ -16,7 +16,8 @@
 //       X'   = diag(P) X + offdiag(P) hi(X).
 //     Rounding then touches off-diagonal values only, which are small and of random sign
 //     (relative error of the result on random 1024 x 1024: 7e-4; 1.7e-3 with A and P rounded
-//     whole, 1.2e-3 to 7e-3 with X in binary16 as well);
+//     whole, 1.2e-3 to 7e-3 with X in binary16 as well; 2.1e-4 is the rounding of the result
+//     itself. Products that read the low halves too would reach that, in 1.6 times the time);
 //   * A and E E are symmetric: only tiles on and above the diagonal are computed, each stored
 //     a second time transposed.
 #include "tgemm_orth.h"
@@ -59,7 +60,8 @@ __device__ __forceinline__ void load_g(const OrthArgs& g, int bt, uint32_t r, ui
 }
 
 // Sums of squares of a matrix, g.nparts partial sums in float64 (squares of float32 values
-// leave float32's range), four chunks of eight values per thread in flight. Bound by reading G.
+// leave float32's range), four chunks of eight values per thread in flight. Bound by reading G:
+// 16 x 512 x 2048 in float32 14.2 us (4.7 TB/s), 4096 x 4096 in binary16 13.8 us.
 __global__ __launch_bounds__(256) void orth_norm(OrthArgs g) {
   __shared__ double w[4];
   const uint32_t part = blockIdx.x % g.nparts, bt = blockIdx.x / g.nparts;
@@ -85,6 +87,7 @@ __global__ __launch_bounds__(256) void orth_norm(OrthArgs g) {
 }
 
 // X_0 = G / (|G| + eps) as two halves, padded with zeros: two chunks of eight values per thread.
+// Bound by memory, 8 bytes per value of float32 G: 16 x 512 x 2048 in 22.6 us (5.9 TB/s).
 __global__ __launch_bounds__(256) void orth_start(OrthArgs g) {
   __shared__ double inv;
   const uint32_t rp = g.tall ? g.np : g.mp, cpr = (g.tall ? g.mp : g.np) / 8;
@@ -124,6 +127,10 @@ __global__ __launch_bounds__(256) void orth_start(OrthArgs g) {
 // ------------------------------------------------------------------------------------
 // The three products of a step, one ping-pong kernel each (tgemm_pingpong.h) on BM x BM
 // tiles of one matrix of the batch; what differs is the operands and the epilogue.
+// 4096 x 4096: Gram 84 us and Square 88 us (136 tiles on and above the diagonal, one per compute
+// unit, 120 units idle; a whole 4096^3 product of the binary16 kernels takes 106), Apply 120 us
+// (1.14 PFLOP/s). 16 x 512 x 2048: 18.1, 11.7 and 38.7 us; Apply moves 142 MB there, 27 us at a
+// copy's rate, and is bound by that and its epilogue.
 enum Product { kGram, kSquare, kApply };
 
 struct OrthStep {
