@@ -3,6 +3,7 @@ here returns before any HIP call)."""
 import os
 import re
 import subprocess
+import sys
 
 import pytest
 
@@ -158,3 +159,14 @@ def test_launch_limits():
         assert product(N=wide + 1, ldc=wide + 1, cfg=tg.MX_SKINNY) == tg.TGEMM_EINVAL_CFG
         # 2^24 tiles of 128 x 128
         assert product(M=33, N=(1 << 31) - 1024, ldc=1 << 31, cfg=tg.MX_128) == tg.TGEMM_EINVAL_DIM
+
+
+def test_library_before_torch():
+    """A program that asks the library for a size or a choice before it imports torch has one HIP
+    runtime in the process: torch's own."""
+    code = ("import tiled_dense_gemm_04_amd as tg\n"
+            "assert tg.orthogonalize_workspace_bytes(1, 64, 64) > 0\n"
+            "import torch\n"
+            "maps = {l.split()[-1] for l in open('/proc/self/maps') if 'libamdhip64' in l}\n"
+            "assert len(maps) == 1, maps\n")
+    subprocess.run([sys.executable, "-c", code], cwd=ROOT, check=True)

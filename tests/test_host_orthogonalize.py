@@ -9,6 +9,8 @@ BIG = 1 << 50
 
 
 def call(batch=2, R=8, C=16, dtype=0, G=A16, ldg=16, sg=128, X=A16, ldx=16, sx=128, steps=5, ws=A16, nbytes=BIG):
+    if nbytes == "short":
+        nbytes = tg.orthogonalize_workspace_bytes(batch, R, C) - 1
     return tg.lib().orthogonalize_f16(batch, R, C, dtype, G, ldg, sg, X, ldx, sx, steps, 3.4445, -4.775, 2.0315, 1.0,
                                       ws, nbytes, None)
 
@@ -23,7 +25,7 @@ def call(batch=2, R=8, C=16, dtype=0, G=A16, ldg=16, sg=128, X=A16, ldx=16, sx=1
     (dict(G=None), tg.TGEMM_ENULL), (dict(X=None), tg.TGEMM_ENULL), (dict(ws=None), tg.TGEMM_ENULL),
     (dict(G=A16 + 1), tg.TGEMM_EALIGN), (dict(G=A16 + 2, dtype=1), tg.TGEMM_EALIGN), (dict(X=A16 + 1), tg.TGEMM_EALIGN),
     (dict(ws=A16 + 128), tg.TGEMM_EALIGN), (dict(nbytes=1000), tg.TGEMM_EWORKSPACE),
-    (dict(nbytes=tg.orthogonalize_workspace_bytes(2, 8, 16) - 1), tg.TGEMM_EWORKSPACE),
+    (dict(nbytes="short"), tg.TGEMM_EWORKSPACE),
     (dict(batch=0, G=None), tg.TGEMM_OK), (dict(R=0, X=None), tg.TGEMM_OK), (dict(C=0, ws=None), tg.TGEMM_OK),
 ])
 def test_refusals(kw, code):

@@ -36,6 +36,7 @@ probe ``tgemm_lds_probe`` (``include/tgemm_stamps.h``).
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -115,6 +116,10 @@ def _load(path: str, stamps: bool) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"{path} is not built; run `python -m tiled_dense_gemm_04_amd.build` "
                           "or __graft_entry__.build()")
+    # torch first: its HIP runtime is then the one this library binds to (loaded the other way
+    # round, the process holds two, and the second finds no usable device)
+    if importlib.util.find_spec("torch") is not None:
+        import torch  # noqa: F401
     L = ctypes.CDLL(path)
     i64, p, i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
     L.gemm_f16.restype = i32
