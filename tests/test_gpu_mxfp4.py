@@ -494,3 +494,20 @@ def test_weight_of_many_rows(gpu):
     scale[-1] = 128
     for y in (tg.mxfp4_gemm_f16(x, codes, scale), tg.mxfp4_gemm(*tg.mxfp4_quant(x), codes, scale)):
         assert bool((y[:, :-1] == 16).all()) and y[0, -1].item() == 32
+
+
+def test_poisoned_copies(gpu):
+    """On the build that fills every LDS copy's destination with NaN bytes first, each kernel's
+    result stays the same bit for bit: no fragment or scale is read before its copy landed."""
+    rng = np.random.default_rng(43)
+    D = tg.debugfill_lib()
+    for M, N, K in ((64, 130, 96), (130, 264, 2080), (300, 520, 1100), (520, 264, 4128)):
+        x = to_dev(spread(rng, M, K, -3, 3))
+        xq, wq = tg.mxfp4_quant(x), tg.mxfp4_quant(to_dev(spread(rng, N, K, -6, 0)))
+        for cfg in CONFIGS:
+            if cfg == tg.MX_SKINNY and M > tg.MX_SKINNY_ROWS:
+                continue
+            log(f"poisoned copies {M}x{N}x{K} kernel {cfg}")
+            assert gpu.equal(tg.mxfp4_gemm(*xq, *wq, cfg=cfg, library=D), tg.mxfp4_gemm(*xq, *wq, cfg=cfg))
+            if cfg != tg.MX_64 and (K % 8 == 0 or cfg in (None, tg.MX_GENERIC, tg.MX_SKINNY)):
+                assert gpu.equal(tg.mxfp4_gemm_f16(x, *wq, cfg=cfg, library=D), tg.mxfp4_gemm_f16(x, *wq, cfg=cfg))

@@ -196,3 +196,13 @@ def test_training_step(gpu):
         mx.check(out.cpu().numpy(), *mx.product(t.astype(np.float64), mx.to_half(wq).astype(np.float64)))
         assert gpu.equal(tg.mxfp4_linear(to_dev(t), codes, scale),
                          tg.mxfp4_gemm(*tg.mxfp4_quant(to_dev(t)), codes, scale))
+
+
+def test_poisoned_copies(gpu):
+    """On the build that fills every LDS copy's destination with NaN bytes first, results stay
+    the same bit for bit (wide and tall, tiles of 128 and of 256)."""
+    rng = np.random.default_rng(44)
+    for shape in ((3, 200, 333), (2, 333, 200), (40, 500, 520), (40, 520, 500)):
+        g = to_dev(rng.standard_normal(shape).astype(np.float32))
+        log(f"poisoned copies {shape}")
+        assert gpu.equal(tg.orthogonalize(g, library=tg.debugfill_lib()), tg.orthogonalize(g))
