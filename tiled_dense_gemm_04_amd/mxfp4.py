@@ -359,10 +359,12 @@ def autograd_functions():
             q = tmp.add(M, N) if need_x else None
             qt = tmp.add(N, M) if need_w else None
             tmp.allocate()
-            kept = ctx.saved_tensors[0].data_ptr()
+            # (the tensor itself, until both products are launched: under saved-tensor hooks, as
+            # checkpointing sets them, it is a copy that nothing else owns)
+            kept, = ctx.saved_tensors
             _packed_quant(dy, q, qt, tmp.base, tmp.base)
-            dx = _packed_gemm(q, tmp.base, ctx.wt, kept, dy.device) if need_x else None
-            dw = _packed_gemm(qt, tmp.base, ctx.xt, kept, dy.device) if need_w else None
+            dx = _packed_gemm(q, tmp.base, ctx.wt, kept.data_ptr(), dy.device) if need_x else None
+            dw = _packed_gemm(qt, tmp.base, ctx.xt, kept.data_ptr(), dy.device) if need_w else None
             return dx, dw
 
     class Mxfp4WeightFunction(torch.autograd.Function):
