@@ -21,9 +21,10 @@ struct OrthArgs {
   int nparts;                            // partial sums of squares per matrix
   float a, b, c, scale;
   // workspace (batch of each): sums of squares, the iterate's high and low halves twice, the
-  // Gram matrix without its diagonal and its diagonal, the polynomial likewise
+  // Gram matrix without its diagonal (high and low half) and its diagonal, the polynomial
+  // likewise
   double* parts;
-  _Float16 *hi[2], *lo[2], *E, *P;
+  _Float16 *hi[2], *lo[2], *E[2], *P[2];
   float *D, *DP;
 };
 

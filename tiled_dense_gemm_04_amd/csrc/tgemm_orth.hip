@@ -5,21 +5,25 @@
 // which drives every singular value of X towards one; the result is scale * X. A tall G keeps
 // its orientation: A = X^T X and X <- a X + X (b A + c A A), so nothing is transposed.
 //
-// The products run on the binary16 MFMAs with float32 sums; what they lose is kept small by
-// where binary16 is used:
-//   * the iterate is held as two halves, hi + lo 2^-11 (22 bits), and only products read hi
-//     alone;
-//   * the diagonals, which dominate A and the polynomial P = a I + b A + c A A once X is near
-//     orthogonal, stay in float32 and out of the products: with A = diag(D) + E,
-//       P_ij = b E_ij + c ((D_i + D_j) E_ij + (E E)_ij)        (i != j, binary16)
-//       P_ii = a + b D_i + c (D_i^2 + (E E)_ii)                (float32)
-//       X'   = diag(P) X + offdiag(P) hi(X).
-//     Rounding then touches off-diagonal values only, which are small and of random sign
-//     (relative error of the result on random 1024 x 1024: 7e-4; 1.7e-3 with A and P rounded
-//     whole, 1.2e-3 to 7e-3 with X in binary16 as well; 2.1e-4 is the rounding of the result
-//     itself. Products that read the low halves too would reach that, in 1.6 times the time);
-//   * A and E E are symmetric: only tiles on and above the diagonal are computed, each stored
-//     a second time transposed.
+// The products run on the binary16 MFMAs with float32 sums, and lose no more than float32
+// products do:
+//   * every matrix between them -- the iterate X, and off the diagonal A and the polynomial
+//     P = a I + b A + c A A -- is held as two halves, hi + lo 2^-11 (22 bits);
+//   * a product runs over its operands' halves three times, hi lo, lo hi, then, with those sums
+//     scaled by 2^-11, hi hi. What is left out, lo lo, is 2^-22 of the terms;
+//   * the diagonals, which dominate A and P once X is near orthogonal, stay in float32 and out of
+//     the products: with A = diag(D) + E,
+//       P_ij = b E_ij + c ((D_i + D_j) E_ij + (E E)_ij)        (i != j)
+//       P_ii = a + b D_i + c (D_i^2 + (E E)_ii)
+//       X'   = diag(P) X + offdiag(P) X.
+//   A and E E are symmetric: only tiles on and above the diagonal are computed, each stored a
+//   second time transposed.
+// Relative errors of the result before its rounding to binary16 (which is 2.1e-4 of it; 5 or 6
+// steps, matrices of 64 x 64 to 512 x 512, emulated in float64): 2e-7 to 9e-7 on random matrices,
+// with or without strong directions, where float32 products lose 1e-6 to 3e-6; 8e-5 on rank one
+// plus 1e-4 of noise, whose small directions the steps draw out of the large one's roundings
+// (float32 products: 3e-4). With the high halves alone in the products (a third of their time)
+// these are 1e-3 and 1.5e-2.
 #include "tgemm_orth.h"
 #include "tgemm_pingpong.h"
 
@@ -126,11 +130,11 @@ __global__ __launch_bounds__(256) void orth_start(OrthArgs g) {
 
 // ------------------------------------------------------------------------------------
 // The three products of a step, one ping-pong kernel each (tgemm_pingpong.h) on BM x BM
-// tiles of one matrix of the batch; what differs is the operands and the epilogue.
-// 4096 x 4096: Gram 84 us and Square 88 us (136 tiles on and above the diagonal, one per compute
-// unit, 120 units idle; a whole 4096^3 product of the binary16 kernels takes 106), Apply 120 us
-// (1.14 PFLOP/s). 16 x 512 x 2048: 18.1, 11.7 and 38.7 us; Apply moves 142 MB there, 27 us at a
-// copy's rate, and is bound by that and its epilogue.
+// tiles of one matrix of the batch; what differs is the operands and the epilogue. Bound by the
+// MFMAs of the three passes: 4096 x 4096: Gram 229 us and Square 241 us (136 tiles on and above the
+// diagonal, one per compute unit, 120 units idle; a whole 4096^3 product of the binary16 kernels
+// takes 106), Apply 318 us (1.30 PFLOP/s). 16 x 512 x 2048: 45.5, 23.0 and 64.0 us, of which Apply's
+// passes are 34 at 1.52 PFLOP/s; its epilogue moves 134 MB, 23 us at a copy's rate.
 enum Product { kGram, kSquare, kApply };
 
 struct OrthStep {
@@ -203,23 +207,36 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
   const int64_t xsz = (int64_t)g.mp * g.np, esz = (int64_t)g.mp * g.mp;
   const _Float16* const hi = g.hi[st.in] + bt * xsz;
   const _Float16* const lo = g.lo[st.in] + bt * xsz;
-  _Float16* const E = g.E + bt * esz;
-  _Float16* const PM = g.P + bt * esz;
+  const _Float16* const E[2] = {g.E[0] + bt * esz, g.E[1] + bt * esz};
   float* const D = g.D + (int64_t)bt * g.mp;
   float* const DP = g.DP + (int64_t)bt * g.mp;
   const int ldx = TALL ? g.mp : g.np;  // the iterate's row length
-  const _Float16* const Aop = P == kGram ? hi : P == kSquare ? E : TALL ? hi : PM;
-  const _Float16* const Bop = P == kGram ? hi : P == kSquare ? E : TALL ? PM : hi;
-  const int lda = P == kGram || (P == kApply && TALL) ? ldx : g.mp;
-  const int ldb = P == kGram || (P == kApply && !TALL) ? ldx : g.mp;
+  const _Float16* const PM[2] = {g.P[0] + bt * esz, g.P[1] + bt * esz};
+  const bool a_is_x = P == kGram || (P == kApply && TALL), b_is_x = P == kGram || (P == kApply && !TALL);
+  const _Float16* const Aop[2] = {a_is_x ? hi : P == kSquare ? E[0] : PM[0], a_is_x ? lo : P == kSquare ? E[1] : PM[1]};
+  const _Float16* const Bop[2] = {b_is_x ? hi : P == kSquare ? E[0] : PM[0], b_is_x ? lo : P == kSquare ? E[1] : PM[1]};
+  const int lda = a_is_x ? ldx : g.mp, ldb = b_is_x ? ldx : g.mp;
 
   OpA opa;
   OpB opb;
-  opa.init_copies(Aop, lda, row0, mvalid, BK, wave, lane);
-  opb.init_copies(Bop, ldb, col0, nvalid, BK, wave, lane);
+  opa.init_copies(Aop[0], lda, row0, mvalid, BK, wave, lane);
+  opb.init_copies(Bop[0], ldb, col0, nvalid, BK, wave, lane);
   const uint32_t a_lds0 = lds_addr(a_lds) + wave * 1024, b_lds0 = lds_addr(b_lds) + wave * 1024;
+  // The k-loop runs over the operands' halves three times: hi lo, lo hi, and, with the sums of
+  // those scaled back, hi hi. (K is a multiple of the k-tile: every tile is whole.)
+  const int64_t a_low = (const char*)Aop[1] - (const char*)Aop[0], b_low = (const char*)Bop[1] - (const char*)Bop[0];
+  const char *a_next = opa.base, *b_next = opb.base + b_low;
+  int ct = 0, pass = 0;  // the tile copied next
   auto copy_tile = [&](int kt, auto) __attribute__((always_inline)) {
-    const int4v ra = opa.rsrc(kt, nk, nk), rb = opb.rsrc(kt, nk, nk);
+    const int4v ra = make_rsrc(a_next, pass < 3 ? opa.rng_full : 0u), rb = make_rsrc(b_next, pass < 3 ? opb.rng_full : 0u);
+    a_next += opa.step;
+    b_next += opb.step;
+    if (++ct == nk) {
+      ct = 0;
+      ++pass;
+      a_next = opa.base + (pass == 1 ? a_low : 0);
+      b_next = opb.base;
+    }
     const int slot = kt % STAGES;
 #pragma unroll
     for (int j = 0; j < OpA::LD; ++j) dma_to_lds(ra, a_lds0 + slot * A_BYTES + j * NW * 1024, opa.off[j]);
@@ -244,14 +261,21 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) sum[i][j] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
+  int low_left = 2 * nk;  // tiles of the passes with a low half
   auto mma_tile = [&]() __attribute__((always_inline)) {
+    if (low_left-- == 0) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) sum[i][j] *= 1.0f / kLo;
+    }
 #pragma unroll
     for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
       for (int fn = 0; fn < FN; ++fn)
         sum[fm][fn] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[fn], fa[fm], sum[fm][fn], 0, 0, 0);
   };
-  pingpong_schedule<STAGES, PT, PT, (A_KMAJ && B_KMAJ && BM == 256)>(wave / 4, nk, copy_tile, read_tile, mma_tile);
+  pingpong_schedule<STAGES, PT, PT, (A_KMAJ && B_KMAJ && BM == 256)>(wave / 4, 3 * nk, copy_tile, read_tile, mma_tile);
   __syncthreads();  // the ring is free for staging
   float4v joined_sum[KG == 2 ? FE : 1][FN];
   if constexpr (KG == 2) join_k_groups<FM, FN>(smem, sum, joined_sum, wave, lane);
@@ -264,9 +288,24 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
   char* const stage = smem + wave * (orth_lds_bytes<BM>() / NW);
   static_assert(ST::BYTES <= orth_lds_bytes<BM>() / NW, "staged tile");
   const int rv = rows - wr0, cv = cols - wc0;
+  // What the high halves of the sums leave, in their place (rounded again: the rounded values
+  // kept from the staging would spill).
+  auto take_low = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int fm = 0; fm < FE; ++fm)
+#pragma unroll
+      for (int fn = 0; fn < FN; ++fn) {
+        asm volatile("" : "+v"(acc[fm][fn]));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = acc[fm][fn][e];
+          acc[fm][fn][e] = (x - (float)(_Float16)x) * kLo;
+        }
+      }
+  };
 
   if constexpr (P == kApply) {
-    // X' = diag(P) X + offdiag(P) hi(X). The old values of kAhead rows of tiles are in flight.
+    // X' = diag(P) X + offdiag(P) X. The old values of kAhead rows of tiles are in flight.
     constexpr int kAhead = FE < 3 ? FE : 3;
     half4 h[kAhead][FN], l[kAhead][FN];
     float dr[kAhead];
@@ -314,23 +353,12 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
       const int64_t o = bt * xsz + (int64_t)wr0 * ldx + wc0;
       store_staged<ST, WTM, false>(stage, lane, g.hi[st.in ^ 1] + o, ldx, rv, cv, 1);
       ST::wave_fence();
-#pragma unroll
-      for (int fm = 0; fm < FE; ++fm)
-#pragma unroll
-        for (int fn = 0; fn < FN; ++fn) {
-          asm volatile("" : "+v"(acc[fm][fn]));  // round again: the rounded values kept from above would spill
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float x = acc[fm][fn][e];
-            acc[fm][fn][e] = (x - (float)(_Float16)x) * kLo;
-          }
-        }
+      take_low();
       ST::template stage<false>(stage, acc, lane);
       ST::wave_fence();
       store_staged<ST, WTM, false>(stage, lane, g.lo[st.in ^ 1] + o, ldx, rv, cv, 1);
     }
   } else {
-    _Float16* const out = P == kGram ? E : PM;
     float* const dout = P == kGram ? D : DP;
     // Row fm of tiles: the diagonal, kept apart in float32, leaves the tile.
     auto split_diagonal = [&](auto fm_c) __attribute__((always_inline)) {
@@ -349,8 +377,8 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
     };
     if constexpr (P == kSquare) {
       // P from E, D and E E; the E values of kAhead rows of tiles are in flight
-      constexpr int kAhead = FE < 3 ? FE : 3;
-      half4 x[kAhead][FN];
+      constexpr int kAhead = 2;  // (three rows spill)
+      half4 h[kAhead][FN], l[kAhead][FN];
       float dr[kAhead];
       float4v dc[FN];
       auto fetch = [&](auto fm_c) __attribute__((always_inline)) {
@@ -358,8 +386,11 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
         const int rr = min(wr0 + 16 * fm + lrow, rows - 1);
         dr[fm % kAhead] = D[rr];
 #pragma unroll
-        for (int fn = 0; fn < FN; ++fn)
-          x[fm % kAhead][fn] = *(const half4*)(E + (int64_t)rr * g.mp + min(wc0 + 16 * fn + 4 * lkg, cols - 4));
+        for (int fn = 0; fn < FN; ++fn) {
+          const int64_t o = (int64_t)rr * g.mp + min(wc0 + 16 * fn + 4 * lkg, cols - 4);
+          h[fm % kAhead][fn] = *(const half4*)(E[0] + o);
+          l[fm % kAhead][fn] = *(const half4*)(E[1] + o);
+        }
       };
 #pragma unroll
       for (int fn = 0; fn < FN; ++fn) dc[fn] = *(const float4v*)(D + min(wc0 + 16 * fn + 4 * lkg, cols - 4));
@@ -373,7 +404,7 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
         for (int fn = 0; fn < FN; ++fn)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float s = acc[fm][fn][e], y = (float)x[fm % kAhead][fn][e];
+            const float s = acc[fm][fn][e], y = joined(h[fm % kAhead][fn][e], l[fm % kAhead][fn][e]);
             acc[fm][fn][e] = r == wc0 + 16 * fn + 4 * lkg + e ? g.a + g.b * d + g.c * (d * d + s)
                                                              : g.b * y + g.c * ((d + dc[fn][e]) * y + s);
           }
@@ -384,15 +415,21 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
     } else {
       static_for<FE>([&](auto fm_c) __attribute__((always_inline)) { split_diagonal(fm_c); });
     }
-    ST::template stage<false>(stage, acc, lane);
-    ST::wave_fence();
-    store_staged<ST, WTM, false>(stage, lane, out + (int64_t)wr0 * g.mp + wc0, g.mp, rv, cv, 1);
-    if (tm != tn) {
-      // the transposed copy: columns of the wave's tile become rows, through LDS at WTM halves
-      // and 16 bytes a column (the pad moves neighbouring columns to other banks)
+    // One half of the tile, and off the diagonal its transpose: columns of the wave's tile become
+    // rows, through LDS at WTM halves and 16 bytes a column (the pad moves neighbouring columns to
+    // other banks).
+    auto write = [&](_Float16* out) __attribute__((always_inline)) {
+      ST::template stage<false>(stage, acc, lane);
+      ST::wave_fence();
+      store_staged<ST, WTM, false>(stage, lane, out + (int64_t)wr0 * g.mp + wc0, g.mp, rv, cv, 1);
+      ST::wave_fence();
+      if (tm == tn) return;
       constexpr int PITCH = WTM * 2 + 16;
       static_assert(WTN * PITCH <= orth_lds_bytes<BM>() / NW, "transposed tile");
-      ST::wave_fence();
+#pragma unroll
+      for (int fm = 0; fm < FE; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn) asm volatile("" : "+v"(acc[fm][fn]));  // (rounded again, as in take_low)
 #pragma unroll
       for (int fm = 0; fm < FE; ++fm)
 #pragma unroll
@@ -408,7 +445,12 @@ __global__ __launch_bounds__(512) void orth_product(OrthArgs g, OrthStep st) {
         const half8 v = *(const TG_LDS half8*)(stage + c * PITCH + ch * 16);
         if (c < cv && 8 * ch < rv) *(half8*)(out + (int64_t)(wc0 + c) * g.mp + wr0 + 8 * ch) = v;
       }
-    }
+      ST::wave_fence();
+    };
+    _Float16* const* const out = P == kGram ? g.E : g.P;
+    write(out[0] + bt * esz);
+    take_low();
+    write(out[1] + bt * esz);
   }
 }
 

@@ -44,8 +44,10 @@ int64_t place(OrthArgs& g, char* base) {
     g.hi[i] = reinterpret_cast<_Float16*>(take(x));
     g.lo[i] = reinterpret_cast<_Float16*>(take(x));
   }
-  g.E = reinterpret_cast<_Float16*>(take(b * m * m * 2));
-  g.P = reinterpret_cast<_Float16*>(take(b * m * m * 2));
+  for (int i = 0; i < 2; ++i) {
+    g.E[i] = reinterpret_cast<_Float16*>(take(b * m * m * 2));
+    g.P[i] = reinterpret_cast<_Float16*>(take(b * m * m * 2));
+  }
   g.D = reinterpret_cast<float*>(take(b * m * 4));
   g.DP = reinterpret_cast<float*>(take(b * m * 4));
   return at;

@@ -51,7 +51,7 @@ def orthogonalize(g, steps: int = 5, scale: float = 1.0, out=None, coefficients=
                   stream=None, library=None):
     """scale * NS(g) as fp16 for fp16 or fp32 g: one matrix (R, C) or a stack (batch, R, C), each
     divided by its Frobenius norm and run through ``steps`` Newton-Schulz products with
-    ``coefficients``. ``out``: fp16, g's shape (allocated if None; g itself if it is fp16).
+    ``coefficients``, to what float32 products give rounded once. ``out``: fp16, g's shape (allocated if None; g itself if it is fp16).
     ``workspace``: a uint8 device tensor of orthogonalize_workspace_bytes(batch, R, C), 256-byte
     aligned (allocated for the call if None)."""
     import torch
