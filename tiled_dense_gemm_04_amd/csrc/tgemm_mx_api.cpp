@@ -58,8 +58,9 @@ bool f16_eligible(int64_t K, const void* A, int64_t lda) {
 //                  14 to 15; 256 x 256 28 to 36;
 //   A in binary16: skinny 5, 9, 12; 128 x 128 tiles 42; 256 x 256 84 to 100.
 // The skinny kernel takes 64 rows of A by 16 of the weight per workgroup.
+int64_t skinny_groups(int64_t M, int64_t N) { return tgemm::ceil_div(M, tgemm::kMxSkinnyTile) * tgemm::ceil_div(N, 16); }
 int choose(bool f16_a, int64_t M, int64_t N) {
-  const int64_t skinny = tgemm::ceil_div(M, tgemm::kMxSkinnyTile) * tgemm::ceil_div(N, 16);
+  const int64_t skinny = skinny_groups(M, N);
   const int64_t t128 = tgemm::ceil_div(M, 128) * tgemm::ceil_div(N, 128);
   const int64_t t64 = tgemm::ceil_div(M, 64) * tgemm::ceil_div(N, 128);
   const bool narrow = N <= kMaxSkinnyN;
@@ -75,6 +76,15 @@ int choose(bool f16_a, int64_t M, int64_t N) {
   return t128 <= 256 ? tgemm::kMx128 : tgemm::kMx256;
 }
 
+// Binary16 A that the tiles cannot take (its alignment, stride or K): the skinny kernel up to four
+// rounds of its workgroups, then the generic one. 4 rounds, K = 4095: 61 us (65 x 8192), 74 (100 x
+// 8192), 90 (128 x 8192), 88 (256 x 4096), the generic kernel 101 to 117; K = 1001: 32 to 42 against
+// 30 to 33. 8 rounds: 152 (200 x 8192 x 4095) against 120, 72 (200 x 8192 x 1001) against 32.
+int choose_any_a(int64_t M, int64_t N) {
+  return M <= tgemm::kMxSkinnyRows && N <= kMaxSkinnyN && skinny_groups(M, N) <= 4 * 256 ? tgemm::kMxSkinny
+                                                                                       : tgemm::kMxGeneric;
+}
+
 constexpr int kSelectNoop = -100, kSelectZeroFill = -101;
 
 int select(bool f16_a, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* SA, int64_t ldsa,
@@ -85,7 +95,7 @@ int select(bool f16_a, int64_t M, int64_t N, int64_t K, const void* A, int64_t l
   if (K == 0) return kSelectZeroFill;
   if (!mx_eligible(B, ldb, SB, ldsb) || (!f16_a && !mx_eligible(A, lda, SA, ldsa))) return tgemm::kMxGeneric;
   const int cfg = choose(f16_a, M, N);
-  return f16_a && cfg != tgemm::kMxSkinny && !f16_eligible(K, A, lda) ? tgemm::kMxGeneric : cfg;
+  return f16_a && cfg != tgemm::kMxSkinny && !f16_eligible(K, A, lda) ? choose_any_a(M, N) : cfg;
 }
 
 // Runs the product; force: a kernel index, or -1 for the choice.

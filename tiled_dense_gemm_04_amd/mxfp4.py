@@ -17,6 +17,7 @@ MX_BLOCK_BYTES = 16
 MX_MAX_DIM = (1 << 31) - 512         # TGEMM_MX_MAX_DIM
 MX_GENERIC, MX_SKINNY, MX_128, MX_256, MX_64 = range(5)   # TGEMM_MX_*
 MX_SKINNY_ROWS = 256
+MX_ALIGNED = 256                     # stands for an aligned pointer where only the choice is asked for
 
 _i64, _p, _i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
 _GEMM = [_i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i32, _p]
@@ -184,23 +185,23 @@ def _padded_rows(x):
 
 def mxfp4_gemm_f16(a, b, scale_b, c=None, relu: bool = False, stream=None, cfg: int | None = None, library=None):
     """C = ReLU?(a @ W^T) of fp16 a (M, K) and an MXFP4 weight W (N x K values decoded to
-    fp16); c: (M, N) fp16 (allocated if None). ``cfg`` forces a kernel (MX_*). More than
-    MX_SKINNY_ROWS rows that the fast kernels cannot take (K or the row stride no multiple of 8,
-    a base off 16 bytes) are copied once to rows they can, which costs far less than the generic
-    kernel."""
+    fp16); c: (M, N) fp16 (allocated if None). ``cfg`` forces a kernel (MX_*). Where the choice
+    falls on tiles that cannot take ``a`` (K or the row stride no multiple of 8, a base off 16
+    bytes), its rows are copied once to ones they can (100 x 8192 x 4095: 47 us against 110 on the
+    generic kernel)."""
     M, K, lda = _operand(a, "a")
-    if M > MX_SKINNY_ROWS and cfg is None and K and (K % 8 or lda % 8 or a.data_ptr() % 16):
-        if stream is None:
-            a = _padded_rows(a)
-        else:
-            with _allocating(stream, a.device):
-                a = _padded_rows(a)
-        M, K, lda = _operand(a, "a")
     N, kb, ldb, ldsb, device = _matrix(b, scale_b, "b")
     if -(-K // MX_BLOCK) != kb:
         raise ValueError(f"inner dimensions differ: a has {K} columns, b rows of {kb} blocks")
     if a.device != device:
         raise ValueError("all operands must be on the same device")
+    if cfg is None and (K % 8 or lda % 8 or a.data_ptr() % 16):
+        k8 = -(-K // 8) * 8
+        if (library or lib()).mxfp4_select_config(1, M, N, k8, MX_ALIGNED, k8, None, 0, b.data_ptr(), ldb,
+                                                  scale_b.data_ptr(), ldsb, MX_ALIGNED, N) in (MX_128, MX_256):
+            with _allocating(stream, device):
+                a = _padded_rows(a)
+            M, K, lda = _operand(a, "a")
     c, ldc = _output(c, M, N, device, stream)
     if M == 1 and lda % 8:  # one row: its stride is only its length (which the fast kernels want padded)
         lda = -(-lda // 8) * 8
