@@ -25,9 +25,10 @@ extern "C" {
  *   scale, lds : R rows of KB bytes (lds >= max(1, KB) bytes), one E8M0 scale per block: byte s
  *                stands for 2^(s - 127), 255 for NaN.
  * The fast kernels take codes and scales 16-byte aligned, with ldq and lds multiples of 16, at
- * most 2 * TGEMM_FAST_MAX_LD bytes; other arguments take the generic kernel with the same results
- * (within float32 summation order). No size may exceed TGEMM_MX_MAX_DIM. Device pointers,
- * ownership, streams and errors as for gemm_f16.
+ * most 2 * TGEMM_FAST_MAX_LD bytes (they read the scales of a row in 16-byte pieces, the last one
+ * whole); the one for few rows takes scales of any alignment and lds. Other arguments take the
+ * generic kernel with the same results (within float32 summation order). No size may exceed
+ * TGEMM_MX_MAX_DIM. Device pointers, ownership, streams and errors as for gemm_f16.
  */
 #define TGEMM_MX_MAX_DIM (TGEMM_MAX_DIM - 512)
 

@@ -729,14 +729,17 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f16_mxfp4_pp(MxGemmArgs g) 
 // the weight's fragment holds block l / 16 (of four) of row l % 16, 32 codes.
 // 1 x 8192 x 4096: 5.9 us with MXFP4 A, 6.7 with binary16 (a weight of 17.8 MB: 3.0 and 2.7 TB/s,
 // launch included); 1 x 8192 x 8192: 9.3 and 12.2.
+// Rows of scales that are not padded to 16 bytes cost a little (1 x 8192 x 3000: 3.7 -> 4.6 us, binary16
+// 4.7 -> 5.3; 8 x 8192 x 8200: 7.9 -> 10.2, 13.4 -> 16.8; the generic kernel 72 to 273).
 // Codes of A come the same way. Binary16 A meets a block's codes in four MFMAs of 8 k per lane,
 // step j taking k 32 (l / 16) + 8 j .. + 7 on both sides (any order of k will do that both
 // operands share). Loaded straight into that layout, every lane would touch a 64-byte segment
 // of its own for 16 bytes of it (13 us for 37 x 3000 x 4096, against 9); so the rows of A are
 // loaded 256 contiguous bytes each, four rows per load, and pass through a part of LDS that
 // belongs to the wave (no barrier; chunk c of row r at place c ^ r, free of bank conflicts).
-// LR: loads that cover the rows of A (4 MT, or one for up to four rows, the others zeros).
-template <int MT, int W, int LR, bool F16A>
+// LR: loads that cover the rows of A (4 MT, or one for up to four rows, the others zeros). PADDED: the
+// rows of scales lie in whole 16-byte pieces.
+template <int MT, int W, int LR, bool F16A, bool PADDED>
 __global__ __launch_bounds__(64 * W) void gemm_mxfp4_skinny(MxGemmArgs g) {
   constexpr int A_BYTES = F16A ? MT * 16 * 256 : 0;              // per wave: 16 MT rows of 128 k
   constexpr int P_BYTES = W * MT * 64 * 16;                      // partial sums, in the same place
@@ -750,6 +753,16 @@ __global__ __launch_bounds__(64 * W) void gemm_mxfp4_skinny(MxGemmArgs g) {
   const int n = min(n0 + lrow, g.N - 1);  // rows past N read the last one, their sums are dropped
   const uint8_t* const brow = g.B + (int64_t)n * g.ldb + lblk * kMxBlockBytes;
   const uint8_t* const srow = g.SB + (int64_t)n * g.ldsb;
+  // The 16 scales of a run, one load; rows that are not padded to 16 bytes have no bytes past KB, so
+  // a lane takes its own four of the last run one by one.
+  auto run_scales = [&](const uint8_t* row, int kb0) __attribute__((always_inline)) {
+    if (PADDED || kb0 + 16 <= g.KB) return load_any<uint4v>(row + kb0);
+    uint4v v = {0, 0, 0, 0};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (kb0 + 4 * c + lblk < g.KB) v[c] = (uint32_t)row[kb0 + 4 * c + lblk] << (8 * lblk);
+    return v;
+  };
   const int runs = (g.KB + 15) / 16;
   char* const a_lds = smem + wave * A_BYTES;
   float4v acc[MT];
@@ -763,7 +776,7 @@ __global__ __launch_bounds__(64 * W) void gemm_mxfp4_skinny(MxGemmArgs g) {
   for (int r = wave; r < runs; r += W) {
     const int kb0 = r * 16;
     uint4v w[4];
-    const uint4v sv = load_any<uint4v>(srow + kb0);
+    const uint4v sv = run_scales(srow, kb0);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       w[c] = (uint4v){0, 0, 0, 0};
@@ -814,7 +827,7 @@ __global__ __launch_bounds__(64 * W) void gemm_mxfp4_skinny(MxGemmArgs g) {
       for (int i = 0; i < MT; ++i) {
         const int m = m0 + min(16 * i + lrow, rows - 1);  // rows past M read the last one
         const uint8_t* const arow = (const uint8_t*)g.A + (int64_t)m * g.lda + (int64_t)(kb0 + lblk) * kMxBlockBytes;
-        const uint4v sa = load_any<uint4v>(g.SA + (int64_t)m * g.ldsa + kb0);
+        const uint4v sa = run_scales(g.SA + (int64_t)m * g.ldsa, kb0);
         uint4v a[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -987,27 +1000,36 @@ hipError_t launch_mx_256(const MxGemmArgs& g, hipStream_t s, int device) {
   return launch_big(gemm_mxfp4_pp256<4>, kMx256Lds, ready, g, s, device);
 }
 
-template <int MT, int W, bool F16A, int LR = 4 * MT>
+template <int MT, int W, bool F16A, int LR, bool PADDED>
 hipError_t launch_skinny_tile(const MxGemmArgs& g, hipStream_t s, int device) {
   static std::atomic<uint64_t> ready{0};
   constexpr int lds = W * MT * (F16A ? 4096 : 1024);
   const dim3 grid((unsigned)ceil_div(g.N, 16), (unsigned)ceil_div(g.M, kMxSkinnyTile));
-  return launch_big(gemm_mxfp4_skinny<MT, W, LR, F16A>, lds, ready, g, s, device, grid, 64 * W);
+  return launch_big(gemm_mxfp4_skinny<MT, W, LR, F16A, PADDED>, lds, ready, g, s, device, grid, 64 * W);
 }
 
 // Eight waves, or sixteen for up to 16 rows where K has more than eight runs of 512 (every run
-// of a wave after its first waits for memory again; more rows need the registers).
-template <bool F16A>
+// of a wave after its first waits for memory again; more rows need the registers, and so do 5 to 16
+// binary16 rows beside scales taken one by one).
+template <bool F16A, bool PADDED>
 hipError_t launch_skinny(const MxGemmArgs& g, hipStream_t s, int device) {
+  const bool deep = g.KB > 8 * 16;
   switch (g.M >= kMxSkinnyTile ? 4 : (g.M + 15) / 16) {
     case 1:
       if (F16A && g.M <= 4)
-        return g.KB > 8 * 16 ? launch_skinny_tile<1, 16, F16A, 1>(g, s, device) : launch_skinny_tile<1, 8, F16A, 1>(g, s, device);
-      return g.KB > 8 * 16 ? launch_skinny_tile<1, 16, F16A>(g, s, device) : launch_skinny_tile<1, 8, F16A>(g, s, device);
-    case 2: return launch_skinny_tile<2, 8, F16A>(g, s, device);
-    case 3: return launch_skinny_tile<3, 8, F16A>(g, s, device);
-    default: return launch_skinny_tile<4, 8, F16A>(g, s, device);
+        return deep ? launch_skinny_tile<1, 16, F16A, 1, PADDED>(g, s, device) : launch_skinny_tile<1, 8, F16A, 1, PADDED>(g, s, device);
+      return deep ? launch_skinny_tile<1, F16A && !PADDED ? 8 : 16, F16A, 4, PADDED>(g, s, device)
+                  : launch_skinny_tile<1, 8, F16A, 4, PADDED>(g, s, device);
+    case 2: return launch_skinny_tile<2, 8, F16A, 8, PADDED>(g, s, device);
+    case 3: return launch_skinny_tile<3, 8, F16A, 12, PADDED>(g, s, device);
+    default: return launch_skinny_tile<4, 8, F16A, 16, PADDED>(g, s, device);
   }
+}
+template <bool F16A>
+hipError_t launch_skinny(const MxGemmArgs& g, hipStream_t s, int device) {
+  auto padded = [](const uint8_t* S, int64_t lds) { return ((reinterpret_cast<uintptr_t>(S) | (uintptr_t)lds) & 15) == 0; };
+  return padded(g.SB, g.ldsb) && (F16A || padded(g.SA, g.ldsa)) ? launch_skinny<F16A, true>(g, s, device)
+                                                              : launch_skinny<F16A, false>(g, s, device);
 }
 
 }  // namespace

@@ -42,14 +42,15 @@ int validate(bool f16_a, int64_t M, int64_t N, int64_t K, const void* A, int64_t
 }
 
 // The fast kernels copy 16-byte chunks (a whole MX block, 16 scales, 8 binary16 values) and
-// address a 256-row operand tile through a 32-bit buffer range. The skinny kernel takes binary16
-// A of any alignment.
-bool mx_eligible(const void* Q, int64_t ldq, const void* S, int64_t lds) {
-  const int64_t cap = 2 * TGEMM_FAST_MAX_LD;  // bytes
-  return aligned16(Q) && aligned16(S) && ldq % 16 == 0 && lds % 16 == 0 && ldq <= cap && lds <= cap;
-}
+// address a 256-row operand tile through a 32-bit buffer range. The skinny kernel takes scales
+// and binary16 A of any alignment.
+bool rows_eligible(const void* p, int64_t ld) { return aligned16(p) && ld % 16 == 0 && ld <= 2 * TGEMM_FAST_MAX_LD; }
 bool f16_eligible(int64_t K, const void* A, int64_t lda) {
   return aligned16(A) && lda % 8 == 0 && K % 8 == 0 && lda <= TGEMM_FAST_MAX_LD;
+}
+bool tiles_eligible(bool f16_a, int64_t K, const void* A, int64_t lda, const void* SA, int64_t ldsa, const void* SB,
+                    int64_t ldsb) {
+  return rows_eligible(SB, ldsb) && (f16_a ? f16_eligible(K, A, lda) : rows_eligible(SA, ldsa));
 }
 
 // Kernel choice of a fast-eligible call, by rounds of workgroups over the 256 compute units. One
@@ -76,13 +77,16 @@ int choose(bool f16_a, int64_t M, int64_t N) {
   return t128 <= 256 ? tgemm::kMx128 : tgemm::kMx256;
 }
 
-// Binary16 A that the tiles cannot take (its alignment, stride or K): the skinny kernel up to four
-// rounds of its workgroups, then the generic one. 4 rounds, K = 4095: 61 us (65 x 8192), 74 (100 x
-// 8192), 90 (128 x 8192), 88 (256 x 4096), the generic kernel 101 to 117; K = 1001: 32 to 42 against
-// 30 to 33. 8 rounds: 152 (200 x 8192 x 4095) against 120, 72 (200 x 8192 x 1001) against 32.
-int choose_any_a(int64_t M, int64_t N) {
-  return M <= tgemm::kMxSkinnyRows && N <= kMaxSkinnyN && skinny_groups(M, N) <= 4 * 256 ? tgemm::kMxSkinny
-                                                                                       : tgemm::kMxGeneric;
+// Binary16 A or scales that the tiles cannot take (their alignment or stride, K): the skinny kernel
+// up to a number of rounds of its workgroups, then the generic one.
+//   A in binary16, 4 rounds: K = 4095: 61 us (65 x 8192), 74 (100 x 8192), 90 (128 x 8192), 88 (256 x
+//   4096), the generic kernel 101 to 117; K = 1001: 32 to 42 against 30 to 33. 8 rounds: 152 (200 x
+//   8192 x 4095) against 120, 72 (200 x 8192 x 1001) against 32.
+//   A in MXFP4, 16 rounds: 109 us (256 x 16384 x 4095), 39 (x 1001), the generic kernel 151 and 42.
+//   32 rounds: 213 (256 x 32768 x 4095) against 181, 79 against 55.
+int choose_any(bool f16_a, int64_t M, int64_t N) {
+  return M <= tgemm::kMxSkinnyRows && N <= kMaxSkinnyN && skinny_groups(M, N) <= (f16_a ? 4 : 16) * 256 ? tgemm::kMxSkinny
+                                                                                                   : tgemm::kMxGeneric;
 }
 
 constexpr int kSelectNoop = -100, kSelectZeroFill = -101;
@@ -93,9 +97,10 @@ int select(bool f16_a, int64_t M, int64_t N, int64_t K, const void* A, int64_t l
   if (v != TGEMM_OK) return v;
   if (M == 0 || N == 0) return kSelectNoop;
   if (K == 0) return kSelectZeroFill;
-  if (!mx_eligible(B, ldb, SB, ldsb) || (!f16_a && !mx_eligible(A, lda, SA, ldsa))) return tgemm::kMxGeneric;
+  if (!rows_eligible(B, ldb) || (!f16_a && !rows_eligible(A, lda))) return tgemm::kMxGeneric;
   const int cfg = choose(f16_a, M, N);
-  return f16_a && cfg != tgemm::kMxSkinny && !f16_eligible(K, A, lda) ? choose_any_a(M, N) : cfg;
+  if (cfg == tgemm::kMxSkinny) return cfg;
+  return tiles_eligible(f16_a, K, A, lda, SA, ldsa, SB, ldsb) ? cfg : choose_any(f16_a, M, N);
 }
 
 // Runs the product; force: a kernel index, or -1 for the choice.
@@ -107,8 +112,10 @@ int run(bool f16_a, int force, int64_t M, int64_t N, int64_t K, const void* A, i
   if (cfg < 0 && cfg != kSelectZeroFill) return cfg;
   if (force >= 0 && cfg != kSelectZeroFill) {
     if (force != tgemm::kMxGeneric) {
-      if (!mx_eligible(B, ldb, SB, ldsb) || (!f16_a && !mx_eligible(A, lda, SA, ldsa))) return TGEMM_EINVAL_CFG;
-      if (force == tgemm::kMxSkinny ? M > tgemm::kMxSkinnyRows || N > kMaxSkinnyN : f16_a && !f16_eligible(K, A, lda)) return TGEMM_EINVAL_CFG;
+      if (!rows_eligible(B, ldb) || (!f16_a && !rows_eligible(A, lda))) return TGEMM_EINVAL_CFG;
+      if (force == tgemm::kMxSkinny ? M > tgemm::kMxSkinnyRows || N > kMaxSkinnyN
+                                    : !tiles_eligible(f16_a, K, A, lda, SA, ldsa, SB, ldsb))
+        return TGEMM_EINVAL_CFG;
       if (force == tgemm::kMx64 && f16_a) return TGEMM_EINVAL_CFG;
     }
     cfg = force;

@@ -4,6 +4,9 @@ Argument marshalling for the mxfp4_* entry points of ``include/tgemm_ops.h``, as
 other wrappers. An MXFP4 matrix of R x K values is a pair (codes, scale) of uint8 device
 tensors: codes (R, 16 ceil(K/32)), two E2M1 codes a byte, zero past K; scale (R, ceil(K/32)),
 E8M0, in rows padded to 16 bytes where this module allocates them (the fast kernels' alignment).
+A copy of such a scale (``clone``, ``contiguous``, a checkpoint) has its rows close together: every
+operator takes it, but a product on the tile kernels lays it out again in every call: a program that
+loads a weight copies it into ``mxfp4_empty``'s tensors.
 """
 from __future__ import annotations
 
@@ -18,6 +21,7 @@ MX_MAX_DIM = (1 << 31) - 512         # TGEMM_MX_MAX_DIM
 MX_GENERIC, MX_SKINNY, MX_128, MX_256, MX_64 = range(5)   # TGEMM_MX_*
 MX_SKINNY_ROWS = 256
 MX_ALIGNED = 256                     # stands for an aligned pointer where only the choice is asked for
+MX_MAX_LDS = 1 << 23                 # the largest row stride of scales and codes in the tile kernels
 
 _i64, _p, _i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
 _GEMM = [_i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _i32, _p]
@@ -153,6 +157,37 @@ def mxfp4_dequant(codes, scale, k: int, out=None, stream=None, library=None):
     return out
 
 
+def _on_tiles(library, *args) -> bool:
+    """Whether a product's choice falls on a tile kernel (args: mxfp4_select_config's)."""
+    return library.mxfp4_select_config(*args) in (MX_64, MX_128, MX_256)
+
+
+def _in_pieces(scale, ld) -> bool:
+    """Scales as the tile kernels take them: rows in whole 16-byte pieces."""
+    return ld % 16 == 0 and scale.data_ptr() % 16 == 0
+
+
+def _worth_laying_out(M, N, kb) -> bool:
+    """Whether a product whose scales are not in pieces takes longer on the generic kernel (about 7
+    us, and 0.75 more per block of 32 k in each round of 128 x 128 tiles) than a copy of the scales
+    and the tiles: 300 x 300 x 132 11 us against 9, 260 15 and 9.5, 516 22 and 11; 4096 x 4096 x 36
+    37 and 13; the copy takes the host another 9 us."""
+    return (kb + 8) * -(-(-(-M // 128) * -(-N // 128)) // 256) >= 24
+
+
+def _laid_out(scale, ld, stream):
+    """(scale, row stride) in rows padded to 16 bytes: itself, or a copy made on the call's stream."""
+    import torch
+    if _in_pieces(scale, ld):
+        return scale, ld
+    rows, kb = scale.shape
+    pad = -(-kb // 16) * 16
+    with _allocating(stream, scale.device):
+        out = torch.empty((rows, pad), dtype=torch.uint8, device=scale.device)
+        out[:, :kb] = scale
+    return out, pad
+
+
 def mxfp4_gemm(a, scale_a, b, scale_b, c=None, relu: bool = False, stream=None, cfg: int | None = None, library=None):
     """C = ReLU?(A @ B^T) of two MXFP4 matrices, A (M x K) and B (N x K); c: (M, N) fp16
     (allocated if None). ``cfg`` forces a kernel (MX_*)."""
@@ -162,6 +197,11 @@ def mxfp4_gemm(a, scale_a, b, scale_b, c=None, relu: bool = False, stream=None, 
         raise ValueError(f"inner dimensions differ: rows of {kb} and {kb2} blocks")
     if device_b != device:
         raise ValueError("all operands must be on the same device")
+    if (cfg is None and not (_in_pieces(scale_a, ldsa) and _in_pieces(scale_b, ldsb)) and _worth_laying_out(M, N, kb)
+            and _on_tiles(library or lib(), 0, M, N, kb * MX_BLOCK, a.data_ptr(), lda, MX_ALIGNED, MX_MAX_LDS,
+                          b.data_ptr(), ldb, MX_ALIGNED, MX_MAX_LDS, MX_ALIGNED, N)):
+        scale_a, ldsa = _laid_out(scale_a, ldsa, stream)
+        scale_b, ldsb = _laid_out(scale_b, ldsb, stream)
     c, ldc = _output(c, M, N, device, stream)
     args = (M, N, kb * MX_BLOCK, a.data_ptr(), lda, scale_a.data_ptr(), ldsa, b.data_ptr(), ldb, scale_b.data_ptr(),
             ldsb, c.data_ptr(), ldc, int(relu), _stream(stream, device))
@@ -188,20 +228,23 @@ def mxfp4_gemm_f16(a, b, scale_b, c=None, relu: bool = False, stream=None, cfg: 
     fp16); c: (M, N) fp16 (allocated if None). ``cfg`` forces a kernel (MX_*). Where the choice
     falls on tiles that cannot take ``a`` (K or the row stride no multiple of 8, a base off 16
     bytes), its rows are copied once to ones they can (100 x 8192 x 4095: 47 us against 110 on the
-    generic kernel)."""
+    generic kernel); and the scales likewise."""
     M, K, lda = _operand(a, "a")
     N, kb, ldb, ldsb, device = _matrix(b, scale_b, "b")
     if -(-K // MX_BLOCK) != kb:
         raise ValueError(f"inner dimensions differ: a has {K} columns, b rows of {kb} blocks")
     if a.device != device:
         raise ValueError("all operands must be on the same device")
-    if cfg is None and (K % 8 or lda % 8 or a.data_ptr() % 16):
+    odd, pieces = K % 8 or lda % 8 or a.data_ptr() % 16, _in_pieces(scale_b, ldsb)
+    if cfg is None and (odd or not pieces) and (pieces or _worth_laying_out(M, N, kb)):
         k8 = -(-K // 8) * 8
-        if (library or lib()).mxfp4_select_config(1, M, N, k8, MX_ALIGNED, k8, None, 0, b.data_ptr(), ldb,
-                                                  scale_b.data_ptr(), ldsb, MX_ALIGNED, N) in (MX_128, MX_256):
-            with _allocating(stream, device):
-                a = _padded_rows(a)
-            M, K, lda = _operand(a, "a")
+        if _on_tiles(library or lib(), 1, M, N, k8, MX_ALIGNED, k8, None, 0, b.data_ptr(), ldb, MX_ALIGNED, MX_MAX_LDS,
+                     MX_ALIGNED, N):
+            if odd:
+                with _allocating(stream, device):
+                    a = _padded_rows(a)
+                M, K, lda = _operand(a, "a")
+            scale_b, ldsb = _laid_out(scale_b, ldsb, stream)
     c, ldc = _output(c, M, N, device, stream)
     if M == 1 and lda % 8:  # one row: its stride is only its length (which the fast kernels want padded)
         lda = -(-lda // 8) * 8
