@@ -74,3 +74,18 @@ def test_kept_block_lives_in_a_checkpoint(calls):
     assert len(products) == 2
     for begin, nbytes, alive in products:
         assert any(lo <= begin and begin + nbytes <= hi for lo, hi in alive)
+
+
+@pytest.mark.parametrize("wrong", [lambda t: t[:-1], lambda t: t.to("meta"), lambda t: t.float(), lambda t: t.repeat_interleave(2)[::2]],
+                         ids=["shorter", "elsewhere", "another type", "strided"])
+def test_a_hook_that_returns_something_else_is_refused(calls, wrong):
+    """The products take addresses: a saved block that is not the forward pass's must not reach them."""
+    seen, _ = calls
+    x = torch.ones(70, 100, dtype=torch.float16, requires_grad=True)
+    w = torch.ones(40, 100, dtype=torch.float16, requires_grad=True)
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: t, wrong):
+        y = linear(x, w)
+    seen.clear()
+    with pytest.raises(RuntimeError, match="saved"):
+        y.backward(torch.ones_like(y))
+    assert not seen

@@ -389,6 +389,7 @@ def autograd_functions():
             kept = cols.allocate()
             rows.allocate()
             ctx.save_for_backward(kept)
+            ctx.kept = kept.shape
             _packed_quant(x, xq, ctx.xt, rows.base, cols.base)
             _packed_quant(w, wq, ctx.wt, rows.base, cols.base)
             return _packed_gemm(xq, rows.base, wq, rows.base, x.device)
@@ -406,6 +407,8 @@ def autograd_functions():
             # (the tensor itself, until both products are launched: under saved-tensor hooks, as
             # checkpointing sets them, it is a copy that nothing else owns)
             kept, = ctx.saved_tensors
+            if (kept.shape, kept.dtype, kept.device, kept.is_contiguous()) != (ctx.kept, torch.uint8, dy.device, True):
+                raise RuntimeError("a saved-tensor hook returned another tensor than the forward pass saved")
             _packed_quant(dy, q, qt, tmp.base, tmp.base)
             dx = _packed_gemm(q, tmp.base, ctx.wt, kept.data_ptr(), dy.device) if need_x else None
             dw = _packed_gemm(qt, tmp.base, ctx.xt, kept.data_ptr(), dy.device) if need_w else None
