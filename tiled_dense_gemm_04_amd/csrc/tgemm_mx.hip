@@ -140,7 +140,9 @@ __global__ __launch_bounds__(256) void quant_mxfp4_rows(MxQuantArgs q) {
 // c at place j ^ (c / 8) % 8, which spreads the sixteen columns groups written at once over
 // the banks) and leave as 128 contiguous bytes per column. Bound by memory and by the strided
 // rows and columns it is reached through: 16384 x 4096 along the columns 36.5 us (4.7 TB/s), along
-// both axes 49.7 us (4.1 TB/s; two passes would read X twice and take 67).
+// both axes 50 to 52 us (4.0 TB/s; two passes would read X twice and take 67). The 13 us between them
+// are the rows' codes and scales, 36 MB in pieces of 64 (half a line, a tile being 128 columns wide)
+// and 4 bytes: 6 us at a copy's rate.
 template <bool ROWS>
 __global__ __launch_bounds__(256) void quant_mxfp4_cols(MxQuantArgs q) {
   __shared__ __attribute__((aligned(16))) uint8_t codes[128 * 128];
@@ -153,7 +155,7 @@ __global__ __launch_bounds__(256) void quant_mxfp4_cols(MxQuantArgs q) {
   const int col = c0 + 8 * cg;
   // Tiles inside the matrix are loaded without checks (4096 x 4096 along both axes: 14.0 -> 13.3
   // us). Columns alone: both row blocks' loads come first (2048 x 1024: 5.2 -> 4.5 us, 16384 x
-  // 4096: 37.4 -> 36.5); the rows' work beside them leaves no registers for that (50 -> 52 us).
+  // 4096: 37.4 -> 36.5); beside the rows' work that measured slower (50 -> 52 us).
   constexpr int AHEAD = ROWS ? 1 : 2;
   uint4v xs[AHEAD][8];
   auto load = [&](int h, bool checked) __attribute__((always_inline)) {
@@ -304,11 +306,12 @@ __global__ __launch_bounds__(256) void dequant_mxfp4_rows(MxDequantArgs q) {
 //
 // Small output grids: the two-group ping-pong (tgemm_pingpong.h). Each group takes half of every
 // k-tile on wave tiles of 64 x 64 (128 x 128 tiles; a third fewer LDS reads than 64 x 32 tiles over
-// the whole of it) or 64 x 32 (64 x 128 tiles), and the groups' sums are joined at the end. What
-// bounds them is how many bytes a compute unit has on their way: 128 x 128 tiles have room for
-// four slots of 32 KB, 64 x 128 ones for six of 24 KB on twice the compute units. 512 x 4096 x
-// 4096: 12.7 us on 64 x 128 tiles (14.6 on 128 x 128); 2048 x 2048 x 4096: 15.4 us on 128 x 128
-// (22.9 on 64 x 128), 2.2 PFLOP/s.
+// the whole of it) or 64 x 32 (64 x 128 tiles), and the groups' sums are joined at the end. 128 x
+// 128 tiles have room for four slots of 32 KB, 64 x 128 ones for six of 24 KB on twice the compute
+// units. 512 x 4096 x 4096: 11.6 to 13 us on 64 x 128 tiles (14.6 on 128 x 128); 2048 x 2048 x 4096:
+// 15.4 us on 128 x 128 (22.9 on 64 x 128), 2.2 PFLOP/s. By K (256 x 4096: 6.3 us at 1001, 11.0 at
+// 4095) a round of 64 x 128 tiles is 4.7 us (launch, first copies, join and stores) and 0.39 a k-tile,
+// whose copies at 118 GB/s are 0.2 and whose MFMAs 0.16: they do not overlap as they should, which is open.
 template <int BM, int STAGES, int PANEL>
 __global__ __launch_bounds__(512) void gemm_mxfp4_small(MxGemmArgs g) {
   constexpr int BN = 128, NW = 8, WN = BM == 128 ? 2 : 4, WTN = BN / WN, FM = 4, FN = WTN / 16;
@@ -440,10 +443,11 @@ constexpr int kMxSmallLds = STAGES * (BM + 128) * 128 + 4 * (BM + 128) * 16;
 // ks takes block 2 (l / 16) + ks of the k-tile on both sides, so its two scales of a row are
 // neighbouring bytes: one 2-byte read, the MFMA picks the byte. Blocks past KB: zero codes, and
 // the scale bytes (whatever the padding holds) are cleared.
-// 8192^3 in 242 us (4.55 PFLOP/s), 4096^3 in 35 to 39. Its MFMAs alone, from registers, take 169
-// us for 8192^3 (power holds the clock at 1.74 GHz), with the loop's barriers 182, the copies and
-// reads alone 150: what bounds it is the matrix pipe's power and the part of the reads that the
-// other group's MFMAs do not cover.
+// 8192^3 in 252 us (4.4 PFLOP/s). Its MFMAs alone, from registers, take 169 us for 8192^3 (power
+// holds the clock at 1.74 GHz), with the loop's barriers 182, the copies and reads alone 150: what
+// bounds it is the matrix pipe's power and the part of the reads that the other group's MFMAs do
+// not cover. 4096^3 in 37 to 38: one round of tiles, whose 16 intervals take 31 at 8192^3's pace; its
+// first copies and its epilogue have nothing to overlap with.
 template <int PANEL>
 __global__ __launch_bounds__(512) void gemm_mxfp4_pp256(MxGemmArgs g) {
   constexpr int BM = 256, BN = 256, WM = 2, WN = 4, NC = 4, WTM = BM / WM, WTN = BN / WN, FM = WTM / 16, FN = WTN / 16;
@@ -611,8 +615,10 @@ constexpr int kMx256Lds = 4 * 256 * 128 + 3 * 512 * 16;
 // 16 bytes: every bank once) and four conversions with the block's scale, done in the phase
 // in which the other group's MFMAs keep the matrix pipe busy. Scales come 16 bytes a row, which
 // covers 16 k-tiles, in two slots. 4096^3 in 103 to 110 us on 256 x 256 tiles (8192^3: 798 us,
-// 1.38 PFLOP/s, the rate of the binary16 kernels, which MFMA issue and power bound); 512 x 4096 x
-// 4096 in 41.5 us on 128 x 128 tiles, which wait for their copies.
+// 1.38 PFLOP/s, the rate of the binary16 kernels, which MFMA issue and power bound). 512 x 4096 x
+// 4096 takes 41.5 us on 128 x 128 tiles: 128 workgroups for 256 compute units, each running 128
+// k-tiles at 0.29 us (K = 1001: 12.7 us). What a k-tile waits for is open; k-tiles of 64 (A's rows in 128-byte pieces
+// instead of 64) measured the same, so it is not the size of the copies' pieces.
 // Requirements (host): A, B, SB 16-byte aligned, lda and K multiples of 8, ldb, ldsb of 16.
 template <int BM, int BN, int WM, int WN, int STAGES>
 constexpr int wq_lds_bytes() {
@@ -722,13 +728,15 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_f16_mxfp4_pp(MxGemmArgs g) 
 
 // ------------------------------------------------------------------------------------
 // Few rows (single tokens and small batches): bound by reading the weight once for every 64 rows
-// of A, and at these sizes by the latency of a launch and of two dependent trips to memory. A
+// of A, and at these sizes by the latency of a launch and of dependent trips to memory (two up to 16
+// rows; four of A's chunks one after another in a run for more than 32 binary16 rows). A
 // workgroup owns 16 rows of the weight and up to 64 of A and splits K over its W waves in runs of
 // 512 (16 blocks: one 16-byte load of scales per row, four loads of codes), so all of a wave's
 // loads of a run are in flight at once; the waves' partial sums are added in wave order. Lane l of
 // the weight's fragment holds block l / 16 (of four) of row l % 16, 32 codes.
-// 1 x 8192 x 4096: 5.9 us with MXFP4 A, 6.7 with binary16 (a weight of 17.8 MB: 3.0 and 2.7 TB/s,
-// launch included); 1 x 8192 x 8192: 9.3 and 12.2.
+// 1 x 8192 x 4096: 6.0 us with MXFP4 A, 7.1 with binary16 (a weight of 17.8 MB: 3.0 and 2.5 TB/s,
+// launch included); 1 x 8192 x 8192: 10.4 and 13.4, of which 3 are binary16 A's way through LDS and
+// the decode; 37 x 3000 x 4096 with binary16 A 9.5, on 188 workgroups.
 // Rows of scales that are not padded to 16 bytes cost a little (1 x 8192 x 3000: 3.7 -> 4.6 us, binary16
 // 4.7 -> 5.3; 8 x 8192 x 8200: 7.9 -> 10.2, 13.4 -> 16.8; the generic kernel 72 to 273).
 // Codes of A come the same way. Binary16 A meets a block's codes in four MFMAs of 8 k per lane,

@@ -131,10 +131,10 @@ __global__ __launch_bounds__(256) void orth_start(OrthArgs g) {
 // ------------------------------------------------------------------------------------
 // The three products of a step, one ping-pong kernel each (tgemm_pingpong.h) on BM x BM
 // tiles of one matrix of the batch; what differs is the operands and the epilogue. Bound by the
-// MFMAs of the three passes: 4096 x 4096: Gram 229 us and Square 241 us (136 tiles on and above the
-// diagonal, one per compute unit, 120 units idle; a whole 4096^3 product of the binary16 kernels
-// takes 106), Apply 318 us (1.30 PFLOP/s). 16 x 512 x 2048: 45.5, 23.0 and 64.0 us, of which Apply's
-// passes are 34 at 1.52 PFLOP/s; its epilogue moves 134 MB, 23 us at a copy's rate.
+// MFMAs of the three passes: 4096 x 4096: Gram 229 to 249 us and Square 241 to 258 (136 tiles on and
+// above the diagonal, one per compute unit, 120 units idle; a whole 4096^3 product of the binary16
+// kernels takes 106), Apply 318 to 330 (1.3 PFLOP/s). 16 x 512 x 2048: 46, 23.5 and 65 us, of which
+// Apply's passes are 34 at 1.52 PFLOP/s; its epilogue moves 134 MB, 23 us at a copy's rate.
 enum Product { kGram, kSquare, kApply };
 
 struct OrthStep {
