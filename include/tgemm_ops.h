@@ -70,11 +70,12 @@ TGEMM_API int mxfp4_gemm(int64_t M, int64_t N, int64_t K,
 /*
  * C = ReLU?(A @ W^T) of binary16 A (M x K, lda elements) and an MXFP4 weight (N x K) decoded to
  * binary16 as mxfp4_dequant does, accumulated in float32. For few rows (single tokens, small
- * batches) a kernel reads the weight once for every 64 rows, with A of any alignment and K; it is
- * taken while ceil(M/64) * ceil(N/16) is at most 768 (1024 for an A that the others cannot take).
- * The other fast kernels also need A 16-byte aligned, lda and K multiples of 8 and lda at most
- * TGEMM_FAST_MAX_LD: past those sizes a caller with other rows of A copies them to ones padded
- * with zeros (100 x 8192 x 4095: 47 us with that copy, 74 without). Otherwise as mxfp4_gemm.
+ * batches) a kernel reads the weight once for every 64 rows, with A of any alignment and K: up to
+ * 32 rows always, up to 256 while ceil(M/64) * ceil(N/16) is at most 768 (1024 for an A or scales
+ * that the others cannot take). The other fast kernels also need A 16-byte aligned, lda and K
+ * multiples of 8 and lda at most TGEMM_FAST_MAX_LD: past those sizes a caller with other rows of A
+ * copies them to ones padded with zeros (100 x 8192 x 4095: 47 us with that copy, 74 without).
+ * Otherwise as mxfp4_gemm.
  */
 TGEMM_API int mxfp4_gemm_f16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
                              const void* B, int64_t ldb, const void* scale_b, int64_t ldsb,
