@@ -162,11 +162,6 @@ def _on_tiles(library, *args) -> bool:
     return library.mxfp4_select_config(*args) in (MX_64, MX_128, MX_256)
 
 
-def _in_pieces(scale, ld) -> bool:
-    """Scales as the tile kernels take them: rows in whole 16-byte pieces."""
-    return ld % 16 == 0 and scale.data_ptr() % 16 == 0
-
-
 def _worth_laying_out(M, N, kb) -> bool:
     """Whether a product whose scales are not in pieces takes longer on the generic kernel (about 7
     us, and 0.75 more per block of 32 k in each round of 128 x 128 tiles) than a copy of the scales
@@ -176,16 +171,18 @@ def _worth_laying_out(M, N, kb) -> bool:
 
 
 def _laid_out(scale, ld, stream):
-    """(scale, row stride) in rows padded to 16 bytes: itself, or a copy made on the call's stream."""
+    """(scale, address, row stride) with rows in whole 16-byte pieces, as the tile kernels take them:
+    itself, or a padded copy made on the call's stream."""
     import torch
-    if _in_pieces(scale, ld):
-        return scale, ld
+    at = scale.data_ptr()
+    if not (ld | at) & 15:
+        return scale, at, ld
     rows, kb = scale.shape
     pad = -(-kb // 16) * 16
     with _allocating(stream, scale.device):
         out = torch.empty((rows, pad), dtype=torch.uint8, device=scale.device)
         out[:, :kb] = scale
-    return out, pad
+    return out, out.data_ptr(), pad
 
 
 def mxfp4_gemm(a, scale_a, b, scale_b, c=None, relu: bool = False, stream=None, cfg: int | None = None, library=None):
@@ -197,14 +194,15 @@ def mxfp4_gemm(a, scale_a, b, scale_b, c=None, relu: bool = False, stream=None, 
         raise ValueError(f"inner dimensions differ: rows of {kb} and {kb2} blocks")
     if device_b != device:
         raise ValueError("all operands must be on the same device")
-    if (cfg is None and not (_in_pieces(scale_a, ldsa) and _in_pieces(scale_b, ldsb)) and _worth_laying_out(M, N, kb)
+    sa, sb = scale_a.data_ptr(), scale_b.data_ptr()
+    if ((sa | ldsa | sb | ldsb) & 15 and cfg is None and _worth_laying_out(M, N, kb)
             and _on_tiles(library or lib(), 0, M, N, kb * MX_BLOCK, a.data_ptr(), lda, MX_ALIGNED, MX_MAX_LDS,
                           b.data_ptr(), ldb, MX_ALIGNED, MX_MAX_LDS, MX_ALIGNED, N)):
-        scale_a, ldsa = _laid_out(scale_a, ldsa, stream)
-        scale_b, ldsb = _laid_out(scale_b, ldsb, stream)
+        scale_a, sa, ldsa = _laid_out(scale_a, ldsa, stream)
+        scale_b, sb, ldsb = _laid_out(scale_b, ldsb, stream)
     c, ldc = _output(c, M, N, device, stream)
-    args = (M, N, kb * MX_BLOCK, a.data_ptr(), lda, scale_a.data_ptr(), ldsa, b.data_ptr(), ldb, scale_b.data_ptr(),
-            ldsb, c.data_ptr(), ldc, int(relu), _stream(stream, device))
+    args = (M, N, kb * MX_BLOCK, a.data_ptr(), lda, sa, ldsa, b.data_ptr(), ldb, sb, ldsb, c.data_ptr(), ldc, int(relu),
+            _stream(stream, device))
     rc = (_call("mxfp4_gemm", args, device, library) if cfg is None
           else _call("mxfp4_gemm_cfg", (cfg, *args), device, library))
     if rc != TGEMM_OK:
@@ -235,8 +233,9 @@ def mxfp4_gemm_f16(a, b, scale_b, c=None, relu: bool = False, stream=None, cfg: 
         raise ValueError(f"inner dimensions differ: a has {K} columns, b rows of {kb} blocks")
     if a.device != device:
         raise ValueError("all operands must be on the same device")
-    odd, pieces = K % 8 or lda % 8 or a.data_ptr() % 16, _in_pieces(scale_b, ldsb)
-    if cfg is None and (odd or not pieces) and (pieces or _worth_laying_out(M, N, kb)):
+    at, sb = a.data_ptr(), scale_b.data_ptr()
+    odd, close = (K | lda) & 7 or at & 15, (sb | ldsb) & 15
+    if (odd or close) and cfg is None and (not close or _worth_laying_out(M, N, kb)):
         k8 = -(-K // 8) * 8
         if _on_tiles(library or lib(), 1, M, N, k8, MX_ALIGNED, k8, None, 0, b.data_ptr(), ldb, MX_ALIGNED, MX_MAX_LDS,
                      MX_ALIGNED, N):
@@ -244,12 +243,12 @@ def mxfp4_gemm_f16(a, b, scale_b, c=None, relu: bool = False, stream=None, cfg: 
                 with _allocating(stream, device):
                     a = _padded_rows(a)
                 M, K, lda = _operand(a, "a")
-            scale_b, ldsb = _laid_out(scale_b, ldsb, stream)
+                at = a.data_ptr()
+            scale_b, sb, ldsb = _laid_out(scale_b, ldsb, stream)
     c, ldc = _output(c, M, N, device, stream)
     if M == 1 and lda % 8:  # one row: its stride is only its length (which the fast kernels want padded)
         lda = -(-lda // 8) * 8
-    args = (M, N, K, a.data_ptr(), lda, b.data_ptr(), ldb, scale_b.data_ptr(), ldsb, c.data_ptr(), ldc, int(relu),
-            _stream(stream, device))
+    args = (M, N, K, at, lda, b.data_ptr(), ldb, sb, ldsb, c.data_ptr(), ldc, int(relu), _stream(stream, device))
     rc = (_call("mxfp4_gemm_f16", args, device, library) if cfg is None
           else _call("mxfp4_gemm_f16_cfg", (cfg, *args), device, library))
     if rc != TGEMM_OK:
