@@ -1,9 +1,10 @@
 /*
  * tgemm_ops.h -- C ABI of libtgemm, the operators beside the GEMMs of tgemm.h: MXFP4 (4-bit
- * microscaled) matrices with their quantiser and products, and the orthogonalisation of a
- * weight's update. The same library and conventions
- * (row-major storage, device pointers owned by the caller, nothing allocated, enqueue-only calls
- * on the given stream, the TGEMM_E* codes of tgemm.h, C not overlapping an input).
+ * microscaled) matrices with their quantiser and products, the orthogonalisation of a weight's
+ * update, the root-mean-square norm with the residual's addition, and an expert layer's routing
+ * (tokens sorted by expert and back) and products. The same library and conventions (row-major
+ * storage, device pointers owned by the caller, nothing allocated, enqueue-only calls on the given
+ * stream, the TGEMM_E* codes of tgemm.h, C not overlapping an input).
  */
 #ifndef TGEMM_OPS_H_
 #define TGEMM_OPS_H_
@@ -13,6 +14,10 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
+
+/* Types of operands that come in more than one. */
+#define TGEMM_DTYPE_F16 0
+#define TGEMM_DTYPE_F32 1
 
 /*
  * MXFP4: microscaled 4-bit floating point (the OCP microscaling format's FP4). An MXFP4 matrix
@@ -106,14 +111,154 @@ TGEMM_API int mxfp4_gemm_f16(int64_t M, int64_t N, int64_t K, const void* A, int
  * zeros gives zeros; one that holds an infinity or a NaN gives NaN in that matrix. X must be
  * 2-byte and G aligned to its type.
  */
-#define TGEMM_DTYPE_F16 0
-#define TGEMM_DTYPE_F32 1
 TGEMM_API int64_t orthogonalize_workspace_bytes(int64_t batch, int64_t R, int64_t C);
 TGEMM_API int orthogonalize_f16(int64_t batch, int64_t R, int64_t C, int dtype,
                                 const void* G, int64_t ldg, int64_t stride_g,
                                 void* X, int64_t ldx, int64_t stride_x,
                                 int steps, float a, float b, float c, float scale,
                                 void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * Root-mean-square norm with the residual's addition, for each row of X (R x K binary16):
+ *   h = round(x + residual) to the residual's type (h = x without a residual),
+ *   y = h * W / sqrt(mean(h^2) + eps),
+ * with float32 sums, to any of
+ *   Y, ldy           : y as binary16;
+ *   Q, ldq and scale : y as E4M3 codes and float32 scales per 1 x 128 block, R x K codes and R x
+ *                      ceil(K/128) scales, contiguous, as gemm_fp8_block takes them. They are made
+ *                      from the float32 y (not from one rounded to binary16): s = amax / 448, q =
+ *                      E4M3(y / s) to nearest even. A block of magnitudes below 2^-100 has codes 0
+ *                      and scale 1; one that holds an infinity or a NaN codes 0 and scale NaN;
+ *   residual_out     : h, in the residual's type (residual itself, with its stride, to update it in
+ *                      place). Y may be X with its stride; no other overlap;
+ *   rstd             : R float32, 1 / sqrt(mean(h^2) + eps), for the backward pass.
+ * Each may be NULL, but not Y and Q both; Q and scale go together and residual_out needs a residual
+ * (else TGEMM_ENULL). residual_dtype and w_dtype are TGEMM_DTYPE_F16 or TGEMM_DTYPE_F32 (residual
+ * NULL: none, its type is not looked at). K is at most TGEMM_NORM_MAX_K, R times the threads of a row
+ * (64 up to K = 1024, 256 up to 4096, 512 up to 8192, else 1024) at most 2^32 - 2048, eps at least 0
+ * (with 0, a row of zeros gives NaN); else TGEMM_EINVAL_DIM. Pointers need the alignment of their type; no stride or K needs more.
+ * Values of h past 1.8e19 (their squares leave float32) give zeros.
+ */
+#define TGEMM_NORM_MAX_K 16384
+TGEMM_API int rmsnorm_f16(int64_t R, int64_t K, const void* X, int64_t ldx,
+                          const void* residual, int64_t ldr, int residual_dtype, const void* W, int w_dtype, float eps,
+                          void* residual_out, int64_t ldro, void* Y, int64_t ldy,
+                          void* Q, int64_t ldq, float* scale, float* rstd, void* stream);
+
+/*
+ * Its gradient, from dY (the gradient of y), H (h as it was stored: residual_out, or X where there
+ * was no residual; h_dtype its type), W, rstd and dH (the gradient of residual_out, of H's type;
+ * NULL: none), with xhat = h rstd:
+ *   dX = rstd (W dY - xhat mean(W dY xhat)) + dH as binary16; dR the same in H's type (the
+ *   residual's gradient; NULL: not wanted); dW = the sum over the rows of dY xhat in W's type (NULL:
+ *   not wanted), float32 partial sums added in a fixed order.
+ *   workspace : 256-byte aligned, rmsnorm_f16_backward_workspace_bytes(R, K) bytes, nothing expected
+ *               of its contents (not needed without dW); calls that may overlap in time need
+ *               different ones.
+ * dX may be dY and dR may be dH or H, with their strides; no other overlap. R == 0 writes dW = 0.
+ */
+TGEMM_API int64_t rmsnorm_f16_backward_workspace_bytes(int64_t R, int64_t K);
+TGEMM_API int rmsnorm_f16_backward(int64_t R, int64_t K, const void* dY, int64_t lddy,
+                                   const void* H, int64_t ldh, int h_dtype, const void* W, int w_dtype,
+                                   const float* rstd, const void* dH, int64_t lddh, void* dX, int64_t lddx,
+                                   void* dR, int64_t lddr, void* dW, void* workspace, int64_t workspace_bytes,
+                                   void* stream);
+
+/*
+ * Tokens sorted by expert. Each of `tokens` tokens has k slots, slot t * k + j with an id in [0,
+ * experts), or any other number for no expert (a padding token, an expert that lives elsewhere):
+ *   ids, ldi : tokens x k ids, TGEMM_INDEX_I32 or _I64, row stride ldi >= max(1, k);
+ *   offsets  : experts + 1 int32: how many slots have a smaller expert. Expert e owns the sorted rows
+ *              offsets[e] .. offsets[e + 1], and offsets[experts] rows are in use;
+ *   order    : tokens * k int32: the slot of each sorted row, in slot order inside an expert, -1 behind
+ *              the last row in use;
+ *   place    : tokens x k int32, contiguous: each slot's sorted row, -1 for a slot of no expert.
+ *   workspace: 256-byte aligned, expert_sort_workspace_bytes(tokens, k, experts) bytes (0 up to 65536
+ *              slots), nothing expected of its contents; calls that may overlap in time need different
+ *              ones.
+ * experts is 1 .. TGEMM_MAX_EXPERTS and tokens * k at most TGEMM_MAX_SLOTS (else TGEMM_EINVAL_DIM).
+ * Deterministic; one launch up to 65536 slots, two beyond.
+ */
+#define TGEMM_INDEX_I32 0
+#define TGEMM_INDEX_I64 1
+#define TGEMM_MAX_EXPERTS 1024
+#define TGEMM_MAX_SLOTS (((int64_t)1 << 26) - 1024)
+TGEMM_API int64_t expert_sort_workspace_bytes(int64_t tokens, int64_t k, int64_t experts);
+TGEMM_API int expert_sort(int64_t tokens, int64_t k, int64_t experts, const void* ids, int64_t ldi, int ids_type,
+                          void* offsets, void* order, void* place, void* workspace, int64_t workspace_bytes,
+                          void* stream);
+
+/*
+ * Rows out to their places: XS[place[t, j], :] = X[t, :] for every slot (X tokens x H, XS rows x H,
+ * binary16). A place outside [0, rows) is skipped, two slots with one place leave one of their rows.
+ * With offsets (experts + 1 int32, as expert_sort writes them) the rows of XS behind
+ * offsets[experts] are set to zero; with NULL they are left as they were.
+ */
+TGEMM_API int expert_gather_f16(int64_t tokens, int64_t k, int64_t rows, int64_t H, const void* X, int64_t ldx,
+                                const void* place, void* XS, int64_t ldxs, const void* offsets, int64_t experts,
+                                void* stream);
+
+/*
+ * And back: OUT[t, :] = sum_j weights[t, j] * Y[place[t, j], :], summed in float32 in the order of j
+ * and rounded to binary16 once; a slot without a place in [0, rows) adds nothing, a token without
+ * any gives zeros. weights: tokens x k, contiguous, of w_dtype (NULL: ones, which makes this the
+ * gradient of expert_gather_f16).
+ */
+TGEMM_API int expert_combine_f16(int64_t tokens, int64_t k, int64_t rows, int64_t H, const void* Y, int64_t ldy,
+                                 const void* place, const void* weights, int w_dtype, void* OUT, int64_t ldo,
+                                 void* stream);
+
+/*
+ * Its gradient: dY[place[t, j], :] = weights[t, j] * dOUT[t, :] and dweights[t, j] = <dOUT[t, :],
+ * Y[place[t, j], :]> (of w_dtype; 0 for a slot of no place), either NULL where it is not wanted (Y is
+ * read for dweights only). Rows of dY of no slot as for expert_gather_f16.
+ */
+TGEMM_API int expert_combine_f16_backward(int64_t tokens, int64_t k, int64_t rows, int64_t H, const void* dOUT,
+                                          int64_t lddo, const void* Y, int64_t ldy, const void* place,
+                                          const void* weights, int w_dtype, void* dY, int64_t lddy, void* dweights,
+                                          const void* offsets, int64_t experts, void* stream);
+
+/*
+ * The experts' products over sorted rows: gemm_f16_grouped where only the device knows the groups.
+ * A (rows x K) and C (rows x N) binary16; expert e owns rows offsets[e] .. offsets[e + 1] (experts + 1
+ * int32 in device memory, not decreasing; values outside [0, rows] are clamped) and the matrix at B +
+ * e * stride_b (elements), N x K with trans_b (a linear layer's weight), else K x N:
+ *   C[p, :] = ReLU?(A[p, :] op(B_e)),
+ * accumulated in float32 and rounded to binary16 once. Rows of C that no expert owns are left as they
+ * were, or, with zero_rest, those from offsets[experts] on are set to zero. K == 0 writes zeros to the
+ * rows that are owned. The tile kernels need A and B 16-byte aligned, lda, ldb, stride_b and their
+ * contiguous dimensions multiples of 8, lda and ldb at most TGEMM_FAST_MAX_LD; other arguments take the
+ * generic kernel. A launch of 2^23 workgroups or more is TGEMM_EINVAL_DIM.
+ */
+TGEMM_API int expert_gemm_f16(int trans_b, int64_t rows, int64_t experts, int64_t N, int64_t K,
+                              const void* A, int64_t lda, const void* offsets, const void* B, int64_t ldb,
+                              int64_t stride_b, void* C, int64_t ldc, int relu, int zero_rest, void* stream);
+
+/*
+ * The products' gradient by the experts' matrices: C_e = A_e^T B_e for every expert, A (rows x M) and
+ * B (rows x N), C_e (M x N binary16) at C + e * stride_c; zeros for an expert of no rows. (With C =
+ * A B_e^T above: dA = dC B_e is expert_gemm_f16 without trans_b, dB_e = dC_e^T A_e.) stride_c is at
+ * least (M - 1) * ldc + N.
+ */
+TGEMM_API int expert_gemm_f16_tn(int64_t rows, int64_t experts, int64_t M, int64_t N, const void* A, int64_t lda,
+                                 const void* B, int64_t ldb, const void* offsets, void* C, int64_t ldc,
+                                 int64_t stride_c, void* stream);
+
+/* Tooling: the experts' products forced to kernel idx (TGEMM_EXPERT_*; TGEMM_EINVAL_CFG for an index
+ * out of range or a kernel that cannot take the arguments), and the kernel a call takes (form 0: rows
+ * with trans_b, 1: rows without, 2: the _tn product, K ignored; -100 for a call that launches nothing). */
+#define TGEMM_EXPERT_GENERIC 0
+#define TGEMM_EXPERT_32 1   /* 32 x 128 tiles; not of the _tn product */
+#define TGEMM_EXPERT_128 2
+#define TGEMM_EXPERT_256 3
+TGEMM_API int expert_gemm_f16_cfg(int idx, int trans_b, int64_t rows, int64_t experts, int64_t N, int64_t K,
+                                  const void* A, int64_t lda, const void* offsets, const void* B, int64_t ldb,
+                                  int64_t stride_b, void* C, int64_t ldc, int relu, int zero_rest, void* stream);
+TGEMM_API int expert_gemm_f16_tn_cfg(int idx, int64_t rows, int64_t experts, int64_t M, int64_t N,
+                                     const void* A, int64_t lda, const void* B, int64_t ldb, const void* offsets,
+                                     void* C, int64_t ldc, int64_t stride_c, void* stream);
+TGEMM_API int expert_gemm_select_config(int form, int64_t rows, int64_t experts, int64_t M, int64_t N, int64_t K,
+                                        const void* A, int64_t lda, const void* B, int64_t ldb, int64_t stride_b);
 
 /* MXFP4 tooling: the two products forced to kernel idx (TGEMM_MX_*; TGEMM_EINVAL_CFG for an
  * index out of range, a fast kernel that cannot take the arguments, or the skinny kernel with M

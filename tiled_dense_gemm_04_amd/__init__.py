@@ -23,8 +23,12 @@ through gemm_f16_ex).
 The operators of ``include/tgemm_ops.h``: MXFP4 (4-bit microscaled) matrices in
 ``mxfp4.py`` (``mxfp4_quant``, ``mxfp4_dequant``, ``mxfp4_gemm``, ``mxfp4_gemm_f16``,
 ``mxfp4_linear``, and the autograd forms ``Mxfp4LinearFunction`` and
-``Mxfp4WeightFunction``), and the Newton-Schulz orthogonalisation of weight updates,
-``orthogonalize``.
+``Mxfp4WeightFunction``), the Newton-Schulz orthogonalisation of weight updates,
+``orthogonalize``, the root-mean-square norm in ``norm.py`` (``rmsnorm``, ``rmsnorm_fp8_block`` and
+``RmsNormFunction``), and an expert layer's routing and products in ``experts.py``
+(``expert_sort``, ``expert_gather``, ``expert_combine``, ``expert_gemm_f16``,
+``expert_gemm_f16_tn`` and the autograd forms ``ExpertGatherFunction``,
+``ExpertCombineFunction`` and ``ExpertGemmFunction``).
 
 The tooling
 twin ``libtgemm_stamps.so`` (``stamps_lib()``, measurement tools only) compiles every config
@@ -678,6 +682,12 @@ def __getattr__(name):
     if name in ("Mxfp4LinearFunction", "Mxfp4WeightFunction"):
         globals().update(mxfp4.autograd_functions())
         return globals()[name]
+    if name == "RmsNormFunction":
+        globals().update(norm.autograd_functions())
+        return globals()[name]
+    if name in ("ExpertGatherFunction", "ExpertCombineFunction", "ExpertGemmFunction"):
+        globals().update(experts.autograd_functions())
+        return globals()[name]
     raise AttributeError(name)
 
 
@@ -823,7 +833,13 @@ from .mxfp4 import (MX_64, MX_128, MX_256, MX_BLOCK, MX_BLOCK_BYTES, MX_GENERIC,
                     mxfp4_select_config)
 from . import newton_schulz  # noqa: E402
 from .newton_schulz import NS_COEFFICIENTS, orthogonalize, orthogonalize_workspace_bytes  # noqa: E402,F401
+from . import norm  # noqa: E402
+from .norm import NORM_MAX_K, rmsnorm, rmsnorm_fp8_block  # noqa: E402,F401
+from . import experts  # noqa: E402
+from .experts import (EXPERT_32, EXPERT_128, EXPERT_256, EXPERT_GENERIC, MAX_EXPERTS, MAX_SLOTS, ExpertOrder,  # noqa: E402,F401
+                      expert_combine, expert_gather, expert_gemm_f16, expert_gemm_f16_tn, expert_gemm_select_config,
+                      expert_sort)
 
-OPS_SIGNATURES = {**mxfp4.SIGNATURES, **newton_schulz.SIGNATURES}
+OPS_SIGNATURES = {**mxfp4.SIGNATURES, **newton_schulz.SIGNATURES, **norm.SIGNATURES, **experts.SIGNATURES}
 # Every symbol include/tgemm_ops.h declares.
 OPS_EXPORTS = tuple(OPS_SIGNATURES)

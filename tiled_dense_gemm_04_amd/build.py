@@ -30,8 +30,11 @@ ARCH = "gfx950"
 
 SOURCES = [os.path.join(CSRC, "tgemm_kernels.hip"), os.path.join(CSRC, "tgemm_fp8.hip"),
            os.path.join(CSRC, "tgemm_mx.hip"), os.path.join(CSRC, "tgemm_orth.hip"),
+           os.path.join(CSRC, "tgemm_norm.hip"), os.path.join(CSRC, "tgemm_expert.hip"),
+           os.path.join(CSRC, "tgemm_expert_gemm.hip"),
            os.path.join(CSRC, "tgemm_api.cpp"),
-           os.path.join(CSRC, "tgemm_mx_api.cpp"), os.path.join(CSRC, "tgemm_orth_api.cpp")]
+           os.path.join(CSRC, "tgemm_mx_api.cpp"), os.path.join(CSRC, "tgemm_orth_api.cpp"),
+           os.path.join(CSRC, "tgemm_norm_api.cpp"), os.path.join(CSRC, "tgemm_expert_api.cpp")]
 
 # Device code: gfx950 only. Packed-fp32 instruction selection is switched off for all
 # device code; -fvisibility=hidden keeps everything but the TGEMM_API entry points local.

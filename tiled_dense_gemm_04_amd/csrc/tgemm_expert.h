@@ -1,0 +1,69 @@
+// tgemm_expert.h -- shared between the kernels of the expert layer (tgemm_expert.hip: tokens sorted
+// by expert and back; tgemm_expert_gemm.hip: the experts' products) and their host side
+// (tgemm_expert_api.cpp).
+#pragma once
+
+#include "tgemm_internal.h"
+
+namespace tgemm {
+
+constexpr int kMaxExperts = 1024;
+
+// Sorting. Slot s = t * k + j holds the id of choice j of token t.
+struct ExpertSortArgs {
+  const void* ids;
+  int64_t ldi;        // elements from one token's ids to the next's
+  int tokens, k, n;   // n = tokens * k
+  int experts, ids_i64;
+  int *offsets, *order, *place;
+  int* counts;        // workspace: kSortSegments x (experts + 1)
+};
+// Up to this many slots one launch sorts (a workgroup per expert); beyond, two, over segments.
+constexpr int kSortOneLaunch = 65536;
+constexpr int kSortSegments = 256;
+hipError_t launch_expert_sort(const ExpertSortArgs& g, hipStream_t s);
+
+// Rows out to their places and back. Any index outside [0, rows) counts as no row.
+struct ExpertRowsArgs {
+  const _Float16 *src, *aux;  // gather: X; combine: Y; its gradient: dout and Y
+  _Float16* dst;
+  int64_t lds_, lda, ldd;     // strides of src, aux and dst, elements
+  const int *place, *offsets; // offsets[experts]: the rows in use (null: rows behind them are left as they were)
+  const void* weights;        // tokens x k, contiguous (null: ones)
+  void* dweights;
+  int tokens, k, rows, H, experts, w_f32;
+};
+hipError_t launch_expert_gather(const ExpertRowsArgs& g, hipStream_t s);
+hipError_t launch_expert_combine(const ExpertRowsArgs& g, hipStream_t s);
+hipError_t launch_expert_combine_grad(const ExpertRowsArgs& g, hipStream_t s);
+
+// Products. Expert e owns rows offsets[e] .. offsets[e + 1] of A (and C, or B):
+//   rows:    C[p, :] = ReLU?(A[p, :] op(B_e)),  B_e N x K (nt) or K x N;
+//   weights: C_e (M x N) = A_e^T B_e over the expert's rows.
+struct ExpertGemmArgs {
+  const _Float16 *A, *B;
+  _Float16* C;
+  const int* offsets;
+  int64_t lda, ldb, stride_b, ldc, stride_c;  // elements
+  int rows, experts, M, N, K;                 // M: columns of A in the weights' form
+  int relu, vec_c, zero_rest;
+  int tiles_m, tiles_n;
+};
+enum ExpertForm { kExpertNT = 0, kExpertNN = 1, kExpertTN = 2 };
+// Kernels of a product, by index (tooling ABI: the _cfg entry point).
+enum ExpertConfig { kExpertGeneric = 0, kExpert32 = 1, kExpert128 = 2, kExpert256 = 3, kExpertConfigs = 4 };
+constexpr int expert_tile_m(int cfg) { return cfg == kExpert256 ? 256 : cfg == kExpert32 ? 32 : 128; }
+constexpr int expert_tile_n(int cfg) { return cfg == kExpert256 ? 256 : 128; }
+// Workgroups of a launch. The rows' form: c rows of an expert need ceil(c / BM) tile rows, so all of
+// them at most rows / BM + the number of experts that have one; and one tile row more where the
+// rows behind the last group are to be zeroed by workgroups of no tile.
+inline int64_t expert_gemm_groups(int cfg, int form, int64_t rows, int64_t experts, int64_t M, int64_t N) {
+  const int64_t tn = ceil_div(N, expert_tile_n(cfg));
+  if (form == kExpertTN) return experts * ceil_div(M, expert_tile_m(cfg)) * tn;
+  return (rows / expert_tile_m(cfg) + (experts < rows ? experts : rows) + 1) * tn;
+}
+hipError_t launch_expert_gemm(int cfg, ExpertForm form, const ExpertGemmArgs& g, hipStream_t s, int device);
+
+int current_device(int* device);  // tgemm_api.cpp
+
+}  // namespace tgemm

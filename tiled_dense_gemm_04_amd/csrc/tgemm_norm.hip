@@ -1,0 +1,327 @@
+// tgemm_norm.hip -- gfx950 kernels of the root-mean-square norm with the residual's addition, its
+// output in binary16 or in E4M3 codes with a scale per 1 x 128 block, and its gradient.
+//
+//   h = round(x + r) to the residual's type (h = x without one), rstd = 1 / sqrt(mean h^2 + eps),
+//   y = h rstd w;  codes of a block: s = max |y| / 448, q = E4M3(y / s).
+//   Backward, xhat = h rstd:  dx = rstd (w dy - xhat mean(w dy xhat)) + dh,  dw = sum_rows dy xhat.
+// h is the value that is stored, so that the backward pass, which reads it, is the gradient of what
+// was computed; y stays in float32 until its one rounding (the codes are not made from a rounded
+// binary16 y). Every sum is float32. Both passes are bound by memory: a row is read once, held in
+// the registers of 64 to 1024 threads, eight consecutive values a chunk, and written once.
+#include "tgemm_device.h"
+#include "tgemm_norm.h"
+#include "tgemm_rows.h"
+
+namespace tgemm {
+namespace {
+
+// Sum over the TPR threads of a row (TPR = 64: a wave of its own; else the workgroup, every thread
+// adding the waves' sums in wave order). `lds` holds a float per wave; a slow wave may still read it
+// when the call returns, so calls that follow each other alternate between two arrays.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* lds) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+  if constexpr (TPR > 64) {
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < TPR / 64; ++w) v += lds[w];
+  }
+  return v;
+}
+
+// Two floats to two E4M3 codes in the low or high half of a word (round to nearest even).
+template <bool HI>
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b, uint32_t old) {
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, (int)old, HI);
+}
+
+// Codes and scale of a lane's eight values of a 1 x 128 block (16 neighbouring lanes). Magnitudes
+// order like their bit patterns, infinities and NaN at the top: such a block gets a NaN scale and
+// zero codes, so that the products it goes to are NaN. A block below 2^-100 counts as zeros (its
+// scale's reciprocal would leave float32).
+__device__ __forceinline__ float block_codes(const float (&y)[8], uint2v& codes) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 16));
+  codes = (uint2v){0u, 0u};
+  if (m >= 0x7F800000u) return __builtin_nanf("");
+  if (m < 0x0D800000u) return 1.0f;  // 2^-100
+  const float s = __uint_as_float(m) / 448.0f, r = 1.0f / s;
+  float q[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    // y / s: the product with the reciprocal, corrected once by its exact residual
+    const float q0 = y[e] * r;
+    q[e] = __builtin_fmaf(__builtin_fmaf(-q0, s, y[e]), r, q0);
+  }
+  codes[0] = e4m3_pair<true>(q[2], q[3], e4m3_pair<false>(q[0], q[1], 0u));
+  codes[1] = e4m3_pair<true>(q[6], q[7], e4m3_pair<false>(q[4], q[5], 0u));
+  return s;
+}
+
+// ------------------------------------------------------------------------------------
+// Forward. TPR threads a row, CH chunks of eight values a thread: thread t holds chunks t + i TPR,
+// so a 1 x 128 block is 16 neighbouring lanes. The residual, x and the weight of a row are all in
+// flight before the one reduction.
+template <int TPR, int CH, int RES>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_rows(NormArgs g) {
+  __shared__ float lds[TPR > 64 ? TPR / 64 : 1];
+  constexpr int RPG = TPR < 256 ? 256 / TPR : 1;  // rows per workgroup
+  const int t = threadIdx.x % TPR;
+  const int64_t row = (int64_t)blockIdx.x * RPG + threadIdx.x / TPR;
+  const bool live = row < g.R;
+  const int64_t r = live ? row : g.R - 1;
+  float h[CH][8], w[CH][8];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int k = 8 * (t + i * TPR), n = g.K - k;
+    half8 x = load_half8(g.X + r * g.ldx + k, n);
+    if constexpr (RES == kResF32) load_float8((const float*)g.Rin + r * g.ldr + k, n, h[i]);
+    if constexpr (RES == kResF16) {
+      const half8 a = load_half8((const _Float16*)g.Rin + r * g.ldr + k, n);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) h[i][e] = (float)a[e];
+    }
+    if (g.w_f32) {
+      load_float8((const float*)g.W + k, n, w[i]);
+    } else {
+      const half8 a = load_half8((const _Float16*)g.W + k, n);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[i][e] = (float)a[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) h[i][e] = RES == kResNone ? (float)x[e] : h[i][e] + (float)x[e];
+  }
+  float ss = 0.0f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int k = 8 * (t + i * TPR), n = g.K - k;
+    if constexpr (RES == kResF16) {
+      half8 a;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        a[e] = (_Float16)h[i][e];
+        h[i][e] = (float)a[e];
+      }
+      if (live && g.Rout != nullptr) store_half8((_Float16*)g.Rout + r * g.ldro + k, a, n);
+    }
+    if constexpr (RES == kResF32) {
+      if (live && g.Rout != nullptr) store_float8((float*)g.Rout + r * g.ldro + k, h[i], n);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[i][e], h[i][e], ss);
+  }
+  const float rstd = 1.0f / sqrtf(row_sum<TPR>(ss, lds) / (float)g.K + g.eps);
+  if (live && t == 0 && g.rstd != nullptr) g.rstd[r] = rstd;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int k = 8 * (t + i * TPR), n = g.K - k;
+    float y[8];
+    half8 a;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[e] = h[i][e] * rstd * w[i][e];
+      a[e] = (_Float16)y[e];
+    }
+    if (live && g.Y != nullptr) store_half8(g.Y + r * g.ldy + k, a, n);
+    if (g.Q != nullptr) {
+      uint2v codes;
+      const float s = block_codes(y, codes);  // (zeros past K)
+      if (live) store_bytes8(g.Q + r * g.ldq + k, codes, n);
+      if (live && n > 0 && t % 16 == 0) g.S[r * g.KB + k / kFp8Block] = s;
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------
+// Backward. A workgroup takes rows blockIdx.x, + gridDim.x, ... (times its rows at once); a thread
+// keeps its columns' weights and its sums of dw in registers over all of them, and the sums leave
+// as one row of partial sums per workgroup, added in a fixed order by norm_weight_grad.
+template <int TPR, int CH, bool H32>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_grad_rows(NormGradArgs g) {
+  __shared__ float lds[2][TPR > 64 ? TPR / 64 : 1];
+  constexpr int RPG = TPR < 256 ? 256 / TPR : 1;
+  const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  float w[CH][8], dw[CH][8];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int k = 8 * (t + i * TPR), n = g.K - k;
+    if (g.w_f32) {
+      load_float8((const float*)g.W + k, n, w[i]);
+    } else {
+      const half8 a = load_half8((const _Float16*)g.W + k, n);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[i][e] = (float)a[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
+  }
+  const float inv_k = 1.0f / (float)g.K;
+  int parity = 0;
+  for (int64_t first = (int64_t)blockIdx.x * RPG; first < g.R; first += (int64_t)gridDim.x * RPG, parity ^= 1) {
+    const bool live = first + sub < g.R;
+    const int64_t r = live ? first + sub : g.R - 1;
+    const float rstd = live ? g.rstd[r] : 0.0f;  // (a row past the last adds nothing to dw)
+    half8 dy[CH];
+    float xh[CH][8];
+    float c = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int k = 8 * (t + i * TPR), n = g.K - k;
+      dy[i] = load_half8(g.dY + r * g.lddy + k, n);
+      if constexpr (H32) {
+        load_float8((const float*)g.H + r * g.ldh + k, n, xh[i]);
+      } else {
+        const half8 a = load_half8((const _Float16*)g.H + r * g.ldh + k, n);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) xh[i][e] = (float)a[e];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        xh[i][e] *= rstd;
+        const float p = (float)dy[i][e] * xh[i][e];
+        if (live) dw[i][e] += p;
+        c = __builtin_fmaf(p, w[i][e], c);
+      }
+    c = row_sum<TPR>(c, lds[parity]) * inv_k;
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int k = 8 * (t + i * TPR), n = g.K - k;
+        float dx[8], dh[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dh[e] = 0.0f;
+        if (g.dH != nullptr) {
+          if constexpr (H32) {
+            load_float8((const float*)g.dH + r * g.lddh + k, n, dh);
+          } else {
+            const half8 a = load_half8((const _Float16*)g.dH + r * g.lddh + k, n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dh[e] = (float)a[e];
+          }
+        }
+        half8 a;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          dx[e] = __builtin_fmaf(rstd, __builtin_fmaf(-xh[i][e], c, (float)dy[i][e] * w[i][e]), dh[e]);
+          a[e] = (_Float16)dx[e];
+        }
+        store_half8(g.dX + r * g.lddx + k, a, n);
+        if (g.dR != nullptr) {
+          if constexpr (H32)
+            store_float8((float*)g.dR + r * g.lddr + k, dx, n);
+          else
+            store_half8((_Float16*)g.dR + r * g.lddr + k, a, n);
+        }
+      }
+    }
+  }
+  if (g.dW == nullptr) return;
+  float* const out = g.parts + (int64_t)blockIdx.x * g.K;
+  if constexpr (RPG > 1) {  // the waves' rows are joined, in wave order
+    __shared__ float join[RPG][CH * 512];
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) join[sub][8 * (t + i * TPR) + e] = dw[i][e];
+    __syncthreads();
+    for (int k = threadIdx.x; k < g.K; k += 256) {
+      float v = join[0][k];
+#pragma unroll
+      for (int w = 1; w < RPG; ++w) v += join[w][k];
+      out[k] = v;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < CH; ++i) store_float8(out + 8 * (t + i * TPR), dw[i], g.K - 8 * (t + i * TPR));
+  }
+}
+
+// dw from the partial sums: 64 columns per workgroup, wave w adds rows w, w + 16, ...; the waves'
+// sums are added in wave order.
+__global__ __launch_bounds__(1024) void norm_weight_grad(NormGradArgs g) {
+  __shared__ float lds[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int k = (int)blockIdx.x * 64 + lane;
+  float v = 0.0f;
+  if (k < g.K) {
+#pragma unroll 8
+    for (int p = wave; p < g.groups; p += 16) v += g.parts[(int64_t)p * g.K + k];
+  }
+  lds[wave][lane] = v;
+  __syncthreads();
+  if (wave != 0 || k >= g.K) return;
+#pragma unroll
+  for (int w = 1; w < 16; ++w) v += lds[w][lane];
+  if (g.w_f32)
+    ((float*)g.dW)[k] = v;
+  else
+    ((_Float16*)g.dW)[k] = (_Float16)v;
+}
+
+// Threads per row and chunks per thread for rows of K values: NORM_SHAPE(TPR, CH).
+#define TGEMM_NORM_SHAPES(NORM_SHAPE, K)       \
+  if (K <= 512) return NORM_SHAPE(64, 1);      \
+  if (K <= 1024) return NORM_SHAPE(64, 2);     \
+  if (K <= 2048) return NORM_SHAPE(256, 1);    \
+  if (K <= 4096) return NORM_SHAPE(256, 2);    \
+  if (K <= 8192) return NORM_SHAPE(512, 2);    \
+  return NORM_SHAPE(1024, 2);
+
+template <int TPR, int CH, int RES>
+hipError_t launch_rows(const NormArgs& g, hipStream_t s) {
+  constexpr int threads = TPR < 256 ? 256 : TPR, rpg = threads / TPR;
+  hipLaunchKernelGGL((rmsnorm_rows<TPR, CH, RES>), dim3((unsigned)ceil_div(g.R, rpg)), dim3(threads), 0, s, g);
+  return hipGetLastError();
+}
+template <int RES>
+hipError_t launch_forward(const NormArgs& g, hipStream_t s) {
+#define TGEMM_NORM_LAUNCH(TPR, CH) (launch_rows<TPR, CH, RES>(g, s))
+  TGEMM_NORM_SHAPES(TGEMM_NORM_LAUNCH, g.K)
+#undef TGEMM_NORM_LAUNCH
+}
+
+template <int TPR, int CH, bool H32>
+hipError_t launch_grad_rows(const NormGradArgs& g, hipStream_t s) {
+  constexpr int threads = TPR < 256 ? 256 : TPR;
+  hipLaunchKernelGGL((rmsnorm_grad_rows<TPR, CH, H32>), dim3((unsigned)g.groups), dim3(threads), 0, s, g);
+  return hipGetLastError();
+}
+template <bool H32>
+hipError_t launch_grad(const NormGradArgs& g, hipStream_t s) {
+#define TGEMM_NORM_LAUNCH(TPR, CH) (launch_grad_rows<TPR, CH, H32>(g, s))
+  TGEMM_NORM_SHAPES(TGEMM_NORM_LAUNCH, g.K)
+#undef TGEMM_NORM_LAUNCH
+}
+
+}  // namespace
+
+int norm_grad_groups(int64_t R, int64_t K) {
+  const int64_t at_once = norm_row_threads(K) == 64 ? 4 : 1, want = ceil_div(R, at_once);
+  return (int)(want < kNormGradGroups ? want : kNormGradGroups);
+}
+
+hipError_t launch_rmsnorm(const NormArgs& g, int residual, hipStream_t s) {
+  switch (residual) {
+    case kResF16: return launch_forward<kResF16>(g, s);
+    case kResF32: return launch_forward<kResF32>(g, s);
+    default: return launch_forward<kResNone>(g, s);
+  }
+}
+
+hipError_t launch_rmsnorm_backward(const NormGradArgs& g, bool h_f32, hipStream_t s) {
+  const hipError_t e = g.groups == 0 ? hipSuccess : h_f32 ? launch_grad<true>(g, s) : launch_grad<false>(g, s);
+  if (e != hipSuccess || g.dW == nullptr) return e;
+  hipLaunchKernelGGL(norm_weight_grad, dim3((unsigned)ceil_div(g.K, 64)), dim3(1024), 0, s, g);
+  return hipGetLastError();
+}
+
+}  // namespace tgemm
