@@ -201,11 +201,12 @@ GROUPS = {"one_row": groups([1]), "empty_first": groups([0, 5, 0, 1], 3), "ragge
           "all_in_one": groups([0, 0, 300, 0]), "none": groups([0, 0, 0], 40), "tiles": groups([256, 128, 32]),
           "wide": groups([257, 300, 511], 1),
           "many": groups(np.random.default_rng(3).integers(0, 4, 200), 9),
+          "rounds": groups([900, 700, 3000, 129, 255]),
           "most": groups(np.random.default_rng(4).integers(0, 2, 1024), 2)}
 SIZES = [(8, 8), (40, 64), (264, 72), (136, 520), (520, 1000)]   # N, K: the tiles' edges, k-tiles of 32 and 64
 ODD = [(1, 1), (129, 65), (258, 131)]
 FORMS = ["nt", "nn", "tn"]
-CONFIGS = [None, tg.EXPERT_GENERIC, tg.EXPERT_32, tg.EXPERT_128, tg.EXPERT_256]
+CONFIGS = [None, tg.EXPERT_GENERIC, tg.EXPERT_32, tg.EXPERT_128, tg.EXPERT_256, tg.EXPERT_TILES]
 
 
 def stack_with_pad(b, pad, gap):
@@ -257,7 +258,7 @@ def test_products_exact(gpu, form, cfg):
     sizes = SIZES if cfg not in (None, tg.EXPERT_GENERIC) else SIZES + ODD
     for name, (offsets, rows) in GROUPS.items():
         for i, (N, K) in enumerate(sizes):
-            if name == "most" and N * K > 3000:
+            if name == "most" and N * K > 3000 or name == "rounds" and N * K < 3000:
                 continue
             print(f"{form} cfg {cfg} {name} {rows} rows N {N} K {K}", flush=True)
             if form == "nn" and cfg not in (None, tg.EXPERT_GENERIC):
@@ -381,7 +382,7 @@ def test_large_offsets_in_a_long_buffer(gpu):
     b = gpu.zeros((2, N, K), dtype=gpu.float16, device="cuda")
     b[1] = 2
     offsets = to_dev(np.array([0, 69000, rows], dtype=np.int32))
-    for cfg in (None, tg.EXPERT_GENERIC, tg.EXPERT_32, tg.EXPERT_128, tg.EXPERT_256):
+    for cfg in CONFIGS:
         c = tg.expert_gemm_f16(a, b, offsets, cfg=cfg)
         assert (c[:-300] == 0).all() and (c[-300:] == 16).all()
     d = tg.expert_gemm_f16_tn(c, a, offsets)

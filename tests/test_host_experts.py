@@ -85,7 +85,7 @@ def gemm(tb=1, rows=100, E=4, N=64, K=32, A=P, lda=32, off=P, B=P, ldb=32, sb=20
     (dict(lda=31), LD), (dict(ldb=31), LD), (dict(tb=0, ldb=63), LD), (dict(ldc=63), LD), (dict(sb=-1), LD),
     (dict(A=None), NULL), (dict(B=None), NULL), (dict(C=None), NULL), (dict(off=None), NULL), (dict(A=P + 1), ALIGN),
     (dict(off=P + 2), ALIGN), (dict(rows=(1 << 31) - 1, N=65536, ldc=65536, sb=1 << 21), DIM),
-    (dict(cfg=4), tg.TGEMM_EINVAL_CFG), (dict(cfg=-1), tg.TGEMM_EINVAL_CFG), (dict(cfg=2, A=P + 2), tg.TGEMM_EINVAL_CFG),
+    (dict(cfg=5), tg.TGEMM_EINVAL_CFG), (dict(cfg=-1), tg.TGEMM_EINVAL_CFG), (dict(cfg=2, A=P + 2), tg.TGEMM_EINVAL_CFG),
     (dict(cfg=1, lda=33), tg.TGEMM_EINVAL_CFG), (dict(cfg=3, sb=2049), tg.TGEMM_EINVAL_CFG),
     (dict(cfg=1, K=0), tg.TGEMM_EINVAL_CFG), (dict(rows=0, A=None), OK), (dict(N=0), OK),
 ])
@@ -113,22 +113,23 @@ def test_kernel_choice():
     for form in ("nt", "nn"):
         assert f(form, 64, 64, N=2048, K=4096) == tg.EXPERT_32
         assert f(form, 1, 64, N=2048, K=4096) == tg.EXPERT_32
-        assert f(form, 16384, 16, N=4096, K=2048) == tg.EXPERT_256
-        assert f(form, 1600, 16, N=512, K=512) == tg.EXPERT_128
+        assert f(form, 16384, 16, N=4096, K=2048) == tg.EXPERT_TILES
+        assert f(form, 1600, 16, N=512, K=512) == tg.EXPERT_TILES
         assert f(form, 64, 8, N=64, K=63) == tg.EXPERT_GENERIC      # K is contiguous in A
         assert f(form, 64, 8, N=64, K=64, A=P + 2) == tg.EXPERT_GENERIC
         assert f(form, 64, 8, N=64, K=64, stride_b=4097) == tg.EXPERT_GENERIC
         assert f(form, 64, 8, N=64, K=0) == tg.EXPERT_GENERIC
         assert f(form, 0, 8, N=64, K=64) == -100 and f(form, 64, 0, N=64, K=64) == DIM
     assert f("nt", 64, 8, N=65, K=64) == tg.EXPERT_32 and f("nn", 64, 8, N=65, K=64) == tg.EXPERT_GENERIC
-    assert f("tn", 8192, 8, M=2048, N=2048) == tg.EXPERT_256 and f("tn", 8192, 8, M=256, N=256) == tg.EXPERT_128
+    assert f("tn", 8192, 8, M=2048, N=2048) == tg.EXPERT_TILES and f("tn", 1, 8, M=256, N=256) == tg.EXPERT_TILES
     assert f("tn", 8192, 8, M=255, N=256) == tg.EXPERT_GENERIC
 
 
 def test_header_limits():
     text = open(os.path.join(ROOT, "include", "tgemm_ops.h")).read()
     assert f"#define TGEMM_MAX_EXPERTS {tg.MAX_EXPERTS}" in text and "(((int64_t)1 << 26) - 1024)" in text
-    for name, value in (("GENERIC", tg.EXPERT_GENERIC), ("32", tg.EXPERT_32), ("128", tg.EXPERT_128), ("256", tg.EXPERT_256)):
+    for name, value in (("GENERIC", tg.EXPERT_GENERIC), ("32", tg.EXPERT_32), ("128", tg.EXPERT_128), ("256", tg.EXPERT_256),
+                        ("TILES", tg.EXPERT_TILES)):
         assert re.search(rf"#define TGEMM_EXPERT_{name} {value}\b", text)
 
 

@@ -48,19 +48,32 @@ struct ExpertGemmArgs {
   int rows, experts, M, N, K;                 // M: columns of A in the weights' form
   int relu, vec_c, zero_rest;
   int tiles_m, tiles_n;
+  int mode;                                   // of the tile kernel, and the most tiles it may go over
+  uint32_t max_tiles;
 };
 enum ExpertForm { kExpertNT = 0, kExpertNN = 1, kExpertTN = 2 };
-// Kernels of a product, by index (tooling ABI: the _cfg entry point).
-enum ExpertConfig { kExpertGeneric = 0, kExpert32 = 1, kExpert128 = 2, kExpert256 = 3, kExpertConfigs = 4 };
-constexpr int expert_tile_m(int cfg) { return cfg == kExpert256 ? 256 : cfg == kExpert32 ? 32 : 128; }
-constexpr int expert_tile_n(int cfg) { return cfg == kExpert256 ? 256 : 128; }
-// Workgroups of a launch. The rows' form: c rows of an expert need ceil(c / BM) tile rows, so all of
-// them at most rows / BM + the number of experts that have one; and one tile row more where the
-// rows behind the last group are to be zeroed by workgroups of no tile.
+// Kernels of a product, by index (tooling ABI: the _cfg entry point). kExpertTiles mixes tiles of 256 x
+// 256 and 128 x 128; kExpert128 and kExpert256 are the same kernel held to one of them (but for
+// edges).
+enum ExpertConfig { kExpertGeneric = 0, kExpert32 = 1, kExpert128 = 2, kExpert256 = 3, kExpertTiles = 4, kExpertConfigs = 5 };
+enum ExpertTileMode { kTilesAuto = 0, kTilesSmall = 1, kTilesBig = 2 };
+constexpr int kExpertTileGroups = 256;  // workgroups of the tile kernel, each of which goes over tiles: one a compute unit
+constexpr int expert_tile_m(int cfg) { return cfg == kExpert32 ? 32 : 128; }
+constexpr int expert_tile_n(int) { return 128; }
+// Workgroups of a launch. The rows' form of the others has one a tile: c rows of an expert need ceil(c
+// / BM) tile rows, so all of them at most rows / BM + the number of experts that have one; and one
+// tile row more where the rows behind the last group are to be zeroed by workgroups of no tile.
 inline int64_t expert_gemm_groups(int cfg, int form, int64_t rows, int64_t experts, int64_t M, int64_t N) {
+  if (cfg >= kExpert128) return kExpertTileGroups;
   const int64_t tn = ceil_div(N, expert_tile_n(cfg));
   if (form == kExpertTN) return experts * ceil_div(M, expert_tile_m(cfg)) * tn;
   return (rows / expert_tile_m(cfg) + (experts < rows ? experts : rows) + 1) * tn;
+}
+// The most 128 x 128 tiles that any division of the rows gives the tile kernel.
+inline int64_t expert_max_tiles(int form, int64_t rows, int64_t experts, int64_t M, int64_t N) {
+  const int64_t tn = ceil_div(N, 128) + 1;
+  if (form == kExpertTN) return experts * (ceil_div(M, 128) + 1) * tn;
+  return (rows / 128 + 2 * (experts < rows ? experts : rows)) * tn;
 }
 hipError_t launch_expert_gemm(int cfg, ExpertForm form, const ExpertGemmArgs& g, hipStream_t s, int device);
 

@@ -51,11 +51,9 @@ bool chunks(const void* p, int64_t ld, int64_t width) {
 // Kernel of a product whose operands the tiles take, by the rows an expert has on average.
 int choose(int form, int64_t rows, int64_t experts, int64_t M, int64_t N) {
   const int64_t met = rows < experts ? at_least_1(rows) : experts, each = rows / met;
-  if (form == tgemm::kExpertTN)
-    return experts * tgemm::ceil_div(M, 256) * tgemm::ceil_div(N, 256) >= 256 ? tgemm::kExpert256 : tgemm::kExpert128;
-  if (each <= 48) return tgemm::kExpert32;
-  return each >= 256 && tgemm::ceil_div(rows, 256) * tgemm::ceil_div(N, 256) >= 200 ? tgemm::kExpert256
-                                                                                   : tgemm::kExpert128;
+  (void)M;
+  (void)N;
+  return form != tgemm::kExpertTN && each <= 48 ? tgemm::kExpert32 : tgemm::kExpertTiles;
 }
 
 int validate(int form, int64_t rows, int64_t experts, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
@@ -103,8 +101,11 @@ int run(int force, int form, int64_t rows, int64_t experts, int64_t M, int64_t N
     if (force == tgemm::kExpert32 && form == tgemm::kExpertTN) return TGEMM_EINVAL_CFG;
     cfg = force;
   }
-  // the runtime takes fewer than 2^32 threads per launch, 512 a workgroup at most
-  if (tgemm::expert_gemm_groups(cfg, form, rows, experts, M, N) >= ((int64_t)1 << 23)) return TGEMM_EINVAL_DIM;
+  // the runtime takes fewer than 2^32 threads per launch, 512 a workgroup at most; the tile kernel counts
+  // its tiles in 32 bits
+  if (tgemm::expert_gemm_groups(cfg, form, rows, experts, M, N) >= ((int64_t)1 << 23) ||
+      tgemm::expert_max_tiles(form, rows, experts, M, N) >= ((int64_t)1 << 31))
+    return TGEMM_EINVAL_DIM;
   int dev = -1;
   const int d = tgemm::current_device(&dev);
   if (d != TGEMM_OK) return d;

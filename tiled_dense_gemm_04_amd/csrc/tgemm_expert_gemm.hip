@@ -88,20 +88,20 @@ __device__ __forceinline__ RowTile find_tile(const ExpertGemmArgs& g, int lane) 
   return t;
 }
 
-// The rows behind the last group, zeroed by the workgroups past the last tile.
+// The rows behind the last group, zeroed by `parts` workgroups, of which this is `part`.
 template <int THREADS>
-__device__ void zero_rest(const ExpertGemmArgs& g, const RowTile& t) {
-  if (!g.zero_rest || t.past_count == 0) return;
+__device__ void zero_rest(const ExpertGemmArgs& g, int part, int parts) {
+  if (!g.zero_rest || parts == 0) return;
   const half8 zero = {0, 0, 0, 0, 0, 0, 0, 0};
   const int chunks = (g.N + 7) / 8;
-  for (int r = clamped(g, g.experts) + t.past; r < g.rows; r += t.past_count)
-    for (int c = threadIdx.x; c < chunks; c += THREADS) store_half8(g.C + (int64_t)r * g.ldc + 8 * c, zero, g.N - 8 * c);
+  for (int64_t r = (int64_t)clamped(g, g.experts) + part; r < g.rows; r += parts)
+    for (int c = threadIdx.x; c < chunks; c += THREADS) store_half8(g.C + r * g.ldc + 8 * c, zero, g.N - 8 * c);
 }
 
 // ------------------------------------------------------------------------------------
 // BM x BM tiles on the two-group ping-pong schedule (tgemm_pingpong.h): 256 x 256 with k-tiles of
 // 32, or 128 x 128 with k-tiles of 64 of which each wave group takes half, the groups' sums joined at
-// the end.
+// the end. A, B and C point at the tile's first row or column of each.
 template <int BM>
 constexpr int kTileKg = BM == 128 ? 2 : 1;
 template <int BM>
@@ -109,6 +109,7 @@ constexpr int tile_lds_bytes() {
   constexpr int ring = 4 * 2 * BM * 64 * kTileKg<BM>, st = 8 * StagedTile<BM / 2 / kTileKg<BM>, BM * kTileKg<BM> / 4>::BYTES;
   return ring > st ? ring : st;
 }
+constexpr int kTileLds = tile_lds_bytes<256>() > tile_lds_bytes<128>() ? tile_lds_bytes<256>() : tile_lds_bytes<128>();
 template <bool JOINED, typename A, typename B>
 __device__ __forceinline__ auto& pick_sums(A& own, B& joined) {
   if constexpr (JOINED)
@@ -118,7 +119,8 @@ __device__ __forceinline__ auto& pick_sums(A& own, B& joined) {
 }
 
 template <int BM, ExpertForm F>
-__global__ __launch_bounds__(512) void expert_tiles(ExpertGemmArgs g) {
+__device__ __forceinline__ void tile_product(const ExpertGemmArgs& g, char* smem, const _Float16* A, const _Float16* B,
+                                             _Float16* C, int mvalid, int nvalid, int K) {
   constexpr int NW = 8, STAGES = 4, KG = kTileKg<BM>, WN = 4 / KG, BK = 32 * KG;
   constexpr int WTN = BM / WN, FM = BM / 32, FN = WTN / 16;
   constexpr int WTM = BM / 2 / KG, FE = FM / KG;  // after the groups are joined
@@ -128,48 +130,22 @@ __global__ __launch_bounds__(512) void expert_tiles(ExpertGemmArgs g) {
   constexpr int A_BYTES = OpA::BYTES, B_BYTES = OpB::BYTES, PT = OpA::LD + OpB::LD;
   static_assert(OpA::REM == 0 && OpB::REM == 0, "copies split evenly");
 
-  extern __shared__ __attribute__((aligned(16))) char smem[];
   char* const a_lds = smem;
   char* const b_lds = smem + STAGES * A_BYTES;
-  const int tid = threadIdx.x, lane = tid & 63;
+  // (a thread index of the tile's own: what follows from it is not carried over the loop over tiles,
+  // where it would spill)
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-
-  int row0, col0, mvalid, K;
-  const _Float16 *A, *B;
-  _Float16* C;
-  if constexpr (F == kExpertTN) {
-    const int tiles = g.tiles_m * g.tiles_n;
-    const int64_t lid = xcd_logical_id(blockIdx.x, (int64_t)tiles * g.experts, 1);
-    const int e = __builtin_amdgcn_readfirstlane((int)(lid / tiles));
-    int64_t tm, tn;
-    panel_tile(lid - (int64_t)e * tiles, g.tiles_m, g.tiles_n, 4, &tm, &tn);
-    const RowRange r = expert_rows(g, e);
-    row0 = __builtin_amdgcn_readfirstlane((int)tm) * BM;
-    col0 = __builtin_amdgcn_readfirstlane((int)tn) * BM;
-    mvalid = min(BM, g.M - row0);
-    K = __builtin_amdgcn_readfirstlane(r.count);
-    const int64_t first = __builtin_amdgcn_readfirstlane(r.first);
-    A = g.A + first * g.lda;
-    B = g.B + first * g.ldb;
-    C = g.C + e * g.stride_c;
-  } else {
-    const RowTile t = find_tile<BM, 4>(g, lane);
-    if (t.e < 0) return zero_rest<512>(g, t);
-    row0 = t.tm * BM;
-    col0 = t.tn * BM;
-    mvalid = min(BM, t.rows.count - row0);
-    K = g.K;
-    A = g.A + (int64_t)t.rows.first * g.lda;
-    B = g.B + t.e * g.stride_b;
-    C = g.C + (int64_t)t.rows.first * g.ldc;
-  }
-  const int nvalid = min(BM, g.N - col0);
+  mvalid = min(BM, mvalid);
+  nvalid = min(BM, nvalid);
   const int nk = (K + BK - 1) / BK, kin_last = K - (nk - 1) * BK;
 
   OpA opa;
   OpB opb;
-  opa.init_copies(A, g.lda, row0, mvalid, kin_last, wave, lane);
-  opb.init_copies(B, g.ldb, col0, nvalid, kin_last, wave, lane);
+  opa.init_copies(A, g.lda, 0, mvalid, kin_last, wave, lane);
+  opb.init_copies(B, g.ldb, 0, nvalid, kin_last, wave, lane);
   const uint32_t a_lds0 = lds_addr(a_lds) + wave * 1024, b_lds0 = lds_addr(b_lds) + wave * 1024;
   TileStream sa, sb;
   sa.init(opa, nk);
@@ -223,8 +199,221 @@ __global__ __launch_bounds__(512) void expert_tiles(ExpertGemmArgs g) {
   else
     ST::template stage<false>(stage, acc, lane);
   ST::wave_fence();
-  store_staged<ST, WTM, false>(stage, lane, C + (int64_t)(row0 + wr0) * g.ldc + col0 + wc0, g.ldc, mvalid - wr0,
-                               nvalid - wc0, g.vec_c);
+  store_staged<ST, WTM, false>(stage, lane, C + (int64_t)wr0 * g.ldc + wc0, g.ldc, mvalid - wr0, nvalid - wc0, g.vec_c);
+}
+
+// How an M x N part of C is cut: 256 x 256 tiles, and 128 x 128 ones along its lower and right edge
+// where no more than half of a big tile would be used.
+struct Cut {
+  uint32_t mb, nb;           // big tiles
+  uint32_t low, low_count;   // first row of the lower edge, its tiles (0: none)
+  uint32_t right_count;      // tiles of the right edge (at column 256 nb)
+  __device__ Cut(uint32_t M, uint32_t N) {
+    mb = (M + 127) / 256;
+    nb = (N + 127) / 256;
+    low = mb * 256;
+    low_count = M > low ? (N + 127) / 128 : 0;
+    right_count = N > nb * 256 ? (min(M, low) + 127) / 128 : 0;
+  }
+  __device__ uint32_t big() const { return mb * nb; }
+  __device__ uint32_t small() const { return low_count + right_count; }
+};
+
+// The tiles of a launch, in the order in which its workgroups take them (workgroup w those at w, w +
+// gridDim.x, ...): `kept` big tiles; the other big ones in quarters; the small ones. One big tile
+// takes about as long as three small ones, so big tiles that would fill less than half of the compute
+// units in a last round go in quarters. (Counts are of 32 bits: the host keeps those of offsets that
+// do not decrease below 2^31, and the length of the list below that bound whatever the offsets hold.)
+struct TileList {
+  uint32_t kept, quarters, edges;  // big tiles, quarters (4 a tile), edge tiles
+  __device__ void cut(uint32_t big, uint32_t small, int mode) {
+    constexpr uint32_t G = kExpertTileGroups;
+    const uint32_t rest = big % G;
+    bool keep = mode == kTilesBig;
+    if (mode == kTilesAuto) {
+      const uint32_t idle = rest == 0 ? 0 : G - rest;
+      const uint32_t as_big = (rest == 0 ? 0 : 3) + (small > idle ? (small - idle + G - 1) / G : 0);
+      keep = as_big <= (4 * rest + small + G - 1) / G;
+    }
+    kept = mode == kTilesSmall ? 0 : keep ? big : big - rest;
+    quarters = 4 * (big - kept);
+    edges = small;
+  }
+};
+
+// A tile: of which expert, from which row and column of its part of C on.
+struct Tile {
+  int e;
+  uint32_t row0, col0;
+  RowRange rows;
+  bool big;
+};
+
+// The list and, for each lane, what finds a tile in it, in LDS: the registers are the product's.
+struct FinderState {
+  TileList list;
+  uint32_t big_incl[64], small_incl[64];  // rows' form: tiles of a lane's experts and those before
+  int rank[64];                           // weights' form: the place of a lane's expert, most rows first
+};
+
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
+
+// Consecutive ids of `total` on one XCD (xcd_logical_id in 32 bits), inside each round of the launch's
+// workgroups: an XCD that took a contiguous part of all of them would take the longest of the
+// weights' form, which come first (16384 rows, 16 uneven experts, 4096 x 2048: 495 us, so 281).
+__device__ __forceinline__ uint32_t xcd_id(uint32_t at, uint32_t total) {
+  constexpr uint32_t G = kExpertTileGroups;
+  const uint32_t first = at / G * G, wg = at - first, n = min(G, total - first);
+  if (n < (uint32_t)kNumXcd) return at;
+  const uint32_t q = n / kNumXcd, r = n % kNumXcd, x = wg % kNumXcd, j = wg / kNumXcd;
+  return first + x * q + min(x, r) + j;
+}
+
+template <ExpertForm F>
+struct TileFinder {
+  TG_LDS FinderState* st;
+
+  // (by one wave; a barrier follows)
+  __device__ void init(const ExpertGemmArgs& g, int lane) {
+    TileList list;
+    if constexpr (F == kExpertTN) {
+      const Cut c(g.M, g.N);
+      list.cut(c.big() * g.experts, c.small() * g.experts, g.mode);
+      int rank = lane;
+      if (g.experts <= 64) {
+        const int mine = lane < g.experts ? expert_rows(g, lane).count : -1;
+        rank = 0;
+        for (int j = 0; j < g.experts; ++j) {
+          const int other = __builtin_amdgcn_readlane(mine, j);
+          rank += other > mine || (other == mine && j < lane) ? 1 : 0;
+        }
+      }
+      st->rank[lane] = rank;
+    } else {
+      const int per = (g.experts + 63) / 64, e0 = min(lane * per, g.experts), e1 = min(e0 + per, g.experts);
+      uint32_t big = 0, small = 0;
+      for (int e = e0; e < e1; ++e) {
+        const Cut c(expert_rows(g, e).count, g.N);
+        big += c.big();
+        small += c.small();
+      }
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const uint32_t b = __shfl_up(big, o, 64), s = __shfl_up(small, o, 64);
+        if (lane >= o) {
+          big += b;
+          small += s;
+        }
+      }
+      st->big_incl[lane] = big;
+      st->small_incl[lane] = small;
+      list.cut(__shfl(big, 63, 64), __shfl(small, 63, 64), g.mode);
+    }
+    if (lane == 0) {
+      st->list.kept = list.kept;
+      st->list.quarters = list.quarters;
+      st->list.edges = list.edges;
+    }
+  }
+
+  // Tile `at` of the list into t (uniform); false past its end.
+  __device__ bool get(const ExpertGemmArgs& g, uint32_t at, int lane, Tile& t) const {
+    const uint32_t kept = uniform(st->list.kept), quarters = uniform(st->list.quarters), rest = quarters + uniform(st->list.edges);
+    if (at >= min(kept + rest, g.max_tiles)) return false;
+    // i: which of the big tiles, or of the small ones; a quarter names its big tile
+    uint32_t i, quarter = 4;
+    bool big = true;
+    if (at < kept) {
+      i = xcd_id(at, kept);
+    } else {
+      i = xcd_id(at - kept, rest);
+      big = i < quarters;
+      if (big) {
+        quarter = i & 3;
+        i = kept + i / 4;
+      } else {
+        i -= quarters;
+      }
+    }
+    uint32_t M;
+    int e;
+    if constexpr (F == kExpertTN) {
+      M = g.M;
+      const Cut c(M, g.N);
+      const uint32_t each = big ? c.big() : c.small();
+      e = (int)(i / each);
+      i -= e * each;
+      if (g.experts <= 64) e = __builtin_ctzll(__builtin_amdgcn_ballot_w64(st->rank[lane] == e && lane < g.experts) | 1ull << 63);
+      t.rows = expert_rows(g, min(e, g.experts - 1));
+    } else {
+      const TG_LDS uint32_t* const incl = big ? st->big_incl : st->small_incl;
+      const int per = (g.experts + 63) / 64;
+      const int owner = __builtin_popcountll(__builtin_amdgcn_ballot_w64(incl[lane] <= i));  // lanes whose tiles end before i
+      if (owner > 0) i -= uniform(incl[owner - 1]);
+      e = min(owner * per, g.experts - 1);
+      const int last = min(e + per, g.experts) - 1;
+      t.rows = expert_rows(g, e);
+      for (;;) {
+        const Cut c(t.rows.count, g.N);
+        const uint32_t n = big ? c.big() : c.small();
+        if (i < n || e == last) break;
+        i -= n;
+        t.rows = expert_rows(g, ++e);
+      }
+      M = t.rows.count;
+    }
+    const Cut c(M, g.N);
+    if (big) {  // panels of four tile rows, the tile rows of a panel first
+      const uint32_t per_panel = 4 * c.nb, p = i / per_panel, within = i - p * per_panel, rows = min(c.mb - 4 * p, 4u);
+      const uint32_t tn = within / rows, tm = 4 * p + within - tn * rows;
+      t.row0 = tm * 256 + (quarter < 4 ? 128 * (quarter >> 1) : 0);
+      t.col0 = tn * 256 + (quarter < 4 ? 128 * (quarter & 1) : 0);
+    } else {
+      const bool lower = i < c.low_count;
+      t.row0 = lower ? c.low : 128 * (i - c.low_count);
+      t.col0 = lower ? 128 * i : 256 * c.nb;
+    }
+    t.big = big && quarter == 4;
+    t.e = __builtin_amdgcn_readfirstlane(e);
+    t.rows.first = __builtin_amdgcn_readfirstlane(t.rows.first);
+    t.rows.count = __builtin_amdgcn_readfirstlane(t.rows.count);
+    t.row0 = uniform(t.row0);
+    t.col0 = uniform(t.col0);
+    return true;
+  }
+};
+
+template <ExpertForm F>
+__global__ __launch_bounds__(512) void expert_tiles(ExpertGemmArgs args) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int lane = threadIdx.x & 63;
+  TileFinder<F> finder = {(TG_LDS FinderState*)(smem + kTileLds)};
+  if (threadIdx.x < 64) finder.init(args, lane);
+  // The arguments are read again for every tile: kept over the loop they would spill.
+  typedef const __attribute__((address_space(4))) ExpertGemmArgs KernelArgs;
+  KernelArgs* source = (KernelArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  for (uint32_t at = blockIdx.x;; at += gridDim.x) {
+    asm volatile("" : "+s"(source));
+    ExpertGemmArgs g;
+    __builtin_memcpy(&g, (const void*)source, sizeof(g));
+    __syncthreads();  // the list is there, and every wave has stored its part of the tile before
+    Tile t;
+    if (!finder.get(g, at, lane, t)) break;
+    const uint32_t M = F == kExpertTN ? g.M : t.rows.count, K = F == kExpertTN ? t.rows.count : g.K;
+    // (offsets that run backwards or change under the launch can leave no such tile)
+    if (t.row0 >= M || t.col0 >= (uint32_t)g.N) continue;
+    const int64_t first = t.rows.first;
+    const _Float16* const A = F == kExpertTN ? g.A + first * g.lda + t.row0 : g.A + (first + t.row0) * g.lda;
+    const _Float16* const B = F == kExpertTN   ? g.B + first * g.ldb + t.col0
+                              : F == kExpertNT ? g.B + t.e * g.stride_b + (int64_t)t.col0 * g.ldb
+                                               : g.B + t.e * g.stride_b + t.col0;
+    _Float16* const C = (F == kExpertTN ? g.C + t.e * g.stride_c : g.C + first * g.ldc) + (int64_t)t.row0 * g.ldc + t.col0;
+    if (t.big)
+      tile_product<256, F>(g, smem, A, B, C, M - t.row0, g.N - t.col0, K);
+    else
+      tile_product<128, F>(g, smem, A, B, C, M - t.row0, g.N - t.col0, K);
+  }
+  if constexpr (F != kExpertTN) zero_rest<512>(args, blockIdx.x, gridDim.x);
 }
 
 // ------------------------------------------------------------------------------------
@@ -252,7 +441,7 @@ __global__ __launch_bounds__(256) void expert_small(ExpertGemmArgs g) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const RowTile t = find_tile<BM, 4>(g, lane);
-  if (t.e < 0) return zero_rest<256>(g, t);
+  if (t.e < 0) return zero_rest<256>(g, t.past, t.past_count);
   const int row0 = t.tm * BM, col0 = t.tn * BN;
   const int mvalid = min(BM, t.rows.count - row0), nvalid = min(BN, g.N - col0);
   const int nk = (g.K + BK - 1) / BK, kin_last = g.K - (nk - 1) * BK;
@@ -342,7 +531,7 @@ __global__ __launch_bounds__(256) void expert_generic(ExpertGemmArgs g) {
     C = g.C + e * g.stride_c;
   } else {
     const RowTile t = find_tile<BM, 4>(g, lane);
-    if (t.e < 0) return zero_rest<256>(g, t);
+    if (t.e < 0) return zero_rest<256>(g, t.past, t.past_count);
     row0 = t.tm * BM;
     col0 = t.tn * BM;
     mvalid = t.rows.count - row0;
@@ -444,16 +633,15 @@ hipError_t launch(K kern, int threads, int lds, std::atomic<uint64_t>& ready, co
   hipLaunchKernelGGL(kern, dim3(grid), dim3(threads), lds, s, g);
   return hipGetLastError();
 }
-template <int BM, ExpertForm F>
-hipError_t launch_tiles(const ExpertGemmArgs& g, unsigned grid, hipStream_t s, int device) {
-  static std::atomic<uint64_t> ready{0};
-  return launch(expert_tiles<BM, F>, 512, tile_lds_bytes<BM>(), ready, g, grid, s, device);
-}
 template <ExpertForm F>
 hipError_t launch_form(int cfg, const ExpertGemmArgs& g, unsigned grid, hipStream_t s, int device) {
   switch (cfg) {
-    case kExpert256: return launch_tiles<256, F>(g, grid, s, device);
-    case kExpert128: return launch_tiles<128, F>(g, grid, s, device);
+    case kExpertTiles:
+    case kExpert128:
+    case kExpert256: {
+      static std::atomic<uint64_t> ready{0};
+      return launch(expert_tiles<F>, 512, kTileLds + (int)sizeof(FinderState), ready, g, grid, s, device);
+    }
     case kExpert32:
       if constexpr (F != kExpertTN) {
         static std::atomic<uint64_t> ready{0};
@@ -471,6 +659,8 @@ hipError_t launch_form(int cfg, const ExpertGemmArgs& g, unsigned grid, hipStrea
 
 hipError_t launch_expert_gemm(int cfg, ExpertForm form, const ExpertGemmArgs& args, hipStream_t s, int device) {
   ExpertGemmArgs g = args;
+  g.mode = cfg == kExpert128 ? kTilesSmall : cfg == kExpert256 ? kTilesBig : kTilesAuto;
+  g.max_tiles = (uint32_t)expert_max_tiles(form, g.rows, g.experts, g.M, g.N);
   const int64_t grid = expert_gemm_groups(cfg, form, g.rows, g.experts, g.M, g.N);
   g.tiles_m = form == kExpertTN ? (int)ceil_div(g.M, expert_tile_m(cfg)) : 0;
   g.tiles_n = (int)ceil_div(g.N, expert_tile_n(cfg));
