@@ -23,11 +23,11 @@ __device__ __forceinline__ int slot_class(const ExpertSortArgs& g, int s) {
     at = (int64_t)t * g.ldi + (s - t * g.k);
   }
   if constexpr (I64) {
-    const int64_t v = ((const int64_t*)g.ids)[at];
-    return v >= 0 && v < g.experts ? (int)v : g.experts;
+    const uint64_t v = ((const uint64_t*)g.ids)[at];
+    return v < (uint64_t)g.experts ? (int)v : g.experts;
   } else {
-    const int v = ((const int*)g.ids)[at];
-    return v >= 0 && v < g.experts ? v : g.experts;
+    const uint32_t v = ((const uint32_t*)g.ids)[at];
+    return v < (uint32_t)g.experts ? (int)v : g.experts;
   }
 }
 
@@ -38,9 +38,10 @@ __device__ __forceinline__ int lanes_below(uint64_t mask) {
 // ------------------------------------------------------------------------------------
 // Up to kSortOneLaunch slots: workgroup c owns class c (c = E: the slots of no expert, which go last
 // with order and place -1). A wave looks through a contiguous part of the slots, 64 at a time, and
-// keeps the ballots of its class in its lanes (lane i that of step i), so the ids are read once; the
-// waves' counts meet in LDS. The ids come from L2 E + 1 times over, which for these sizes costs
+// keeps the ballots of its class in its lanes (lane i that of step i), so the ids are read once and
+// each lane then places the few slots of its ballot; the waves' counts meet in LDS. The ids come from L2 E + 1 times over, which for these sizes costs
 // less than a second launch.
+constexpr int kSortAhead = 16;  // loads in flight
 template <bool I64>
 __global__ __launch_bounds__(1024) void expert_sort_small(ExpertSortArgs g) {
   __shared__ int wave_eq[16], wave_lt[16];
@@ -50,15 +51,16 @@ __global__ __launch_bounds__(1024) void expert_sort_small(ExpertSortArgs g) {
   const int s0 = wave * steps * 64;
   uint64_t mine = 0;
   int eq = 0, lt = 0;
-  for (int i = 0; i < steps; i += 4) {  // four loads in flight
-    int v[4];
+  for (int i = 0; i < steps; i += kSortAhead) {
+    int v[kSortAhead];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < kSortAhead; ++q) {
       const int s = s0 + 64 * (i + q) + lane;
-      v[q] = i + q < steps && s < g.n ? slot_class<I64>(g, s) : kMaxExperts + 1;
+      v[q] = kMaxExperts + 1;
+      if (i + q < steps && s < g.n) v[q] = slot_class<I64>(g, s);
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < kSortAhead; ++q) {
       const uint64_t hit = __builtin_amdgcn_ballot_w64(v[q] == c);
       lt += __builtin_popcountll(__builtin_amdgcn_ballot_w64(v[q] < c));
       eq += __builtin_popcountll(hit);
@@ -76,16 +78,19 @@ __global__ __launch_bounds__(1024) void expert_sort_small(ExpertSortArgs g) {
     if (w < wave) row += wave_eq[w];
   }
   if (threadIdx.x == 0) g.offsets[c] = first;
-  row += first;
-  for (int i = 0; i < steps; ++i) {
-    const uint64_t hit = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(mine >> 32), i) << 32) |
-                         (uint32_t)__builtin_amdgcn_readlane((int)mine, i);
-    if ((hit >> lane) & 1) {
-      const int s = s0 + 64 * i + lane, p = row + lanes_below(hit);
-      g.place[s] = c < g.experts ? p : -1;
-      g.order[p] = c < g.experts ? s : -1;
-    }
-    row += __builtin_popcountll(hit);
+  // lane i places the slots of step i: those of the steps before come first
+  int incl = __builtin_popcountll(mine);
+  const int own = incl;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int up = __shfl_up(incl, o, 64);
+    if (lane >= o) incl += up;
+  }
+  int p = first + row + incl - own;
+  for (; mine != 0; mine &= mine - 1, ++p) {
+    const int s = s0 + 64 * lane + __builtin_ctzll(mine);
+    g.place[s] = c < g.experts ? p : -1;
+    g.order[p] = c < g.experts ? s : -1;
   }
 }
 
@@ -103,31 +108,39 @@ __global__ __launch_bounds__(64 * kSortWaves) void expert_sort_count(ExpertSortA
   for (int e = lane; e <= g.experts; e += 64) count[wave][e] = 0;
   __syncthreads();
   const int64_t s0 = (int64_t)seg * steps * 64;
-  for (int i = 0; i < steps; ++i) {
-    const int64_t s = s0 + 64 * i + lane;
-    const bool live = s < g.n;
-    const int v = live ? slot_class<I64>(g, (int)s) : 0;
-    // lanes of the same class, bit by bit
-    uint64_t same = __builtin_amdgcn_ballot_w64(live);
-    for (int b = 0; b < bits; ++b) {
-      const uint64_t set = __builtin_amdgcn_ballot_w64((v >> b) & 1);
-      same &= (v >> b) & 1 ? set : ~set;
+  for (int i0 = 0; i0 < steps; i0 += 8) {  // eight loads in flight
+    int v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int64_t s = s0 + 64 * (i0 + q) + lane;
+      v[q] = -1;
+      if (i0 + q < steps && s < g.n) v[q] = slot_class<I64>(g, (int)s);
     }
-    if (live) {
-      const int below = lanes_below(same), base = count[wave][v];
-      g.place[s] = base + below;
-      // (the wave's reads above come before this write: LDS runs a wave's accesses in order)
-      if (below == 0) count[wave][v] = base + __builtin_popcountll(same);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      // lanes of the same class, bit by bit
+      uint64_t same = __builtin_amdgcn_ballot_w64(v[q] >= 0);
+      if (same == 0) break;
+      for (int b = 0; b < bits; ++b) {
+        const uint64_t set = __builtin_amdgcn_ballot_w64((v[q] >> b) & 1);
+        same &= (v[q] >> b) & 1 ? set : ~set;
+      }
+      if (v[q] >= 0) {
+        const int below = lanes_below(same), base = count[wave][v[q]];
+        g.place[s0 + 64 * (i0 + q) + lane] = base + below;
+        // (the wave's reads above come before this write: LDS runs a wave's accesses in order)
+        if (below == 0) count[wave][v[q]] = base + __builtin_popcountll(same);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+      __builtin_amdgcn_wave_barrier();
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
   }
   for (int e = lane; e <= g.experts; e += 64) g.counts[(int64_t)seg * (g.experts + 1) + e] = count[wave][e];
 }
 
 template <bool I64>
-__global__ __launch_bounds__(64 * kSortWaves) void expert_sort_place(ExpertSortArgs g, int steps) {
+__global__ __launch_bounds__(64 * kSortWaves) void expert_sort_place(ExpertSortArgs g, int segments, int steps) {
   __shared__ int start[kSortWaves][kMaxExperts + 1];
   __shared__ int total[kMaxExperts + 1];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -135,11 +148,15 @@ __global__ __launch_bounds__(64 * kSortWaves) void expert_sort_place(ExpertSortA
   // column sums: of all segments, and of those before each of this workgroup's
   for (int e = threadIdx.x; e < classes; e += 64 * kSortWaves) {
     int before = 0, all = 0;
-#pragma unroll 8
-    for (int q = 0; q < kSortSegments; ++q) {
-      const int c = g.counts[(int64_t)q * classes + e];
-      if (q < seg0) before += c;
-      all += c;
+    for (int q0 = 0; q0 < segments; q0 += 16) {  // (a multiple of 16)
+      int c[16];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) c[q] = g.counts[(int64_t)(q0 + q) * classes + e];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        if (q0 + q < seg0) before += c[q];
+        all += c[q];
+      }
     }
 #pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
@@ -313,14 +330,17 @@ hipError_t launch_sort(const ExpertSortArgs& g, hipStream_t s) {
     hipLaunchKernelGGL(expert_sort_small<I64>, dim3((unsigned)g.experts + 1), dim3(64 * waves), 0, s, g);
     return hipGetLastError();
   }
-  const int steps = (int)ceil_div(g.n, (int64_t)kSortSegments * 64);
+  // about 1024 slots a segment
+  const int64_t want = ceil_div(g.n, 1024 * 16) * 16;
+  const int segments = (int)(want < kSortSegments ? want : kSortSegments);
+  const int steps = (int)ceil_div(g.n, (int64_t)segments * 64);
   int bits = 1;
   while ((g.experts >> bits) != 0) ++bits;
-  const dim3 grid(kSortSegments / kSortWaves);
+  const dim3 grid(segments / kSortWaves);
   hipLaunchKernelGGL(expert_sort_count<I64>, grid, dim3(64 * kSortWaves), 0, s, g, steps, bits);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(expert_sort_place<I64>, grid, dim3(64 * kSortWaves), 0, s, g, steps);
+  hipLaunchKernelGGL(expert_sort_place<I64>, grid, dim3(64 * kSortWaves), 0, s, g, segments, steps);
   return hipGetLastError();
 }
 

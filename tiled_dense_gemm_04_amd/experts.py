@@ -86,8 +86,8 @@ def expert_sort(ids, experts: int, stream=None, library=None) -> ExpertOrder:
     if ids.numel() and k > 1 and ids.stride(1) != 1:
         raise ValueError("ids must be row-major (stride(1) == 1)")
     ldi = ids.stride(0) if T > 1 and ids.numel() else max(1, k)
-    L, device = library or lib(), ids.device
-    need = int(L.expert_sort_workspace_bytes(T, k, experts))
+    device = ids.device
+    need = (library or lib()).expert_sort_workspace_bytes(T, k, experts)
     if need < 0:
         raise TgemmError(need, "expert_sort_workspace_bytes")
     with _allocating(stream, device):

@@ -62,43 +62,43 @@ def _weight(w, K, device):
     return dtype
 
 
-def _norm(x, weight, residual, eps, y, q, scale, rstd, residual_out, stream, library):
-    """One call; returns the updated residual (allocated if None, None without a residual)."""
+def _new(like, shape, dtype, stream):
+    """An uninitialised tensor on ``like``'s device, allocated on the call's stream; like itself gives
+    the shape where it is contiguous (the cheapest allocation)."""
     import torch
-    R, K, ldx = _operand(x, "x")
-    device = x.device
+    if stream is None:
+        if like.shape == shape and like.is_contiguous():
+            return torch.empty_like(like, dtype=dtype)
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with _allocating(stream, like.device):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _residual(residual, residual_out, shape, device, stream):
+    """(type, row stride, the updated residual, its row stride), the latter allocated if None."""
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+        return 0, 0, None, 0
+    dtype, ld = _typed_operand(residual, "residual", shape, device)
+    if residual_out is None:
+        return dtype, ld, _new(residual, shape, residual.dtype, stream), shape[1] or 1
+    out_dtype, ldo = _typed_operand(residual_out, "residual_out", shape, device)
+    if out_dtype != dtype:
+        raise TypeError("residual_out must have the residual's type")
+    return dtype, ld, residual_out, ldo
+
+
+def _norm(x, ldx, weight, residual, eps, y, ldy, q, ldq, scale, rstd, residual_out, stream, library):
+    """One call on checked x and outputs; returns the updated residual (None without a residual)."""
+    shape, device = x.shape, x.device
+    R, K = shape
     w_dtype = _weight(weight, K, device)
-    r_dtype = ldr = ldro = 0
-    if residual is not None:
-        r_dtype, ldr = _typed_operand(residual, "residual", (R, K), device)
-        if residual_out is None:
-            with _allocating(stream, device):
-                residual_out = torch.empty((R, K), dtype=residual.dtype, device=device)
-        o_dtype, ldro = _typed_operand(residual_out, "residual_out", (R, K), device)
-        if o_dtype != r_dtype:
-            raise TypeError("residual_out must have the residual's type")
-    elif residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    ldy = ldq = 0
-    if y is not None:
-        Ry, Ky, ldy = _operand(y, "out")
-        if (Ry, Ky) != (R, K):
-            raise ValueError(f"out has shape {tuple(y.shape)}, expected {(R, K)}")
-        if y.device != device:
-            raise ValueError("x and out must be on the same device")
-    if q is not None:
-        Rq, Kq, ldq = _operand8(q, "q")
-        if (Rq, Kq) != (R, K):
-            raise ValueError(f"q has shape {tuple(q.shape)}, expected {(R, K)}")
-        _scale_operand(scale, (R, -(-K // FP8_BLOCK)), "scale")
-        if q.device != device or scale.device != device:
-            raise ValueError("x, q and scale must be on the same device")
-
-    def at(t):
-        return None if t is None else t.data_ptr()
-
-    rc = _call("rmsnorm_f16", (R, K, x.data_ptr(), ldx, at(residual), ldr, r_dtype, weight.data_ptr(), w_dtype, eps,
-                               at(residual_out), ldro, at(y), ldy, at(q), ldq, at(scale), at(rstd),
+    r_dtype, ldr, residual_out, ldro = _residual(residual, residual_out, shape, device, stream)
+    rc = _call("rmsnorm_f16", (R, K, x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, r_dtype,
+                               weight.data_ptr(), w_dtype, eps, None if residual is None else residual_out.data_ptr(), ldro,
+                               None if y is None else y.data_ptr(), ldy, None if q is None else q.data_ptr(), ldq,
+                               None if q is None else scale.data_ptr(), None if rstd is None else rstd.data_ptr(),
                                _stream(stream, device)), device, library)
     if rc != TGEMM_OK:
         raise TgemmError(rc, "rmsnorm_f16")
@@ -111,11 +111,16 @@ def rmsnorm(x, weight, residual=None, eps: float = 1e-6, out=None, residual_out=
     ``residual_out``: h's (the residual itself to update it in place); allocated if None. K is at most
     NORM_MAX_K."""
     import torch
+    R, K, ldx = _operand(x, "x")
     if out is None:
-        R, K, _ = _operand(x, "x")
-        with _allocating(stream, x.device):
-            out = torch.empty((R, K), dtype=torch.float16, device=x.device)
-    h = _norm(x, weight, residual, eps, out, None, None, None, residual_out, stream, library)
+        out, ldy = _new(x, x.shape, torch.float16, stream), K or 1
+    else:
+        Ry, Ky, ldy = _operand(out, "out")
+        if (Ry, Ky) != (R, K):
+            raise ValueError(f"out has shape {tuple(out.shape)}, expected {(R, K)}")
+        if out.device != x.device:
+            raise ValueError("x and out must be on the same device")
+    h = _norm(x, ldx, weight, residual, eps, out, ldy, None, 0, None, None, residual_out, stream, library)
     return out if residual is None else (out, h)
 
 
@@ -125,13 +130,21 @@ def rmsnorm_fp8_block(x, weight, residual=None, eps: float = 1e-6, q=None, scale
     from the float32 y in the same pass: (q, scale), or (q, scale, h) with a ``residual``. Arguments as
     ``rmsnorm``; the result goes to ``gemm_fp8_block``."""
     import torch
-    R, K, _ = _operand(x, "x")
-    with _allocating(stream, x.device):
-        if q is None:
-            q = torch.empty((R, K), dtype=torch.uint8, device=x.device)
-        if scale is None:
-            scale = torch.empty((R, -(-K // FP8_BLOCK)), dtype=torch.float32, device=x.device)
-    h = _norm(x, weight, residual, eps, None, q, scale, None, residual_out, stream, library)
+    R, K, ldx = _operand(x, "x")
+    blocks = -(-K // FP8_BLOCK)
+    if q is None:
+        q, ldq = _new(x, x.shape, torch.uint8, stream), K or 1
+    else:
+        Rq, Kq, ldq = _operand8(q, "q")
+        if (Rq, Kq) != (R, K):
+            raise ValueError(f"q has shape {tuple(q.shape)}, expected {(R, K)}")
+    if scale is None:
+        scale = _new(x, (R, blocks), torch.float32, stream)
+    else:
+        _scale_operand(scale, (R, blocks), "scale")
+    if q.device != x.device or scale.device != x.device:
+        raise ValueError("x, q and scale must be on the same device")
+    h = _norm(x, ldx, weight, residual, eps, None, 0, q, ldq, scale, None, residual_out, stream, library)
     return (q, scale) if residual is None else (q, scale, h)
 
 
@@ -140,11 +153,19 @@ def _rows(t, name, dtypes):
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
     rows, cols = t.shape
-    return t if (cols <= 1 or t.stride(1) == 1) and (rows <= 1 or t.stride(0) >= cols) else t.contiguous()
+    ld, step = t.stride()
+    return t if (cols <= 1 or step == 1) and (rows <= 1 or ld >= cols) else t.contiguous()
+
+
+def _ld(t):
+    """Row stride of a 2-D tensor with contiguous rows, as the library takes it."""
+    rows, cols = t.shape
+    return t.stride(0) if rows > 1 else cols or 1
 
 
 def autograd_functions():
     import torch
+    f16, f32 = torch.float16, torch.float32
 
     class RmsNormFunction(torch.autograd.Function):
         """(x, weight, residual or None, eps) -> y, or (y, h) with a residual, for fp16 x (R, K); the
@@ -154,16 +175,14 @@ def autograd_functions():
         @staticmethod
         def forward(ctx, x, weight, residual, eps):
             x = _row_major(x, "x")
-            R, K = x.shape
-            y = torch.empty((R, K), dtype=torch.float16, device=x.device)
-            rstd = torch.empty(R, dtype=torch.float32, device=x.device)
+            y, rstd = _new(x, x.shape, f16, None), torch.empty(x.shape[0], dtype=f32, device=x.device)
             weight = weight.contiguous()
             if residual is not None:
-                residual = _rows(residual, "residual", (torch.float16, torch.float32))
-            h = _norm(x, weight, residual, eps, y, None, None, rstd, None, None, None)
-            ctx.save_for_backward(x if h is None else h, weight, rstd)
-            ctx.saved = tuple((t.shape, t.dtype) for t in (x if h is None else h, weight, rstd))
-            ctx.has_residual = h is not None
+                residual = _rows(residual, "residual", (f16, f32))
+            h = _norm(x, _ld(x), weight, residual, eps, y, x.shape[1] or 1, None, 0, None, rstd, None, None, None)
+            kept = x if h is None else h
+            ctx.save_for_backward(kept, weight, rstd)
+            ctx.saved = kept.shape, kept.dtype, weight.shape, weight.dtype, rstd.shape, x.device
             ctx.set_materialize_grads(False)
             return y if h is None else (y, h)
 
@@ -172,38 +191,37 @@ def autograd_functions():
             if torch.is_grad_enabled():
                 raise RuntimeError("RmsNormFunction has no second derivative (create_graph=True)")
             h, weight, rstd = ctx.saved_tensors
-            for t, (shape, dtype) in zip((h, weight, rstd), ctx.saved):
-                if t.shape != shape or t.dtype != dtype or not t.is_cuda or t.device != h.device:
-                    raise RuntimeError("a saved-tensor hook returned another tensor than the forward pass saved")
-            device = h.device
-            h, weight, rstd = _rows(h, "h", (h.dtype,)), weight.contiguous(), rstd.contiguous()
-            R, K = h.shape
+            shape, dtype, device = h.shape, h.dtype, h.device
+            # the library takes addresses
+            if ((shape, dtype, weight.shape, weight.dtype, rstd.shape, device) != ctx.saved or rstd.dtype != f32
+                    or weight.device != device or rstd.device != device):
+                raise RuntimeError("a saved-tensor hook returned another tensor than the forward pass saved")
             need_x, need_w, need_r, _ = ctx.needs_input_grad
             if dy is None:  # nothing came back through y
                 if dh is None:
                     return None, None, None, None
-                return dh.to(torch.float16) if need_x else None, torch.zeros_like(weight) if need_w else None, \
+                return dh.to(f16) if need_x else None, torch.zeros_like(weight) if need_w else None, \
                     dh if need_r else None, None
-            dy = _rows(dy, "dy", (torch.float16,))
-            dh = None if dh is None else _rows(dh, "dh", (h.dtype,))
-            dx = torch.empty((R, K), dtype=torch.float16, device=device)
-            dr = torch.empty_like(dx, dtype=h.dtype) if need_r and h.dtype != torch.float16 else None
-            dw = torch.empty_like(weight) if need_w else None
-            need = int(lib().rmsnorm_f16_backward_workspace_bytes(R, K)) if need_w else 0
-            workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
-
-            def at(t):
-                return None if t is None else t.data_ptr()
-
-            def ld(t):
-                return 0 if t is None else max(1, K) if R <= 1 else t.stride(0)
-
-            h_dtype = DTYPE_F32 if h.dtype == torch.float32 else DTYPE_F16
-            w_dtype = DTYPE_F32 if weight.dtype == torch.float32 else DTYPE_F16
+            h, weight, rstd, dy = _rows(h, "h", (dtype,)), weight.contiguous(), rstd.contiguous(), _rows(dy, "dy", (f16,))
+            R, K = shape
+            dx = torch.empty(shape, dtype=f16, device=device)
+            dr = torch.empty(shape, dtype=f32, device=device) if need_r and dtype == f32 else None
+            dw = workspace = None
+            need = 0
+            L = lib()
+            if need_w:
+                dw = torch.empty_like(weight)
+                need = L.rmsnorm_f16_backward_workspace_bytes(R, K)
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            ld = K or 1
+            if dh is not None:
+                dh = _rows(dh, "dh", (dtype,))
             rc = _call("rmsnorm_f16_backward",
-                       (R, K, dy.data_ptr(), ld(dy), h.data_ptr(), ld(h), h_dtype, weight.data_ptr(), w_dtype,
-                        rstd.data_ptr(), at(dh), ld(dh), dx.data_ptr(), ld(dx), at(dr), ld(dr), at(dw), at(workspace),
-                        need, _stream(None, device)), device)
+                       (R, K, dy.data_ptr(), _ld(dy), h.data_ptr(), _ld(h), DTYPE_F32 if dtype == f32 else DTYPE_F16,
+                        weight.data_ptr(), DTYPE_F32 if weight.dtype == f32 else DTYPE_F16, rstd.data_ptr(),
+                        None if dh is None else dh.data_ptr(), 0 if dh is None else _ld(dh), dx.data_ptr(), ld,
+                        None if dr is None else dr.data_ptr(), ld, dw.data_ptr() if need_w else None,
+                        workspace.data_ptr() if need else None, need, _stream(None, device)), device, L)
             if rc != TGEMM_OK:
                 raise TgemmError(rc, "rmsnorm_f16_backward")
             if need_r and dr is None:
