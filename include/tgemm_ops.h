@@ -173,11 +173,11 @@ TGEMM_API int rmsnorm_f16_backward(int64_t R, int64_t K, const void* dY, int64_t
  *   order    : tokens * k int32: the slot of each sorted row, in slot order inside an expert, -1 behind
  *              the last row in use;
  *   place    : tokens x k int32, contiguous: each slot's sorted row, -1 for a slot of no expert.
- *   workspace: 256-byte aligned, expert_sort_workspace_bytes(tokens, k, experts) bytes (0 up to 65536
+ *   workspace: 256-byte aligned, expert_sort_workspace_bytes(tokens, k, experts) bytes (0 up to 8192
  *              slots), nothing expected of its contents; calls that may overlap in time need different
  *              ones.
  * experts is 1 .. TGEMM_MAX_EXPERTS and tokens * k at most TGEMM_MAX_SLOTS (else TGEMM_EINVAL_DIM).
- * Deterministic; one launch up to 65536 slots, two beyond.
+ * Deterministic; one launch up to 8192 slots, two beyond.
  */
 #define TGEMM_INDEX_I32 0
 #define TGEMM_INDEX_I64 1

@@ -37,9 +37,10 @@ def check_sort(plan, ids, E):
         assert np.array_equal(got.cpu().numpy(), want), name
 
 
-# Sizes around the 64-slot steps, the 256 slots of a wave's four, 16 waves, and the limit of one launch.
+# Sizes around the 64-slot steps, the chunks of 512 and 2048 slots, the limit of one launch (8192) and that
+# of 256 chunks of 2048.
 SORTS = [(0, 2, 4), (1, 1, 1), (1, 8, 8), (7, 3, 5), (64, 1, 64), (65, 1, 3), (255, 1, 2), (257, 1, 9), (100, 6, 60), (513, 8, 64),
-         (1000, 4, 1024), (4097, 1, 1), (8191, 8, 256), (65536, 1, 7), (65537, 1, 7), (10923, 6, 60), (20001, 5, 1024),
+         (1000, 4, 1024), (4097, 1, 1), (8191, 8, 256), (512, 1, 6), (2048, 4, 33), (2731, 3, 12), (65536, 1, 7), (262145, 2, 40), (65537, 1, 7), (10923, 6, 60), (20001, 5, 1024),
          (140000, 2, 128)]
 
 

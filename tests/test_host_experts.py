@@ -31,7 +31,7 @@ def test_sort_refusals(kw, code):
 
 def test_sort_workspace_bytes():
     f = tg.lib().expert_sort_workspace_bytes
-    assert f(32768, 2, 8) == 0 and f(65537, 1, 8) == 256 * 9 * 4 and f(0, 0, 1) == 0
+    assert f(4096, 2, 8) == 0 and f(8193, 1, 8) == 256 * 9 * 4 and f(0, 0, 1) == 0
     assert f(-1, 1, 8) == DIM and f(1, 1, 0) == DIM and f(tg.MAX_SLOTS + 1, 1, 8) == DIM
 
 

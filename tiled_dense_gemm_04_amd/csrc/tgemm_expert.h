@@ -16,11 +16,11 @@ struct ExpertSortArgs {
   int tokens, k, n;   // n = tokens * k
   int experts, ids_i64;
   int *offsets, *order, *place;
-  int* counts;        // workspace: kSortSegments x (experts + 1)
+  int* counts;        // workspace: kSortChunks x (experts + 1)
 };
-// Up to this many slots one launch sorts (a workgroup per expert); beyond, two, over segments.
-constexpr int kSortOneLaunch = 65536;
-constexpr int kSortSegments = 256;
+// Up to this many slots one launch sorts; beyond, two, over at most kSortChunks chunks of slots.
+constexpr int kSortOneLaunch = 8192;
+constexpr int kSortChunks = 256;
 hipError_t launch_expert_sort(const ExpertSortArgs& g, hipStream_t s);
 
 // Rows out to their places and back. Any index outside [0, rows) counts as no row.

@@ -36,89 +36,71 @@ __device__ __forceinline__ int lanes_below(uint64_t mask) {
 }
 
 // ------------------------------------------------------------------------------------
-// Up to kSortOneLaunch slots: workgroup c owns class c (c = E: the slots of no expert, which go last
-// with order and place -1). A wave looks through a contiguous part of the slots, 64 at a time, and
-// keeps the ballots of its class in its lanes (lane i that of step i), so the ids are read once and
-// each lane then places the few slots of its ballot; the waves' counts meet in LDS. The ids come from L2 E + 1 times over, which for these sizes costs
-// less than a second launch.
-constexpr int kSortAhead = 16;  // loads in flight
+// Sorting. A workgroup owns a chunk of consecutive slots, each of its waves a contiguous segment of it
+// in steps of 64. The waves count their classes in LDS (integer atomics: the same counts in any order);
+// from the slots of each class in the chunks before and of the classes before follows where each
+// wave's first slot of a class goes, and a second pass over the segment hands out the places: lanes of
+// one class are found bit by bit with ballots. place is written in whole lines, by the slots' own
+// workgroup (written by classes, in pieces of a line from every XCD, it took 21 us for 4095 x 8 slots
+// of 64 experts after other work, 10 in a loop).
+//   One launch, up to kSortOneLaunch slots: every workgroup counts the other chunks' slots for itself.
+//   Two, for more: the chunks' counts go through the workspace.
+// Bound by the latency of dependent steps. After other work (ids and results out of the caches): 32 slots
+// 5.0 us, 4096 7.9, 8192 9.2 in one launch, 9.6, 12.7 and 13.0 in two; 16384 14.0 and 13.1, 32760 23.7 and
+// 13.3; 65536 12 to 17 (8 to 256 experts), 2^20 33.
+constexpr int kSortWaves = 8, kSortThreads = 64 * kSortWaves;
+struct SortCounts {
+  int wave[kSortWaves][kMaxExperts + 1];
+  int before[kMaxExperts + 1], all[kMaxExperts + 1];  // slots of a class in the chunks before, and in all
+};
+
+__device__ __forceinline__ void count_slot(int* p) { __hip_atomic_fetch_add(p, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP); }
+
+// Counts slots [s0, s1), one in `stride` from s0 on, by class; eight loads in flight.
 template <bool I64>
-__global__ __launch_bounds__(1024) void expert_sort_small(ExpertSortArgs g) {
-  __shared__ int wave_eq[16], wave_lt[16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-  const int c = blockIdx.x;
-  const int steps = (g.n + 64 * waves - 1) / (64 * waves);  // at most 64
-  const int s0 = wave * steps * 64;
-  uint64_t mine = 0;
-  int eq = 0, lt = 0;
-  for (int i = 0; i < steps; i += kSortAhead) {
-    int v[kSortAhead];
+__device__ __forceinline__ void count_slots(const ExpertSortArgs& g, int64_t s0, int64_t s1, int stride, int* count) {
+  for (; s0 < s1; s0 += 8 * stride) {
+    int v[8];
 #pragma unroll
-    for (int q = 0; q < kSortAhead; ++q) {
-      const int s = s0 + 64 * (i + q) + lane;
-      v[q] = kMaxExperts + 1;
-      if (i + q < steps && s < g.n) v[q] = slot_class<I64>(g, s);
-    }
+    for (int q = 0; q < 8; ++q) v[q] = s0 + q * stride < s1 ? slot_class<I64>(g, (int)(s0 + q * stride)) : -1;
 #pragma unroll
-    for (int q = 0; q < kSortAhead; ++q) {
-      const uint64_t hit = __builtin_amdgcn_ballot_w64(v[q] == c);
-      lt += __builtin_popcountll(__builtin_amdgcn_ballot_w64(v[q] < c));
-      eq += __builtin_popcountll(hit);
-      if (lane == i + q) mine = hit;
-    }
+    for (int q = 0; q < 8; ++q)
+      if (v[q] >= 0) count_slot(count + v[q]);
   }
-  if (lane == 0) {
-    wave_eq[wave] = eq;
-    wave_lt[wave] = lt;
-  }
-  __syncthreads();
-  int first = 0, row = 0;
-  for (int w = 0; w < waves; ++w) {
-    first += wave_lt[w];
-    if (w < wave) row += wave_eq[w];
-  }
-  if (threadIdx.x == 0) g.offsets[c] = first;
-  // lane i places the slots of step i: those of the steps before come first
-  int incl = __builtin_popcountll(mine);
-  const int own = incl;
+}
+
+// Exclusive sums of n counts, by one wave: lane l over counts l * c .. + c.
+__device__ __forceinline__ void exclusive_sums(int* v, int n, int lane) {
+  const int per = (n + 63) / 64, e0 = min(lane * per, n), e1 = min(e0 + per, n);
+  int sum = 0;
+  for (int e = e0; e < e1; ++e) sum += v[e];
+  int incl = sum;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const int up = __shfl_up(incl, o, 64);
     if (lane >= o) incl += up;
   }
-  int p = first + row + incl - own;
-  for (; mine != 0; mine &= mine - 1, ++p) {
-    const int s = s0 + 64 * lane + __builtin_ctzll(mine);
-    g.place[s] = c < g.experts ? p : -1;
-    g.order[p] = c < g.experts ? s : -1;
+  int at = incl - sum;
+  for (int e = e0; e < e1; ++e) {
+    const int c = v[e];
+    v[e] = at;
+    at += c;
   }
 }
 
-// ------------------------------------------------------------------------------------
-// More slots: each of kSortSegments waves counts a contiguous segment by class (a counter per class
-// in LDS) and leaves every slot's rank in its segment in place[]; then each wave finds where its
-// segment's classes start from all segments' counts and writes the places.
-constexpr int kSortWaves = 4;
-
-template <bool I64>
-__global__ __launch_bounds__(64 * kSortWaves) void expert_sort_count(ExpertSortArgs g, int steps, int bits) {
-  __shared__ int count[kSortWaves][kMaxExperts + 1];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int seg = (int)blockIdx.x * kSortWaves + wave;
-  for (int e = lane; e <= g.experts; e += 64) count[wave][e] = 0;
-  __syncthreads();
-  const int64_t s0 = (int64_t)seg * steps * 64;
-  for (int i0 = 0; i0 < steps; i0 += 8) {  // eight loads in flight
-    int v[8];
+// The places of a wave's segment [s0, s1): next[v] is the next place of class v (kept up to date).
+// FINAL: order is written too, and slots of no expert get -1; else place holds the number handed out.
+template <bool I64, bool FINAL>
+__device__ __forceinline__ void place_segment(const ExpertSortArgs& g, int64_t s0, int64_t s1, int bits, int* next, int lane) {
+  for (; s0 < s1; s0 += 64 * 4) {  // four loads in flight
+    int v[4];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      const int64_t s = s0 + 64 * (i0 + q) + lane;
-      v[q] = -1;
-      if (i0 + q < steps && s < g.n) v[q] = slot_class<I64>(g, (int)s);
+    for (int q = 0; q < 4; ++q) {
+      const int64_t s = s0 + 64 * q + lane;
+      v[q] = s < s1 ? slot_class<I64>(g, (int)s) : -1;
     }
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      // lanes of the same class, bit by bit
+    for (int q = 0; q < 4; ++q) {
       uint64_t same = __builtin_amdgcn_ballot_w64(v[q] >= 0);
       if (same == 0) break;
       for (int b = 0; b < bits; ++b) {
@@ -126,83 +108,146 @@ __global__ __launch_bounds__(64 * kSortWaves) void expert_sort_count(ExpertSortA
         same &= (v[q] >> b) & 1 ? set : ~set;
       }
       if (v[q] >= 0) {
-        const int below = lanes_below(same), base = count[wave][v[q]];
-        g.place[s0 + 64 * (i0 + q) + lane] = base + below;
+        const int below = lanes_below(same), first = next[v[q]], p = first + below, s = (int)(s0 + 64 * q + lane);
+        if (FINAL) {
+          g.place[s] = v[q] < g.experts ? p : -1;
+          g.order[p] = v[q] < g.experts ? s : -1;
+        } else {
+          g.place[s] = p;
+        }
         // (the wave's reads above come before this write: LDS runs a wave's accesses in order)
-        if (below == 0) count[wave][v[q]] = base + __builtin_popcountll(same);
+        if (below == 0) next[v[q]] = first + __builtin_popcountll(same);
       }
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
       __builtin_amdgcn_wave_barrier();
       __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
     }
   }
-  for (int e = lane; e <= g.experts; e += 64) g.counts[(int64_t)seg * (g.experts + 1) + e] = count[wave][e];
+}
+
+// A wave's segment of chunk `chunk` of `steps` steps a wave.
+struct Segment {
+  int64_t s0, s1;
+};
+__device__ __forceinline__ Segment segment_of(const ExpertSortArgs& g, int chunk, int wave, int steps) {
+  const int64_t s0 = ((int64_t)chunk * kSortWaves + wave) * steps * 64, s1 = s0 + (int64_t)steps * 64;
+  return {s0 < g.n ? s0 : g.n, s1 < g.n ? s1 : g.n};
 }
 
 template <bool I64>
-__global__ __launch_bounds__(64 * kSortWaves) void expert_sort_place(ExpertSortArgs g, int segments, int steps) {
-  __shared__ int start[kSortWaves][kMaxExperts + 1];
-  __shared__ int total[kMaxExperts + 1];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int seg0 = (int)blockIdx.x * kSortWaves, classes = g.experts + 1;
-  // column sums: of all segments, and of those before each of this workgroup's
-  for (int e = threadIdx.x; e < classes; e += 64 * kSortWaves) {
-    int before = 0, all = 0;
-    for (int q0 = 0; q0 < segments; q0 += 16) {  // (a multiple of 16)
-      int c[16];
+__global__ __launch_bounds__(kSortThreads) void expert_sort_one(ExpertSortArgs g, int steps, int bits) {
+  __shared__ SortCounts c;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, classes = g.experts + 1, chunk = blockIdx.x;
+  for (int e = tid; e < classes; e += kSortThreads) {
 #pragma unroll
-      for (int q = 0; q < 16; ++q) c[q] = g.counts[(int64_t)(q0 + q) * classes + e];
-#pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        if (q0 + q < seg0) before += c[q];
-        all += c[q];
-      }
-    }
+    for (int w = 0; w < kSortWaves; ++w) c.wave[w][e] = 0;
+    c.before[e] = c.all[e] = 0;
+  }
+  __syncthreads();
+  const int64_t s0 = segment_of(g, chunk, 0, steps).s0, s1 = segment_of(g, chunk, kSortWaves - 1, steps).s1;
+  const Segment seg = segment_of(g, chunk, wave, steps);
+  count_slots<I64>(g, seg.s0 + lane, seg.s1, 64, c.wave[wave]);
+  count_slots<I64>(g, tid, s0, kSortThreads, c.before);
+  count_slots<I64>(g, s1 + tid, g.n, kSortThreads, c.all);
+  __syncthreads();
+  for (int e = tid; e < classes; e += kSortThreads) {
+    int at = c.before[e];
 #pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
-      start[w][e] = before;
-      before += g.counts[(int64_t)(seg0 + w) * classes + e];
-    }
-    total[e] = all;
-  }
-  __syncthreads();
-  // exclusive sums of the classes' totals, by the first wave: lane l over classes l * c .. + c
-  if (wave == 0) {
-    const int per = (classes + 63) / 64, e0 = lane * per, e1 = min(e0 + per, classes);
-    int sum = 0;
-    for (int e = e0; e < e1; ++e) sum += total[e];
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int up = __shfl_up(incl, o, 64);
-      if (lane >= o) incl += up;
-    }
-    int at = incl - sum;
-    for (int e = e0; e < e1; ++e) {
-      const int n = total[e];
-      total[e] = at;
-      if (blockIdx.x == 0) g.offsets[e] = at;
+      const int n = c.wave[w][e];
+      c.wave[w][e] = at;
       at += n;
     }
+    c.all[e] += at;
   }
   __syncthreads();
-  const int64_t s0 = (int64_t)(seg0 + wave) * steps * 64;
-  for (int i = 0; i < steps; i += 4) {  // four slots in flight
+  if (wave == 0) exclusive_sums(c.all, classes, lane);
+  __syncthreads();
+  for (int e = tid; e < classes; e += kSortThreads) {
+    const int start = c.all[e];
+    if (chunk == 0) g.offsets[e] = start;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) c.wave[w][e] += start;
+  }
+  __syncthreads();
+  place_segment<I64, true>(g, seg.s0, seg.s1, bits, c.wave[wave], lane);
+}
+
+template <bool I64>
+__global__ __launch_bounds__(kSortThreads) void expert_sort_count(ExpertSortArgs g, int steps, int bits) {
+  __shared__ SortCounts c;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, classes = g.experts + 1, chunk = blockIdx.x;
+  for (int e = tid; e < classes; e += kSortThreads)
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) c.wave[w][e] = 0;
+  __syncthreads();
+  const Segment seg = segment_of(g, chunk, wave, steps);
+  count_slots<I64>(g, seg.s0 + lane, seg.s1, 64, c.wave[wave]);
+  __syncthreads();
+  for (int e = tid; e < classes; e += kSortThreads) {
+    int at = 0;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int n = c.wave[w][e];
+      c.wave[w][e] = at;
+      at += n;
+    }
+    g.counts[(int64_t)chunk * classes + e] = at;
+  }
+  __syncthreads();
+  place_segment<I64, false>(g, seg.s0, seg.s1, bits, c.wave[wave], lane);
+}
+
+template <bool I64>
+__global__ __launch_bounds__(kSortThreads) void expert_sort_place(ExpertSortArgs g, int chunks, int steps) {
+  __shared__ int before[kMaxExperts + 1], all[kMaxExperts + 1];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, classes = g.experts + 1, chunk = blockIdx.x;
+  for (int e = tid; e < classes; e += kSortThreads) before[e] = all[e] = 0;
+  __syncthreads();
+  // column sums over the chunks: 64 classes by 8 waves at a time, 16 rows in flight
+  for (int e0 = 0; e0 < classes; e0 += 64) {
+    const int e = e0 + lane;
+    int b = 0, a = 0;
+    if (e < classes) {
+      for (int q0 = wave * 16; q0 < chunks; q0 += 16 * kSortWaves) {
+        int n[16];
+#pragma unroll
+        for (int q = 0; q < 16; ++q) n[q] = q0 + q < chunks ? g.counts[(int64_t)(q0 + q) * classes + e] : 0;
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          if (q0 + q < chunk) b += n[q];
+          a += n[q];
+        }
+      }
+      if (b != 0) __hip_atomic_fetch_add(before + e, b, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+      if (a != 0) __hip_atomic_fetch_add(all + e, a, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    }
+  }
+  __syncthreads();
+  if (wave == 0) exclusive_sums(all, classes, lane);
+  __syncthreads();
+  for (int e = tid; e < classes; e += kSortThreads) {
+    if (chunk == 0) g.offsets[e] = all[e];
+    before[e] += all[e];
+  }
+  __syncthreads();
+  const int64_t s0 = segment_of(g, chunk, 0, steps).s0, s1 = segment_of(g, chunk, kSortWaves - 1, steps).s1;
+  for (int64_t at = s0 + tid; at < s1; at += 4 * kSortThreads) {  // four slots in flight
     int v[4], rank[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int64_t s = s0 + 64 * (i + q) + lane;
+      const int64_t s = at + q * kSortThreads;
       v[q] = -1;
-      if (i + q < steps && s < g.n) {
+      if (s < s1) {
         v[q] = slot_class<I64>(g, (int)s);
         rank[q] = g.place[s];
       }
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int s = (int)(s0 + 64 * (i + q) + lane);
+      const int s = (int)(at + q * kSortThreads);
       if (v[q] < 0) continue;
-      const int p = total[v[q]] + start[wave][v[q]] + rank[q];
+      const int p = before[v[q]] + rank[q];
       g.place[s] = v[q] < g.experts ? p : -1;
       g.order[p] = v[q] < g.experts ? s : -1;
     }
@@ -324,23 +369,21 @@ __global__ __launch_bounds__(256) void expert_combine_grad(ExpertRowsArgs g, uin
 
 template <bool I64>
 hipError_t launch_sort(const ExpertSortArgs& g, hipStream_t s) {
-  if (g.n <= kSortOneLaunch) {
-    // about four steps of 64 slots per wave, up to 16 waves
-    const int want = (g.n + 255) / 256, waves = want < 1 ? 1 : want > 16 ? 16 : want;
-    hipLaunchKernelGGL(expert_sort_small<I64>, dim3((unsigned)g.experts + 1), dim3(64 * waves), 0, s, g);
-    return hipGetLastError();
-  }
-  // about 1024 slots a segment
-  const int64_t want = ceil_div(g.n, 1024 * 16) * 16;
-  const int segments = (int)(want < kSortSegments ? want : kSortSegments);
-  const int steps = (int)ceil_div(g.n, (int64_t)segments * 64);
   int bits = 1;
   while ((g.experts >> bits) != 0) ++bits;
-  const dim3 grid(segments / kSortWaves);
-  hipLaunchKernelGGL(expert_sort_count<I64>, grid, dim3(64 * kSortWaves), 0, s, g, steps, bits);
+  const int64_t steps_in_all = ceil_div(g.n, kSortThreads);
+  if (g.n <= kSortOneLaunch) {
+    const unsigned chunks = g.n == 0 ? 1 : (unsigned)steps_in_all;  // one step a wave
+    hipLaunchKernelGGL(expert_sort_one<I64>, dim3(chunks), dim3(kSortThreads), 0, s, g, 1, bits);
+    return hipGetLastError();
+  }
+  // four steps a wave (2048 slots a chunk) up to kSortChunks chunks, then longer ones
+  const int64_t least = ceil_div(steps_in_all, kSortChunks);
+  const int steps = (int)(least < 4 ? 4 : least), chunks = (int)ceil_div(steps_in_all, steps);
+  hipLaunchKernelGGL(expert_sort_count<I64>, dim3(chunks), dim3(kSortThreads), 0, s, g, steps, bits);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(expert_sort_place<I64>, grid, dim3(64 * kSortWaves), 0, s, g, segments, steps);
+  hipLaunchKernelGGL(expert_sort_place<I64>, dim3(chunks), dim3(kSortThreads), 0, s, g, chunks, steps);
   return hipGetLastError();
 }
 

@@ -39,7 +39,7 @@ int check_rows(int64_t tokens, int64_t k, int64_t rows, int64_t H) {
 int finish(hipError_t e) { return e == hipSuccess ? TGEMM_OK : TGEMM_ELAUNCH; }
 
 int64_t sort_workspace(int64_t n, int64_t experts) {
-  return n <= tgemm::kSortOneLaunch ? 0 : (int64_t)tgemm::kSortSegments * (experts + 1) * 4;
+  return n <= tgemm::kSortOneLaunch ? 0 : (int64_t)tgemm::kSortChunks * (experts + 1) * 4;
 }
 
 // The tile kernels copy 16-byte chunks along each operand's contiguous dimension and address a
