@@ -252,6 +252,7 @@ TGEMM_API int expert_gemm_f16_tn(int64_t rows, int64_t experts, int64_t M, int64
 #define TGEMM_EXPERT_128 2  /* TGEMM_EXPERT_TILES held to 128 x 128 tiles */
 #define TGEMM_EXPERT_256 3  /* and to 256 x 256, but for edges of half of one or less */
 #define TGEMM_EXPERT_TILES 4
+#define TGEMM_EXPERT_64 5   /* 64 x 128 tiles; not of the _tn product */
 TGEMM_API int expert_gemm_f16_cfg(int idx, int trans_b, int64_t rows, int64_t experts, int64_t N, int64_t K,
                                   const void* A, int64_t lda, const void* offsets, const void* B, int64_t ldb,
                                   int64_t stride_b, void* C, int64_t ldc, int relu, int zero_rest, void* stream);

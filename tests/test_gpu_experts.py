@@ -203,11 +203,13 @@ GROUPS = {"one_row": groups([1]), "empty_first": groups([0, 5, 0, 1], 3), "ragge
           "wide": groups([257, 300, 511], 1),
           "many": groups(np.random.default_rng(3).integers(0, 4, 200), 9),
           "rounds": groups([900, 700, 3000, 129, 255]),
+          "long": groups([5000, 40, 700]),
           "most": groups(np.random.default_rng(4).integers(0, 2, 1024), 2)}
 SIZES = [(8, 8), (40, 64), (264, 72), (136, 520), (520, 1000)]   # N, K: the tiles' edges, k-tiles of 32 and 64
 ODD = [(1, 1), (129, 65), (258, 131)]
 FORMS = ["nt", "nn", "tn"]
-CONFIGS = [None, tg.EXPERT_GENERIC, tg.EXPERT_32, tg.EXPERT_128, tg.EXPERT_256, tg.EXPERT_TILES]
+CONFIGS = [None, tg.EXPERT_GENERIC, tg.EXPERT_32, tg.EXPERT_128, tg.EXPERT_256, tg.EXPERT_TILES, tg.EXPERT_64]
+ROWS_ONLY = (tg.EXPERT_32, tg.EXPERT_64)   # kernels that the weights' form does not have
 
 
 def stack_with_pad(b, pad, gap):
@@ -253,7 +255,7 @@ def exact_product(form, rng, offsets, rows, N, K, cfg, **kw):
 @pytest.mark.parametrize("cfg", CONFIGS, ids=lambda c: f"cfg{c}")
 @pytest.mark.parametrize("form", FORMS)
 def test_products_exact(gpu, form, cfg):
-    if form == "tn" and cfg == tg.EXPERT_32:
+    if form == "tn" and cfg in ROWS_ONLY:
         pytest.skip("not a kernel of this form")
     rng = np.random.default_rng(11)
     sizes = SIZES if cfg not in (None, tg.EXPERT_GENERIC) else SIZES + ODD
@@ -273,10 +275,10 @@ def test_products_exact(gpu, form, cfg):
 def test_products_debug_fill(gpu, form):
     """The build that fills every LDS copy's destination with NaN first: no read before its copy."""
     rng = np.random.default_rng(12)
-    for cfg in (tg.EXPERT_32, tg.EXPERT_128, tg.EXPERT_256):
-        if form == "tn" and cfg == tg.EXPERT_32:
+    for cfg in CONFIGS[2:]:
+        if form == "tn" and cfg in ROWS_ONLY:
             continue
-        for name in ("ragged", "wide", "empty_first"):
+        for name in ("ragged", "wide", "empty_first", "long"):
             offsets, rows = GROUPS[name]
             for N, K in ((264, 72), (136, 520), (8, 8)):
                 print(f"{form} cfg {cfg} {name} N {N} K {K}", flush=True)
@@ -325,7 +327,7 @@ def test_offsets_outside_the_rows_are_clamped(gpu):
     offsets = np.array([-5, 3, 3, 40, 2 ** 31 - 1], dtype=np.int32)
     for cfg in CONFIGS:
         for form in FORMS:
-            if form == "tn" and cfg == tg.EXPERT_32:
+            if form == "tn" and cfg in ROWS_ONLY:
                 continue
             got, want = exact_product(form, rng, offsets, 70, 136, 64, cfg)
             assert np.array_equal(got, want), (cfg, form)
@@ -359,7 +361,7 @@ def test_products_normal(gpu, cfg):
     relu = run_product("nt", a, b, offsets, N, cfg, relu=True, zero_rest=True)
     assert np.array_equal(relu, np.where(got > 0, got, np.float16(0)))
     assert np.array_equal(run_product("nn", a, np.ascontiguousarray(b.transpose(0, 2, 1)), offsets, N, cfg, zero_rest=True), got)
-    if cfg != tg.EXPERT_32:
+    if cfg not in ROWS_ONLY:
         dc = rng.standard_normal((rows, N)).astype(np.float16)
         got = run_product("tn", dc, a, offsets, K, cfg)
         want = ref.products_tn(dc, a, offsets)

@@ -85,7 +85,7 @@ def gemm(tb=1, rows=100, E=4, N=64, K=32, A=P, lda=32, off=P, B=P, ldb=32, sb=20
     (dict(lda=31), LD), (dict(ldb=31), LD), (dict(tb=0, ldb=63), LD), (dict(ldc=63), LD), (dict(sb=-1), LD),
     (dict(A=None), NULL), (dict(B=None), NULL), (dict(C=None), NULL), (dict(off=None), NULL), (dict(A=P + 1), ALIGN),
     (dict(off=P + 2), ALIGN), (dict(rows=(1 << 31) - 1, N=65536, ldc=65536, sb=1 << 21), DIM),
-    (dict(cfg=5), tg.TGEMM_EINVAL_CFG), (dict(cfg=-1), tg.TGEMM_EINVAL_CFG), (dict(cfg=2, A=P + 2), tg.TGEMM_EINVAL_CFG),
+    (dict(cfg=6), tg.TGEMM_EINVAL_CFG), (dict(cfg=-1), tg.TGEMM_EINVAL_CFG), (dict(cfg=2, A=P + 2), tg.TGEMM_EINVAL_CFG),
     (dict(cfg=1, lda=33), tg.TGEMM_EINVAL_CFG), (dict(cfg=3, sb=2049), tg.TGEMM_EINVAL_CFG),
     (dict(cfg=1, K=0), tg.TGEMM_EINVAL_CFG), (dict(rows=0, A=None), OK), (dict(N=0), OK),
 ])
@@ -101,7 +101,7 @@ def gemm_tn(rows=100, E=4, M=64, N=32, A=P, lda=64, B=P, ldb=32, off=P, C=P, ldc
 @pytest.mark.parametrize("kw,code", [
     (dict(M=-1), DIM), (dict(E=0), DIM), (dict(lda=63), LD), (dict(ldb=31), LD), (dict(ldc=31), LD), (dict(sc=2047), LD),
     (dict(A=None), NULL), (dict(C=None), NULL), (dict(off=None), NULL), (dict(C=P + 1), ALIGN),
-    (dict(M=1 << 22, N=1 << 22, lda=1 << 22, ldb=1 << 22, ldc=1 << 22, sc=1 << 50), DIM), (dict(cfg=tg.EXPERT_32), tg.TGEMM_EINVAL_CFG),
+    (dict(M=1 << 22, N=1 << 22, lda=1 << 22, ldb=1 << 22, ldc=1 << 22, sc=1 << 50), DIM), (dict(cfg=tg.EXPERT_32), tg.TGEMM_EINVAL_CFG), (dict(cfg=tg.EXPERT_64), tg.TGEMM_EINVAL_CFG),
     (dict(cfg=tg.EXPERT_128, M=63), tg.TGEMM_EINVAL_CFG), (dict(M=0), OK), (dict(N=0), OK),
 ])
 def test_weight_product_refusals(kw, code):
@@ -114,7 +114,8 @@ def test_kernel_choice():
         assert f(form, 64, 64, N=2048, K=4096) == tg.EXPERT_32
         assert f(form, 1, 64, N=2048, K=4096) == tg.EXPERT_32
         assert f(form, 16384, 16, N=4096, K=2048) == tg.EXPERT_TILES
-        assert f(form, 1600, 16, N=512, K=512) == tg.EXPERT_TILES
+        assert f(form, 1600, 16, N=512, K=512) == tg.EXPERT_TILES and f(form, 96, 16, N=512, K=512) == tg.EXPERT_32
+        assert f(form, 784, 16, N=512, K=512) == tg.EXPERT_64 and f(form, 783, 16, N=512, K=512) == tg.EXPERT_32
         assert f(form, 64, 8, N=64, K=63) == tg.EXPERT_GENERIC      # K is contiguous in A
         assert f(form, 64, 8, N=64, K=64, A=P + 2) == tg.EXPERT_GENERIC
         assert f(form, 64, 8, N=64, K=64, stride_b=4097) == tg.EXPERT_GENERIC
@@ -129,7 +130,7 @@ def test_header_limits():
     text = open(os.path.join(ROOT, "include", "tgemm_ops.h")).read()
     assert f"#define TGEMM_MAX_EXPERTS {tg.MAX_EXPERTS}" in text and "(((int64_t)1 << 26) - 1024)" in text
     for name, value in (("GENERIC", tg.EXPERT_GENERIC), ("32", tg.EXPERT_32), ("128", tg.EXPERT_128), ("256", tg.EXPERT_256),
-                        ("TILES", tg.EXPERT_TILES)):
+                        ("TILES", tg.EXPERT_TILES), ("64", tg.EXPERT_64)):
         assert re.search(rf"#define TGEMM_EXPERT_{name} {value}\b", text)
 
 

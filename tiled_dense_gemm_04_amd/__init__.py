@@ -836,9 +836,8 @@ from .newton_schulz import NS_COEFFICIENTS, orthogonalize, orthogonalize_workspa
 from . import norm  # noqa: E402
 from .norm import NORM_MAX_K, rmsnorm, rmsnorm_fp8_block  # noqa: E402,F401
 from . import experts  # noqa: E402
-from .experts import (EXPERT_32, EXPERT_128, EXPERT_256, EXPERT_GENERIC, EXPERT_TILES, MAX_EXPERTS, MAX_SLOTS,  # noqa: E402,F401
-                      ExpertOrder,
-                      expert_combine, expert_gather, expert_gemm_f16, expert_gemm_f16_tn, expert_gemm_select_config,
+from .experts import (EXPERT_32, EXPERT_64, EXPERT_128, EXPERT_256, EXPERT_GENERIC, EXPERT_TILES, MAX_EXPERTS,  # noqa: E402,F401
+                      MAX_SLOTS, ExpertOrder,                      expert_combine, expert_gather, expert_gemm_f16, expert_gemm_f16_tn, expert_gemm_select_config,
                       expert_sort)
 
 OPS_SIGNATURES = {**mxfp4.SIGNATURES, **newton_schulz.SIGNATURES, **norm.SIGNATURES, **experts.SIGNATURES}

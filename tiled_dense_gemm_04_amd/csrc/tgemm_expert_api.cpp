@@ -48,12 +48,15 @@ bool chunks(const void* p, int64_t ld, int64_t width) {
   return !off(p, 16) && ld % 8 == 0 && width % 8 == 0 && ld <= TGEMM_FAST_MAX_LD;
 }
 
-// Kernel of a product whose operands the tiles take, by the rows an expert has on average.
-int choose(int form, int64_t rows, int64_t experts, int64_t M, int64_t N) {
+// Kernel of a product whose operands the tiles take, by the rows an expert has on average (uneven
+// experts; microseconds of the tiles of 32 rows, of 64, and of 128 and 256):
+//   32 rows: 111, 119, 139 (64 experts, 2048 x 2048), 15, 19, 18 (8);
+//   64: 142, 127, 136 (64), 42, 39, 53 (16), 20.5, 19.6, 18.8 (8);   96: 176, 141, 144 (64);
+//   128: 212, -, 152 (64), 61, 50, 52 (16).
+int choose(int form, int64_t rows, int64_t experts) {
   const int64_t met = rows < experts ? at_least_1(rows) : experts, each = rows / met;
-  (void)M;
-  (void)N;
-  return form != tgemm::kExpertTN && each <= 48 ? tgemm::kExpert32 : tgemm::kExpertTiles;
+  if (form == tgemm::kExpertTN) return tgemm::kExpertTiles;
+  return each <= 48 ? tgemm::kExpert32 : each <= 96 ? tgemm::kExpert64 : tgemm::kExpertTiles;
 }
 
 int validate(int form, int64_t rows, int64_t experts, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
@@ -87,7 +90,7 @@ int select(int form, int64_t rows, int64_t experts, int64_t M, int64_t N, int64_
   const int v = validate(form, rows, experts, M, N, K, A, lda, offsets, B, ldb, stride_b, C, ldc, stride_c);
   if (v != TGEMM_OK) return v;
   if (N == 0 || (form == tgemm::kExpertTN ? M == 0 : rows == 0)) return kSelectNoop;
-  return tiles_eligible(form, M, N, K, A, lda, B, ldb, stride_b) ? choose(form, rows, experts, M, N) : tgemm::kExpertGeneric;
+  return tiles_eligible(form, M, N, K, A, lda, B, ldb, stride_b) ? choose(form, rows, experts) : tgemm::kExpertGeneric;
 }
 
 int run(int force, int form, int64_t rows, int64_t experts, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
@@ -98,13 +101,13 @@ int run(int force, int form, int64_t rows, int64_t experts, int64_t M, int64_t N
   if (cfg < 0) return cfg;
   if (force >= 0) {
     if (force != tgemm::kExpertGeneric && !tiles_eligible(form, M, N, K, A, lda, B, ldb, stride_b)) return TGEMM_EINVAL_CFG;
-    if (force == tgemm::kExpert32 && form == tgemm::kExpertTN) return TGEMM_EINVAL_CFG;
+    if ((force == tgemm::kExpert32 || force == tgemm::kExpert64) && form == tgemm::kExpertTN) return TGEMM_EINVAL_CFG;
     cfg = force;
   }
   // the runtime takes fewer than 2^32 threads per launch, 512 a workgroup at most; the tile kernel counts
   // its tiles in 32 bits
   if (tgemm::expert_gemm_groups(cfg, form, rows, experts, M, N) >= ((int64_t)1 << 23) ||
-      tgemm::expert_max_tiles(form, rows, experts, M, N) >= ((int64_t)1 << 31))
+      (form != tgemm::kExpertTN && tgemm::expert_max_tiles(rows, experts, N) >= ((int64_t)1 << 31)))
     return TGEMM_EINVAL_DIM;
   int dev = -1;
   const int d = tgemm::current_device(&dev);

@@ -219,8 +219,8 @@ struct Cut {
   __device__ uint32_t small() const { return low_count + right_count; }
 };
 
-// The tiles of a launch, in the order in which its workgroups take them (workgroup w those at w, w +
-// gridDim.x, ...): `kept` big tiles; the other big ones in quarters; the small ones. One big tile
+// The tiles of the rows' form, in the order in which its workgroups take them (workgroup w those at w,
+// w + gridDim.x, ...): `kept` big tiles; the other big ones in quarters; the small ones. One big tile
 // takes about as long as three small ones, so big tiles that would fill less than half of the compute
 // units in a last round go in quarters. (Counts are of 32 bits: the host keeps those of offsets that
 // do not decrease below 2^31, and the length of the list below that bound whatever the offsets hold.)
@@ -247,13 +247,27 @@ struct Tile {
   uint32_t row0, col0;
   RowRange rows;
   bool big;
-};
-
-// The list and, for each lane, what finds a tile in it, in LDS: the registers are the product's.
-struct FinderState {
-  TileList list;
-  uint32_t big_incl[64], small_incl[64];  // rows' form: tiles of a lane's experts and those before
-  int rank[64];                           // weights' form: the place of a lane's expert, most rows first
+  // tile i of the big ones (or quarter 0 .. 3 of it) or of the small ones of a part cut by c
+  __device__ void place(const Cut& c, uint32_t i, bool of_big, uint32_t quarter) {
+    if (of_big) {  // panels of four tile rows, the tile rows of a panel first
+      const uint32_t per_panel = 4 * c.nb, p = i / per_panel, within = i - p * per_panel, height = min(c.mb - 4 * p, 4u);
+      const uint32_t tn = within / height, tm = 4 * p + within - tn * height;
+      row0 = tm * 256 + (quarter < 4 ? 128 * (quarter >> 1) : 0);
+      col0 = tn * 256 + (quarter < 4 ? 128 * (quarter & 1) : 0);
+    } else {
+      const bool lower = i < c.low_count;
+      row0 = lower ? c.low : 128 * (i - c.low_count);
+      col0 = lower ? 128 * i : 256 * c.nb;
+    }
+    big = of_big && quarter == 4;
+  }
+  __device__ void make_uniform() {
+    e = __builtin_amdgcn_readfirstlane(e);
+    rows.first = __builtin_amdgcn_readfirstlane(rows.first);
+    rows.count = __builtin_amdgcn_readfirstlane(rows.count);
+    row0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)row0);
+    col0 = (uint32_t)__builtin_amdgcn_readfirstlane((int)col0);
+  }
 };
 
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)v); }
@@ -269,126 +283,96 @@ __device__ __forceinline__ uint32_t xcd_id(uint32_t at, uint32_t total) {
   return first + x * q + min(x, r) + j;
 }
 
-template <ExpertForm F>
+// The rows' form: the list and what finds a tile in it, in LDS (the registers are the product's).
 struct TileFinder {
-  TG_LDS FinderState* st;
-
-  // (by one wave; a barrier follows)
-  __device__ void init(const ExpertGemmArgs& g, int lane) {
-    TileList list;
-    if constexpr (F == kExpertTN) {
-      const Cut c(g.M, g.N);
-      list.cut(c.big() * g.experts, c.small() * g.experts, g.mode);
-      int rank = lane;
-      if (g.experts <= 64) {
-        const int mine = lane < g.experts ? expert_rows(g, lane).count : -1;
-        rank = 0;
-        for (int j = 0; j < g.experts; ++j) {
-          const int other = __builtin_amdgcn_readlane(mine, j);
-          rank += other > mine || (other == mine && j < lane) ? 1 : 0;
-        }
-      }
-      st->rank[lane] = rank;
-    } else {
-      const int per = (g.experts + 63) / 64, e0 = min(lane * per, g.experts), e1 = min(e0 + per, g.experts);
-      uint32_t big = 0, small = 0;
-      for (int e = e0; e < e1; ++e) {
-        const Cut c(expert_rows(g, e).count, g.N);
-        big += c.big();
-        small += c.small();
-      }
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const uint32_t b = __shfl_up(big, o, 64), s = __shfl_up(small, o, 64);
-        if (lane >= o) {
-          big += b;
-          small += s;
-        }
-      }
-      st->big_incl[lane] = big;
-      st->small_incl[lane] = small;
-      list.cut(__shfl(big, 63, 64), __shfl(small, 63, 64), g.mode);
-    }
-    if (lane == 0) {
-      st->list.kept = list.kept;
-      st->list.quarters = list.quarters;
-      st->list.edges = list.edges;
-    }
-  }
-
-  // Tile `at` of the list into t (uniform); false past its end.
-  __device__ bool get(const ExpertGemmArgs& g, uint32_t at, int lane, Tile& t) const {
-    const uint32_t kept = uniform(st->list.kept), quarters = uniform(st->list.quarters), rest = quarters + uniform(st->list.edges);
-    if (at >= min(kept + rest, g.max_tiles)) return false;
-    // i: which of the big tiles, or of the small ones; a quarter names its big tile
-    uint32_t i, quarter = 4;
-    bool big = true;
-    if (at < kept) {
-      i = xcd_id(at, kept);
-    } else {
-      i = xcd_id(at - kept, rest);
-      big = i < quarters;
-      if (big) {
-        quarter = i & 3;
-        i = kept + i / 4;
-      } else {
-        i -= quarters;
-      }
-    }
-    uint32_t M;
-    int e;
-    if constexpr (F == kExpertTN) {
-      M = g.M;
-      const Cut c(M, g.N);
-      const uint32_t each = big ? c.big() : c.small();
-      e = (int)(i / each);
-      i -= e * each;
-      if (g.experts <= 64) e = __builtin_ctzll(__builtin_amdgcn_ballot_w64(st->rank[lane] == e && lane < g.experts) | 1ull << 63);
-      t.rows = expert_rows(g, min(e, g.experts - 1));
-    } else {
-      const TG_LDS uint32_t* const incl = big ? st->big_incl : st->small_incl;
-      const int per = (g.experts + 63) / 64;
-      const int owner = __builtin_popcountll(__builtin_amdgcn_ballot_w64(incl[lane] <= i));  // lanes whose tiles end before i
-      if (owner > 0) i -= uniform(incl[owner - 1]);
-      e = min(owner * per, g.experts - 1);
-      const int last = min(e + per, g.experts) - 1;
-      t.rows = expert_rows(g, e);
-      for (;;) {
-        const Cut c(t.rows.count, g.N);
-        const uint32_t n = big ? c.big() : c.small();
-        if (i < n || e == last) break;
-        i -= n;
-        t.rows = expert_rows(g, ++e);
-      }
-      M = t.rows.count;
-    }
-    const Cut c(M, g.N);
-    if (big) {  // panels of four tile rows, the tile rows of a panel first
-      const uint32_t per_panel = 4 * c.nb, p = i / per_panel, within = i - p * per_panel, rows = min(c.mb - 4 * p, 4u);
-      const uint32_t tn = within / rows, tm = 4 * p + within - tn * rows;
-      t.row0 = tm * 256 + (quarter < 4 ? 128 * (quarter >> 1) : 0);
-      t.col0 = tn * 256 + (quarter < 4 ? 128 * (quarter & 1) : 0);
-    } else {
-      const bool lower = i < c.low_count;
-      t.row0 = lower ? c.low : 128 * (i - c.low_count);
-      t.col0 = lower ? 128 * i : 256 * c.nb;
-    }
-    t.big = big && quarter == 4;
-    t.e = __builtin_amdgcn_readfirstlane(e);
-    t.rows.first = __builtin_amdgcn_readfirstlane(t.rows.first);
-    t.rows.count = __builtin_amdgcn_readfirstlane(t.rows.count);
-    t.row0 = uniform(t.row0);
-    t.col0 = uniform(t.col0);
-    return true;
-  }
+  TileList list;
+  uint32_t big_incl[64], small_incl[64];  // tiles of a lane's experts and those before
+  int offsets[kMaxExperts + 1];           // clamped
 };
+__device__ __forceinline__ RowRange rows_of(const TG_LDS TileFinder* f, int e) {
+  const int a = f->offsets[e], b = f->offsets[e + 1];
+  return {a, b > a ? b - a : 0};
+}
+
+// By the whole workgroup (a barrier follows).
+__device__ __forceinline__ void init_finder(const ExpertGemmArgs& g, TG_LDS TileFinder* f) {
+  for (int e = threadIdx.x; e <= g.experts; e += 512) f->offsets[e] = clamped(g, e);
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  const int lane = threadIdx.x;
+  const int per = (g.experts + 63) / 64, e0 = min(lane * per, g.experts), e1 = min(e0 + per, g.experts);
+  uint32_t big = 0, small = 0;
+  for (int e = e0; e < e1; ++e) {
+    const Cut c(rows_of(f, e).count, g.N);
+    big += c.big();
+    small += c.small();
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint32_t b = __shfl_up(big, o, 64), s = __shfl_up(small, o, 64);
+    if (lane >= o) {
+      big += b;
+      small += s;
+    }
+  }
+  f->big_incl[lane] = big;
+  f->small_incl[lane] = small;
+  TileList list;
+  list.cut(__shfl(big, 63, 64), __shfl(small, 63, 64), g.mode);
+  if (lane == 0) {
+    f->list.kept = list.kept;
+    f->list.quarters = list.quarters;
+    f->list.edges = list.edges;
+  }
+}
+
+// Tile `at` of the list into t (uniform); false past its end.
+__device__ __forceinline__ bool find_in_rows(const ExpertGemmArgs& g, const TG_LDS TileFinder* f, uint32_t at, int lane, Tile& t) {
+  const uint32_t kept = uniform(f->list.kept), quarters = uniform(f->list.quarters), rest = quarters + uniform(f->list.edges);
+  if (at >= min(kept + rest, g.max_tiles)) return false;
+  // i: which of the big tiles, or of the small ones; a quarter names its big tile
+  uint32_t i, quarter = 4;
+  bool big = true;
+  if (at < kept) {
+    i = xcd_id(at, kept);
+  } else {
+    i = xcd_id(at - kept, rest);
+    big = i < quarters;
+    if (big) {
+      quarter = i & 3;
+      i = kept + i / 4;
+    } else {
+      i -= quarters;
+    }
+  }
+  const TG_LDS uint32_t* const incl = big ? f->big_incl : f->small_incl;
+  const int per = (g.experts + 63) / 64;
+  const int owner = __builtin_popcountll(__builtin_amdgcn_ballot_w64(incl[lane] <= i));  // lanes whose tiles end before i
+  if (owner > 0) i -= uniform(incl[owner - 1]);
+  t.e = min(owner * per, g.experts - 1);
+  const int last = min(t.e + per, g.experts) - 1;
+  for (;;) {
+    t.rows = rows_of(f, t.e);
+    const Cut c(t.rows.count, g.N);
+    const uint32_t n = big ? c.big() : c.small();
+    if (i < n || t.e == last) {
+      t.place(c, i, big, quarter);
+      break;
+    }
+    i -= n;
+    ++t.e;
+  }
+  t.make_uniform();
+  return true;
+}
 
 template <ExpertForm F>
 __global__ __launch_bounds__(512) void expert_tiles(ExpertGemmArgs args) {
+  static_assert(F != kExpertTN, "the rows' form");
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int lane = threadIdx.x & 63;
-  TileFinder<F> finder = {(TG_LDS FinderState*)(smem + kTileLds)};
-  if (threadIdx.x < 64) finder.init(args, lane);
+  TG_LDS TileFinder* const finder = (TG_LDS TileFinder*)(smem + kTileLds);
+  init_finder(args, finder);
   // The arguments are read again for every tile: kept over the loop they would spill.
   typedef const __attribute__((address_space(4))) ExpertGemmArgs KernelArgs;
   KernelArgs* source = (KernelArgs*)__builtin_amdgcn_kernarg_segment_ptr();
@@ -398,45 +382,129 @@ __global__ __launch_bounds__(512) void expert_tiles(ExpertGemmArgs args) {
     __builtin_memcpy(&g, (const void*)source, sizeof(g));
     __syncthreads();  // the list is there, and every wave has stored its part of the tile before
     Tile t;
-    if (!finder.get(g, at, lane, t)) break;
-    const uint32_t M = F == kExpertTN ? g.M : t.rows.count, K = F == kExpertTN ? t.rows.count : g.K;
-    // (offsets that run backwards or change under the launch can leave no such tile)
-    if (t.row0 >= M || t.col0 >= (uint32_t)g.N) continue;
-    const int64_t first = t.rows.first;
-    const _Float16* const A = F == kExpertTN ? g.A + first * g.lda + t.row0 : g.A + (first + t.row0) * g.lda;
-    const _Float16* const B = F == kExpertTN   ? g.B + first * g.ldb + t.col0
-                              : F == kExpertNT ? g.B + t.e * g.stride_b + (int64_t)t.col0 * g.ldb
-                                               : g.B + t.e * g.stride_b + t.col0;
-    _Float16* const C = (F == kExpertTN ? g.C + t.e * g.stride_c : g.C + first * g.ldc) + (int64_t)t.row0 * g.ldc + t.col0;
+    if (!find_in_rows(g, finder, at, lane, t)) break;
+    // (offsets that run backwards can leave no such tile)
+    if (t.row0 >= (uint32_t)t.rows.count || t.col0 >= (uint32_t)g.N) continue;
+    const int64_t first = (int64_t)t.rows.first + t.row0;
+    const _Float16* const A = g.A + first * g.lda;
+    const _Float16* const B = g.B + t.e * g.stride_b + (F == kExpertNT ? (int64_t)t.col0 * g.ldb : t.col0);
+    _Float16* const C = g.C + first * g.ldc + t.col0;
     if (t.big)
-      tile_product<256, F>(g, smem, A, B, C, M - t.row0, g.N - t.col0, K);
+      tile_product<256, F>(g, smem, A, B, C, t.rows.count - t.row0, g.N - t.col0, g.K);
     else
-      tile_product<128, F>(g, smem, A, B, C, M - t.row0, g.N - t.col0, K);
+      tile_product<128, F>(g, smem, A, B, C, t.rows.count - t.row0, g.N - t.col0, g.K);
   }
-  if constexpr (F != kExpertTN) zero_rest<512>(args, blockIdx.x, gridDim.x);
+  zero_rest<512>(args, blockIdx.x, gridDim.x);
 }
 
 // ------------------------------------------------------------------------------------
-// Few rows an expert: 32 x 128 tiles, four waves of 32 columns, k-tiles of 64 through a ring of
-// kStages slots, one barrier each: after the barrier of tile t the copies of tile t + kStages - 1 go
+// The weights' form. Every expert has the same tiles, each as long as the expert has rows, so one
+// with many rows would hold up the launch: a workgroup per tile, the longest first, and where the
+// tiles are few those of the `q` experts of most rows in quarters. q is what makes least the tiles' time
+// spread over the compute units plus half of the longest tile's, in units of a row of a big tile: a big
+// tile of K rows takes K + 190, a quarter 0.47 K + 170 (measured: 5 us and 0.027 a row, 4.5 us and
+// 0.0125 a row). Workgroups past the last tile leave.
+__device__ __forceinline__ bool find_in_weights(const ExpertGemmArgs& g, uint32_t at, int lane, Tile& t) {
+  const Cut c(g.M, g.N);
+  const uint32_t B = c.big(), S = c.small(), E = g.experts;
+  uint32_t q = g.mode == kTilesSmall ? E : 0, rank = lane;
+  if (E <= 64) {
+    const int mine = lane < (int)E ? expert_rows(g, lane).count : -1;
+    rank = 0;
+    for (uint32_t j = 0; j < E; ++j) {
+      const int other = __builtin_amdgcn_readlane(mine, (int)j);
+      rank += other > mine || (other == mine && (int)j < lane) ? 1 : 0;
+    }
+    if (lane >= (int)E) rank = lane;
+    if (g.mode == kTilesAuto) {
+      // lane r: the rows of the r-th longest expert, and of those longer
+      const float K = (float)max(__builtin_amdgcn_ds_permute((int)rank * 4, mine), 0);
+      float longer = K;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const float up = __shfl_up(longer, o, 64);
+        if (lane >= o) longer += up;
+      }
+      const float all = __shfl(longer, 63, 64), top = __shfl(K, 0, 64), n = (float)lane;
+      longer -= K;
+      // lane r prices q = r
+      const float spread = (B * (all - longer + 190.0f * (E - n)) + 4 * B * (0.47f * longer + 170.0f * n) +
+                            S * (0.47f * all + 170.0f * E)) * (1.0f / kExpertTileGroups);
+      const float longest = fmaxf(lane < (int)E ? K + 190.0f : 0.0f, lane > 0 || S > 0 ? 0.47f * top + 170.0f : 0.0f);
+      const float cost = lane > (int)E ? __builtin_inff() : spread + 0.5f * longest;
+      float least = cost;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) least = fminf(least, __shfl_xor(least, o, 64));
+      q = __builtin_ctzll(__builtin_amdgcn_ballot_w64(cost == least) | 1ull << 63);
+      if (q > E) q = E;
+    }
+  }
+  const uint32_t big = (E - q) * B, quarters = 4 * q * B, edges = E * S;
+  uint32_t i, r, quarter = 4;
+  bool of_big = true;
+  if (at < big) {
+    i = xcd_id(at, big);
+    r = i / B;
+    i -= r * B;
+    r += q;
+  } else if (at < big + quarters) {
+    i = xcd_id(at - big, quarters);
+    r = i / (4 * B);
+    i -= r * 4 * B;
+    quarter = i & 3;
+    i /= 4;
+  } else if (at < big + quarters + edges) {
+    i = xcd_id(at - big - quarters, edges);
+    r = i / S;
+    i -= r * S;
+    of_big = false;
+  } else {
+    return false;
+  }
+  t.e = E <= 64 ? (int)__builtin_ctzll(__builtin_amdgcn_ballot_w64(rank == r && lane < (int)E) | 1ull << 63) : (int)r;
+  t.e = min(t.e, g.experts - 1);
+  t.rows = expert_rows(g, t.e);
+  t.place(c, i, of_big, quarter);
+  t.make_uniform();
+  return true;
+}
+
+__global__ __launch_bounds__(512) void expert_tiles_weights(ExpertGemmArgs g) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  Tile t;
+  if (!find_in_weights(g, blockIdx.x, threadIdx.x & 63, t)) return;
+  const int64_t first = t.rows.first;
+  const _Float16* const A = g.A + first * g.lda + t.row0;
+  const _Float16* const B = g.B + first * g.ldb + t.col0;
+  _Float16* const C = g.C + t.e * g.stride_c + (int64_t)t.row0 * g.ldc + t.col0;
+  if (t.big)
+    tile_product<256, kExpertTN>(g, smem, A, B, C, g.M - t.row0, g.N - t.col0, t.rows.count);
+  else
+    tile_product<128, kExpertTN>(g, smem, A, B, C, g.M - t.row0, g.N - t.col0, t.rows.count);
+}
+
+// ------------------------------------------------------------------------------------
+// Few rows an expert: 32 x 128 or 64 x 128 tiles, four waves of 32 columns, k-tiles of 64 through a ring
+// of STAGES slots, one barrier each: after the barrier of tile t the copies of tile t + STAGES - 1 go
 // into the slot of tile t - 1, which every wave has read. Bound by reading the weights of the
 // experts that are met.
-constexpr int kSmallStages = 4;
-template <ExpertForm F>
+template <int BM>
+constexpr int kSmallStages = BM == 32 ? 4 : 3;  // two workgroups a compute unit
+template <int BM_, ExpertForm F>
 struct SmallTile {
-  static constexpr int BM = 32, BN = 128, BK = 64, NW = 4;
+  static constexpr int BM = BM_, BN = 128, BK = 64, NW = 4, STAGES = kSmallStages<BM_>;
   using OpA = PpOperand<BM, BK, 16, true, NW>;
   using OpB = PpOperand<BN, BK, 16, F == kExpertNT, NW>;
-  static constexpr int PT = OpA::LD + OpB::LD, SLOT = OpA::BYTES + OpB::BYTES, LDS = kSmallStages * SLOT;
+  static constexpr int PT = OpA::LD + OpB::LD, SLOT = OpA::BYTES + OpB::BYTES, LDS = STAGES * SLOT;
   static_assert(OpA::REM == 0 && OpB::REM == 0, "copies split evenly");
 };
 
-template <ExpertForm F>
+template <int BM_, ExpertForm F>
 __global__ __launch_bounds__(256) void expert_small(ExpertGemmArgs g) {
-  using T = SmallTile<F>;
+  using T = SmallTile<BM_, F>;
   using OpA = typename T::OpA;
   using OpB = typename T::OpB;
-  constexpr int BM = T::BM, BN = T::BN, BK = T::BK, NW = T::NW, STAGES = kSmallStages;
+  constexpr int BM = T::BM, BN = T::BN, BK = T::BK, NW = T::NW, STAGES = T::STAGES, FM = BM / 16;
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -466,9 +534,9 @@ __global__ __launch_bounds__(256) void expert_small(ExpertGemmArgs g) {
   };
   opa.init_frags(0, lane);
   opb.init_frags(wave * 32, lane);
-  float4v acc[2][2];
+  float4v acc[FM][2];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -481,21 +549,20 @@ __global__ __launch_bounds__(256) void expert_small(ExpertGemmArgs g) {
     const char* const Bs = As + OpA::BYTES;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      half8 fa[2], fb[2];
+      half8 fa[FM], fb[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        fa[i] = opa.frag(As, i, ks);
-        fb[i] = opb.frag(Bs, i, ks);
-      }
+      for (int i = 0; i < FM; ++i) fa[i] = opa.frag(As, i, ks);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) fb[i] = opb.frag(Bs, i, ks);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[j], fa[i], acc[i][j], 0, 0, 0);
     }
   }
   wait_vmcnt<0>();
   __syncthreads();  // the ring is free for staging
-  using ST = StagedTile<32, 32>;
+  using ST = StagedTile<BM, 32>;
   static_assert(NW * ST::BYTES <= T::LDS, "staged tiles");
   char* const stage = smem + wave * ST::BYTES;
   if (g.relu)
@@ -503,7 +570,7 @@ __global__ __launch_bounds__(256) void expert_small(ExpertGemmArgs g) {
   else
     ST::template stage<false>(stage, acc, lane);
   ST::wave_fence();
-  store_staged<ST, 32, false>(stage, lane, g.C + (int64_t)(t.rows.first + row0) * g.ldc + col0 + wave * 32, g.ldc, mvalid,
+  store_staged<ST, BM, false>(stage, lane, g.C + (int64_t)(t.rows.first + row0) * g.ldc + col0 + wave * 32, g.ldc, mvalid,
                               nvalid - wave * 32, g.vec_c);
 }
 
@@ -633,6 +700,11 @@ hipError_t launch(K kern, int threads, int lds, std::atomic<uint64_t>& ready, co
   hipLaunchKernelGGL(kern, dim3(grid), dim3(threads), lds, s, g);
   return hipGetLastError();
 }
+template <int BM, ExpertForm F>
+hipError_t launch_small(const ExpertGemmArgs& g, unsigned grid, hipStream_t s, int device) {
+  static std::atomic<uint64_t> ready{0};
+  return launch(expert_small<BM, F>, 256, SmallTile<BM, F>::LDS, ready, g, grid, s, device);
+}
 template <ExpertForm F>
 hipError_t launch_form(int cfg, const ExpertGemmArgs& g, unsigned grid, hipStream_t s, int device) {
   switch (cfg) {
@@ -640,15 +712,17 @@ hipError_t launch_form(int cfg, const ExpertGemmArgs& g, unsigned grid, hipStrea
     case kExpert128:
     case kExpert256: {
       static std::atomic<uint64_t> ready{0};
-      return launch(expert_tiles<F>, 512, kTileLds + (int)sizeof(FinderState), ready, g, grid, s, device);
+      if constexpr (F == kExpertTN)
+        return launch(expert_tiles_weights, 512, kTileLds, ready, g, grid, s, device);
+      else
+        return launch(expert_tiles<F>, 512, kTileLds + (int)sizeof(TileFinder), ready, g, grid, s, device);
     }
     case kExpert32:
-      if constexpr (F != kExpertTN) {
-        static std::atomic<uint64_t> ready{0};
-        return launch(expert_small<F>, 256, SmallTile<F>::LDS, ready, g, grid, s, device);
-      } else {
+    case kExpert64:
+      if constexpr (F != kExpertTN)
+        return cfg == kExpert32 ? launch_small<32, F>(g, grid, s, device) : launch_small<64, F>(g, grid, s, device);
+      else
         return hipErrorNotSupported;
-      }
     default:
       hipLaunchKernelGGL(expert_generic<F>, dim3(grid), dim3(256), 0, s, g);
       return hipGetLastError();
@@ -660,10 +734,11 @@ hipError_t launch_form(int cfg, const ExpertGemmArgs& g, unsigned grid, hipStrea
 hipError_t launch_expert_gemm(int cfg, ExpertForm form, const ExpertGemmArgs& args, hipStream_t s, int device) {
   ExpertGemmArgs g = args;
   g.mode = cfg == kExpert128 ? kTilesSmall : cfg == kExpert256 ? kTilesBig : kTilesAuto;
-  g.max_tiles = (uint32_t)expert_max_tiles(form, g.rows, g.experts, g.M, g.N);
+  if (form == kExpertTN && cfg == kExpertTiles && !expert_may_quarter(g.rows, g.experts, g.M, g.N)) g.mode = kTilesBig;
+  g.max_tiles = (uint32_t)expert_max_tiles(g.rows, g.experts, g.N);
   const int64_t grid = expert_gemm_groups(cfg, form, g.rows, g.experts, g.M, g.N);
-  g.tiles_m = form == kExpertTN ? (int)ceil_div(g.M, expert_tile_m(cfg)) : 0;
-  g.tiles_n = (int)ceil_div(g.N, expert_tile_n(cfg));
+  g.tiles_m = form == kExpertTN ? (int)ceil_div(g.M, 128) : 0;
+  g.tiles_n = (int)ceil_div(g.N, 128);
   if (form == kExpertNT) return launch_form<kExpertNT>(cfg, g, (unsigned)grid, s, device);
   if (form == kExpertNN) return launch_form<kExpertNN>(cfg, g, (unsigned)grid, s, device);
   return launch_form<kExpertTN>(cfg, g, (unsigned)grid, s, device);

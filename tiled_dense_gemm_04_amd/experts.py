@@ -21,7 +21,7 @@ from .newton_schulz import DTYPE_F16, DTYPE_F32, _stack
 MAX_EXPERTS = 1024                    # TGEMM_MAX_EXPERTS
 MAX_SLOTS = (1 << 26) - 1024          # TGEMM_MAX_SLOTS
 INDEX_I32, INDEX_I64 = 0, 1           # TGEMM_INDEX_*
-EXPERT_GENERIC, EXPERT_32, EXPERT_128, EXPERT_256, EXPERT_TILES = range(5)   # TGEMM_EXPERT_*
+EXPERT_GENERIC, EXPERT_32, EXPERT_128, EXPERT_256, EXPERT_TILES, EXPERT_64 = range(6)   # TGEMM_EXPERT_*
 
 _i64, _p, _i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int
 _GEMM = [_i32, _i64, _i64, _i64, _i64, _p, _i64, _p, _p, _i64, _i64, _p, _i64, _i32, _i32, _p]
