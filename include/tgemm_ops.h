@@ -135,8 +135,8 @@ TGEMM_API int orthogonalize_f16(int64_t batch, int64_t R, int64_t C, int dtype,
  * Each may be NULL, but not Y and Q both; Q and scale go together and residual_out needs a residual
  * (else TGEMM_ENULL). residual_dtype and w_dtype are TGEMM_DTYPE_F16 or TGEMM_DTYPE_F32 (residual
  * NULL: none, its type is not looked at). K is at most TGEMM_NORM_MAX_K, R times the threads of a row
- * (64 up to K = 1024, 256 up to 4096, 512 up to 8192, else 1024) at most 2^32 - 2048, eps at least 0
- * (with 0, a row of zeros gives NaN); else TGEMM_EINVAL_DIM. Pointers need the alignment of their type; no stride or K needs more.
+ * (16 up to K = 128, 32 up to 256, 64 up to 1024, 256 up to 4096, 512 up to 8192, else 1024) at most
+ * 2^32 - 2048, eps at least 0 (with 0, a row of zeros gives NaN); else TGEMM_EINVAL_DIM. Pointers need the alignment of their type; no stride or K needs more.
  * Values of h past 1.8e19 (their squares leave float32) give zeros.
  */
 #define TGEMM_NORM_MAX_K 16384

@@ -22,7 +22,7 @@ def norm(R=4, K=64, X=P, ldx=64, r=None, ldr=64, rt=F16, W=P, wt=F16, eps=1e-6, 
 @pytest.mark.parametrize("kw,code", [
     (dict(R=-1), tg.TGEMM_EINVAL_DIM), (dict(K=-1), tg.TGEMM_EINVAL_DIM), (dict(K=tg.NORM_MAX_K + 1, ldx=1 << 20), tg.TGEMM_EINVAL_DIM),
     (dict(R=1 << 31), tg.TGEMM_EINVAL_DIM), (dict(R=1 << 24, K=4096, ldx=4096, ldy=4096), tg.TGEMM_EINVAL_DIM),
-    (dict(R=1 << 26), tg.TGEMM_EINVAL_DIM), (dict(wt=2), tg.TGEMM_EINVAL_DIM), (dict(r=P, rt=-1), tg.TGEMM_EINVAL_DIM),
+    (dict(R=1 << 28), tg.TGEMM_EINVAL_DIM), (dict(wt=2), tg.TGEMM_EINVAL_DIM), (dict(r=P, rt=-1), tg.TGEMM_EINVAL_DIM),
     (dict(eps=-1.0), tg.TGEMM_EINVAL_DIM), (dict(eps=float("nan")), tg.TGEMM_EINVAL_DIM),
     (dict(ldx=63), tg.TGEMM_EINVAL_LD), (dict(ldy=63), tg.TGEMM_EINVAL_LD), (dict(r=P, ldr=63), tg.TGEMM_EINVAL_LD),
     (dict(r=P, ro=P, ldro=63), tg.TGEMM_EINVAL_LD), (dict(Q=P, s=P, ldq=63), tg.TGEMM_EINVAL_LD),
@@ -48,7 +48,7 @@ def backward(R=4, K=64, dY=P, lddy=64, H=P, ldh=64, ht=F16, W=P, wt=F16, rstd=P,
     (dict(dY=None), tg.TGEMM_ENULL), (dict(H=None), tg.TGEMM_ENULL), (dict(W=None), tg.TGEMM_ENULL),
     (dict(rstd=None), tg.TGEMM_ENULL), (dict(dX=None), tg.TGEMM_ENULL), (dict(ws=None), tg.TGEMM_ENULL),
     (dict(ws=P + 4), tg.TGEMM_EALIGN), (dict(H=P + 2, ht=F32), tg.TGEMM_EALIGN), (dict(dW=P + 1), tg.TGEMM_EALIGN),
-    (dict(dR=P + 2, ht=F32), tg.TGEMM_EALIGN), (dict(nws=4 * 64 * 4 - 1, R=16), tg.TGEMM_EWORKSPACE),
+    (dict(dR=P + 2, ht=F32), tg.TGEMM_EALIGN), (dict(nws=2 * 64 * 4 - 1, R=33), tg.TGEMM_EWORKSPACE),
     (dict(K=0), tg.TGEMM_OK), (dict(R=0, dW=None), tg.TGEMM_OK),
 ])
 def test_backward_refusals(kw, code):
@@ -58,7 +58,7 @@ def test_backward_refusals(kw, code):
 def test_workspace_bytes():
     f = tg.lib().rmsnorm_f16_backward_workspace_bytes
     assert f(0, 64) == 0 and f(5, 0) == 0 and f(-1, 64) == tg.TGEMM_EINVAL_DIM
-    assert f(1, 64) == 64 * 4 and f(16, 64) == 4 * 64 * 4 and f(1 << 20, 4096) == f(1 << 19, 4096) > 0
+    assert f(1, 64) == 64 * 4 and f(33, 64) == 2 * 64 * 4 and f(3, 4096) == 2 * 4096 * 4 and f(1 << 20, 4096) == f(1 << 19, 4096) > 0
 
 
 def test_header_limits():

@@ -7,7 +7,7 @@
 // h is the value that is stored, so that the backward pass, which reads it, is the gradient of what
 // was computed; y stays in float32 until its one rounding (the codes are not made from a rounded
 // binary16 y). Every sum is float32. Both passes are bound by memory: a row is read once, held in
-// the registers of 64 to 1024 threads, eight consecutive values a chunk, and written once.
+// the registers of 16 to 1024 threads, eight consecutive values a chunk, and written once.
 #include "tgemm_device.h"
 #include "tgemm_norm.h"
 #include "tgemm_rows.h"
@@ -15,13 +15,13 @@
 namespace tgemm {
 namespace {
 
-// Sum over the TPR threads of a row (TPR = 64: a wave of its own; else the workgroup, every thread
+// Sum over the TPR threads of a row (up to 64: lanes of one wave; else the workgroup, every thread
 // adding the waves' sums in wave order). `lds` holds a float per wave; a slow wave may still read it
 // when the call returns, so calls that follow each other alternate between two arrays.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* lds) {
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) v += __shfl_xor(v, o, 64);
+  for (int o = 1; o < (TPR < 64 ? TPR : 64); o <<= 1) v += __shfl_xor(v, o, 64);
   if constexpr (TPR > 64) {
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -67,7 +67,9 @@ __device__ __forceinline__ float block_codes(const float (&y)[8], uint2v& codes)
 // ------------------------------------------------------------------------------------
 // Forward. TPR threads a row, CH chunks of eight values a thread: thread t holds chunks t + i TPR,
 // so a 1 x 128 block is 16 neighbouring lanes. The residual, x and the weight of a row are all in
-// flight before the one reduction.
+// flight before the one reduction. 16384 x 4096 with a binary16 residual: 99 us (5.4 TB/s) to binary16, 87
+// to codes (5.4), where a copy of 1 GiB reaches 5.2; 4095 x 3000 with a float32 one 32 (4.6); one row of
+// 4096 3.5 and 4.1 with its launch.
 template <int TPR, int CH, int RES>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_rows(NormArgs g) {
   __shared__ float lds[TPR > 64 ? TPR / 64 : 1];
@@ -141,7 +143,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_rows(NormArgs g
 // ------------------------------------------------------------------------------------
 // Backward. A workgroup takes rows blockIdx.x, + gridDim.x, ... (times its rows at once); a thread
 // keeps its columns' weights and its sums of dw in registers over all of them, and the sums leave
-// as one row of partial sums per workgroup, added in a fixed order by norm_weight_grad.
+// as one row of partial sums per workgroup, added in a fixed order by norm_weight_grad. With that kernel
+// 8192 x 8192 takes 104 us (5.2 TB/s), 16384 x 4096 110, 16384 x 2048 52, 131072 x 128 18.5.
 template <int TPR, int CH, bool H32>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_grad_rows(NormGradArgs g) {
   __shared__ float lds[2][TPR > 64 ? TPR / 64 : 1];
@@ -227,7 +230,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_grad_rows(NormG
   if (g.dW == nullptr) return;
   float* const out = g.parts + (int64_t)blockIdx.x * g.K;
   if constexpr (RPG > 1) {  // the waves' rows are joined, in wave order
-    __shared__ float join[RPG][CH * 512];
+    __shared__ float join[RPG][CH * 8 * TPR];
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
@@ -253,7 +256,7 @@ __global__ __launch_bounds__(1024) void norm_weight_grad(NormGradArgs g) {
   const int k = (int)blockIdx.x * 64 + lane;
   float v = 0.0f;
   if (k < g.K) {
-#pragma unroll 8
+#pragma unroll 16
     for (int p = wave; p < g.groups; p += 16) v += g.parts[(int64_t)p * g.K + k];
   }
   lds[wave][lane] = v;
@@ -269,6 +272,8 @@ __global__ __launch_bounds__(1024) void norm_weight_grad(NormGradArgs g) {
 
 // Threads per row and chunks per thread for rows of K values: NORM_SHAPE(TPR, CH).
 #define TGEMM_NORM_SHAPES(NORM_SHAPE, K)       \
+  if (K <= 128) return NORM_SHAPE(16, 1);      \
+  if (K <= 256) return NORM_SHAPE(32, 1);      \
   if (K <= 512) return NORM_SHAPE(64, 1);      \
   if (K <= 1024) return NORM_SHAPE(64, 2);     \
   if (K <= 2048) return NORM_SHAPE(256, 1);    \
@@ -304,9 +309,13 @@ hipError_t launch_grad(const NormGradArgs& g, hipStream_t s) {
 
 }  // namespace
 
+// Sixteen waves a compute unit (half of them: 16384 x 2048 68 us instead of 52, 16384 x 4096 117 instead
+// of 110), each group at least twice the rows it holds at once (512 x 4096: 14.4 us with one row a group,
+// 11.8 with two, 14.3 with four).
 int norm_grad_groups(int64_t R, int64_t K) {
-  const int64_t at_once = norm_row_threads(K) == 64 ? 4 : 1, want = ceil_div(R, at_once);
-  return (int)(want < kNormGradGroups ? want : kNormGradGroups);
+  const int64_t threads = norm_row_threads(K), group = threads < 256 ? 256 : threads;
+  const int64_t want = ceil_div(R, 2 * (group / threads)), most = 256 * 1024 / group;
+  return (int)(want < most ? want : most);
 }
 
 hipError_t launch_rmsnorm(const NormArgs& g, int residual, hipStream_t s) {
