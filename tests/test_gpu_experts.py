@@ -418,6 +418,23 @@ def test_product_gradients(gpu):
             assert np.array_equal(da.cpu().numpy(), ref.to_half(ref.products(one, b, offsets, False, np.zeros((rows, K)))[0]))
 
 
+def test_broadcast_weight_gradient(gpu):
+    """One matrix expanded over the experts, and one row expanded over a matrix: gradients are summed."""
+    rng = np.random.default_rng(18)
+    offsets, rows = groups([40, 7, 90])
+    a, dc = small_ints(rng, rows, 64), small_ints(rng, rows, 40)
+    one = small_ints(rng, 40, 64)
+    w = to_dev(one).requires_grad_()
+    c = tg.ExpertGemmFunction.apply(to_dev(a), w.expand(3, 40, 64), to_dev(offsets))
+    assert np.array_equal(c.detach().cpu().numpy(), ref.to_half(a.astype(np.float64) @ one.T.astype(np.float64)))
+    dw, = gpu.autograd.grad(c, w, to_dev(dc))
+    each = ref.products_tn(dc, a, offsets)
+    assert np.abs(dw.cpu().numpy() - each.sum(0)).max() <= 2 * np.abs(each).sum(0).max() * ref.HALF16
+    row = to_dev(one[0]).requires_grad_()
+    c = tg.ExpertGemmFunction.apply(to_dev(a), row.expand(3, 40, 64), to_dev(offsets))
+    assert np.array_equal(c.detach().cpu().numpy(), ref.to_half(np.repeat(a.astype(np.float64) @ one[:1].T.astype(np.float64), 40, 1)))
+
+
 # ------------------------------------------------------------------ together
 def layer_inputs(T, k, E, H, F, seed, dropped=0.1):
     rng = np.random.default_rng(seed)
@@ -514,6 +531,19 @@ def test_layer_on_a_stream_and_in_a_graph(gpu):
         graph.replay()
         gpu.cuda.synchronize()
         assert gpu.equal(out[0], eager[0]) and gpu.equal(out[1], eager[1]), seed
+
+
+def test_training_step_on_a_side_stream(gpu):
+    ids, *vals = layer_inputs(130, 2, 8, 264, 136, seed=45)
+    dout = gpu.full((130, 264), 0.5, dtype=gpu.float16, device="cuda")
+    plain = training_step(gpu, [t.clone().requires_grad_() for t in vals], ids, dout)
+    side = gpu.cuda.Stream()
+    side.wait_stream(gpu.cuda.current_stream())
+    with gpu.cuda.stream(side):
+        other = training_step(gpu, [t.clone().requires_grad_() for t in vals], ids, dout)
+    side.synchronize()
+    gpu.cuda.synchronize()
+    assert all(gpu.equal(a, b) for a, b in zip(plain, other))
 
 
 def test_training_step_in_a_graph(gpu):

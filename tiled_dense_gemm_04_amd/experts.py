@@ -154,27 +154,6 @@ def expert_combine(y, plan: ExpertOrder, weights=None, out=None, stream=None, li
     return out
 
 
-def _combine_grad(dout, y, plan, weights, need_y, need_w, zero_rest):
-    """(dy, dweights) of expert_combine, None for what is not wanted."""
-    import torch
-    T, H, lddo = _operand(dout, "dout")
-    device = dout.device
-    place = plan.place
-    k = place.shape[1]
-    rows, _, ldy = _operand(y, "y")
-    w, w_dtype = _weights(weights, (T, k), device)
-    dy = torch.empty((rows, H), dtype=torch.float16, device=device) if need_y else None
-    dw = torch.empty_like(weights) if need_w else None
-    experts = _offsets(plan.offsets, device) if zero_rest else 0
-    rc = _call("expert_combine_f16_backward",
-               (T, k, rows, H, dout.data_ptr(), lddo, y.data_ptr(), ldy, place.data_ptr(), w, w_dtype,
-                dy.data_ptr() if need_y else None, max(1, H), dw.data_ptr() if need_w else None,
-                plan.offsets.data_ptr() if zero_rest else None, experts, _stream(None, device)), device)
-    if rc != TGEMM_OK:
-        raise TgemmError(rc, "expert_combine_f16_backward")
-    return dy, dw
-
-
 def _stacked(b, name):
     import torch
     if isinstance(b, torch.Tensor) and b.dim() != 3:
@@ -248,25 +227,47 @@ def expert_gemm_select_config(form: str, rows, experts, M=0, N=0, K=0, A=256, ld
                                                stride_b))
 
 
-def _same(t, saved, what="a saved-tensor hook"):
-    """t, checked to be what the forward pass saved (the library takes addresses)."""
-    if (t.shape, t.dtype, t.device) != saved:
-        raise RuntimeError(f"{what} returned another tensor than the forward pass saved")
-    return t
-
-
-def _like(t):
-    return t.shape, t.dtype, t.device
-
-
 def _once():
     import torch
     if torch.is_grad_enabled():
         raise RuntimeError("the expert functions have no second derivative (create_graph=True)")
 
 
+def _like(*tensors):
+    return tuple((t.shape, t.dtype, t.device) for t in tensors)
+
+
+def _saved(ctx):
+    """The saved tensors, checked to be what the forward pass saved (the library takes addresses):
+    saved-tensor hooks may return others."""
+    tensors = ctx.saved_tensors
+    if _like(*tensors) != ctx.saved:
+        raise RuntimeError("a saved-tensor hook returned another tensor than the forward pass saved")
+    return tensors
+
+
+def _ld(t):
+    """Row stride of a 2-D tensor with contiguous rows, as the library takes it."""
+    rows, cols = t.shape
+    return t.stride(0) if rows > 1 else cols or 1
+
+
+def _grad(t, name, shape, device):
+    """An incoming gradient as the library takes it."""
+    t = _row_major(t, name)
+    if t.shape != shape or t.device != device:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)} on {device}")
+    return t
+
+
+def _ran(rc, name):
+    if rc != TGEMM_OK:
+        raise TgemmError(rc, name)
+
+
 def autograd_functions():
     import torch
+    f16 = torch.float16
 
     class ExpertGatherFunction(torch.autograd.Function):
         """(x, *plan) -> the sorted rows, those behind the last in use zero; dx[t] is the sum of its rows'
@@ -275,16 +276,22 @@ def autograd_functions():
         @staticmethod
         def forward(ctx, x, offsets, order, place):
             x = _row_major(x, "x")
-            plan = ExpertOrder(offsets, order, place)
-            ctx.save_for_backward(offsets, place)
-            ctx.saved = _like(offsets), _like(place)
-            return expert_gather(x, plan, zero_rest=True)
+            xs = expert_gather(x, ExpertOrder(offsets, order, place), zero_rest=True)
+            ctx.save_for_backward(place)
+            ctx.saved = _like(place)
+            return xs
 
         @staticmethod
         def backward(ctx, dxs):
             _once()
-            offsets, place = (_same(t, s) for t, s in zip(ctx.saved_tensors, ctx.saved))
-            return expert_combine(_row_major(dxs, "dxs"), ExpertOrder(offsets, None, place)), None, None, None
+            place = _saved(ctx)[0].contiguous()
+            (T, k), device = place.shape, place.device
+            H = dxs.shape[1]
+            dxs = _grad(dxs, "dxs", (T * k, H), device)
+            dx = torch.empty((T, H), dtype=f16, device=device)
+            _ran(_call("expert_combine_f16", (T, k, T * k, H, dxs.data_ptr(), _ld(dxs), place.data_ptr(), None, DTYPE_F32,
+                                              dx.data_ptr(), H or 1, _stream(None, device)), device), "expert_combine_f16")
+            return dx, None, None, None
 
     class ExpertCombineFunction(torch.autograd.Function):
         """(y, weights or None, *plan) -> the tokens' weighted sums; gradients of the rows (zero for rows
@@ -294,40 +301,66 @@ def autograd_functions():
         def forward(ctx, y, weights, offsets, order, place):
             y = _row_major(y, "y")
             weights = None if weights is None else weights.contiguous()
+            out = expert_combine(y, ExpertOrder(offsets, order, place), weights)
+            ctx.experts = _offsets(offsets, y.device)
             kept = (offsets, place, y) if weights is None else (offsets, place, y, weights)
             ctx.save_for_backward(*kept)
-            ctx.saved = tuple(_like(t) for t in kept)
-            return expert_combine(y, ExpertOrder(offsets, order, place), weights)
+            ctx.saved = _like(*kept)
+            return out
 
         @staticmethod
         def backward(ctx, dout):
             _once()
-            offsets, place, y, *weights = (_same(t, s) for t, s in zip(ctx.saved_tensors, ctx.saved))
+            offsets, place, y, *weights = (t.contiguous() for t in _saved(ctx))
+            (T, k), (rows, H), device = place.shape, y.shape, y.device
+            dout = _grad(dout, "dout", (T, H), device)
             need_y, need_w = ctx.needs_input_grad[:2]
-            dy, dw = _combine_grad(_row_major(dout, "dout"), _row_major(y, "y"), ExpertOrder(offsets, None, place),
-                                   weights[0].contiguous() if weights else None, need_y, need_w, need_y)
+            dy = torch.empty((rows, H), dtype=f16, device=device) if need_y else None
+            dw = torch.empty_like(weights[0]) if need_w else None
+            w, w_dtype = _weights(weights[0], (T, k), device) if weights else (None, DTYPE_F32)
+            ld = H or 1
+            _ran(_call("expert_combine_f16_backward",
+                       (T, k, rows, H, dout.data_ptr(), _ld(dout), y.data_ptr(), ld, place.data_ptr(), w, w_dtype,
+                        dy.data_ptr() if need_y else None, ld, dw.data_ptr() if need_w else None, offsets.data_ptr(),
+                        ctx.experts, _stream(None, device)), device), "expert_combine_f16_backward")
             return dy, dw, None, None, None
 
     class ExpertGemmFunction(torch.autograd.Function):
-        """c[p] = a[p] @ b[e]^T (no ReLU) for fp16 a (rows, K) and b (E, N, K), rows of no expert zero; da =
-        dc b_e, db_e = dc_e^T a_e."""
+        """c[p] = a[p] @ b[e]^T (no ReLU) for fp16 a (rows, K) and b (E, N, K), rows from offsets[E] on zero
+        (offsets[0] is 0, as expert_sort writes it); da = dc b_e, db_e = dc_e^T a_e."""
 
         @staticmethod
         def forward(ctx, a, b, offsets):
             a = _row_major(a, "a")
-            b = b if b.numel() == 0 or b.stride(-1) == 1 else b.contiguous()
+            if b.dim() == 3 and b.numel() and (b.stride(2) != 1 or b.stride(1) < b.shape[2]):  # a broadcast weight
+                b = b.contiguous()
+            c = expert_gemm_f16(a, b, offsets, zero_rest=True)
             ctx.save_for_backward(a, b, offsets)
-            ctx.saved = _like(a), _like(b), _like(offsets)
-            return expert_gemm_f16(a, b, offsets, zero_rest=True)
+            ctx.saved = _like(a, b, offsets)
+            return c
 
         @staticmethod
         def backward(ctx, dc):
             _once()
-            a, b, offsets = (_same(t, s) for t, s in zip(ctx.saved_tensors, ctx.saved))
-            dc = _row_major(dc, "dc")
+            a, b, offsets = _saved(ctx)
+            a, offsets = _row_major(a, "a"), offsets.contiguous()
+            if b.stride(-1) != 1 or b.stride(1) < b.shape[2]:
+                b = b.contiguous()
+            (rows, K), (E, N, _), device = a.shape, b.shape, a.device
+            dc = _grad(dc, "dc", (rows, N), device)
             need_a, need_b, _ = ctx.needs_input_grad
-            da = expert_gemm_f16(dc, b, offsets, trans_b=False, zero_rest=True) if need_a else None
-            db = expert_gemm_f16_tn(dc, _row_major(a, "a"), offsets) if need_b else None
+            da = db = None
+            stream = _stream(None, device)
+            if need_a:
+                da = torch.empty((rows, K), dtype=f16, device=device)
+                _ran(_call("expert_gemm_f16", (0, rows, E, K, N, dc.data_ptr(), _ld(dc), offsets.data_ptr(), b.data_ptr(),
+                                               b.stride(1) if N > 1 else K or 1, b.stride(0) if E > 1 else 0, da.data_ptr(),
+                                               K or 1, 0, 1, stream), device), "expert_gemm_f16")
+            if need_b:
+                db = torch.empty((E, N, K), dtype=f16, device=device)
+                _ran(_call("expert_gemm_f16_tn", (rows, E, N, K, dc.data_ptr(), _ld(dc), a.data_ptr(), _ld(a),
+                                                  offsets.data_ptr(), db.data_ptr(), K or 1, N * (K or 1), stream), device),
+                     "expert_gemm_f16_tn")
             return da, db, None
 
     return {"ExpertGatherFunction": ExpertGatherFunction, "ExpertCombineFunction": ExpertCombineFunction,

@@ -8,6 +8,7 @@ takes, both beside h where there is a residual.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 from . import FP8_BLOCK, TGEMM_OK, TgemmError, _operand, _operand8, _scale_operand, lib
 from .mxfp4 import _allocating, _call, _row_major, _stream
@@ -148,6 +149,14 @@ def rmsnorm_fp8_block(x, weight, residual=None, eps: float = 1e-6, q=None, scale
     return (q, scale) if residual is None else (q, scale, h)
 
 
+@functools.lru_cache(maxsize=4096)
+def _workspace_bytes(R, K):
+    n = int(lib().rmsnorm_f16_backward_workspace_bytes(R, K))
+    if n < 0:
+        raise TgemmError(n, "rmsnorm_f16_backward_workspace_bytes")
+    return n
+
+
 def _rows(t, name, dtypes):
     """t itself where its rows are contiguous and apart, else a copy (a broadcast gradient)."""
     if t.dtype not in dtypes:
@@ -208,10 +217,9 @@ def autograd_functions():
             dr = torch.empty(shape, dtype=f32, device=device) if need_r and dtype == f32 else None
             dw = workspace = None
             need = 0
-            L = lib()
             if need_w:
                 dw = torch.empty_like(weight)
-                need = L.rmsnorm_f16_backward_workspace_bytes(R, K)
+                need = _workspace_bytes(R, K)
                 workspace = torch.empty(need, dtype=torch.uint8, device=device)
             ld = K or 1
             if dh is not None:
@@ -221,7 +229,7 @@ def autograd_functions():
                         weight.data_ptr(), DTYPE_F32 if weight.dtype == f32 else DTYPE_F16, rstd.data_ptr(),
                         None if dh is None else dh.data_ptr(), 0 if dh is None else _ld(dh), dx.data_ptr(), ld,
                         None if dr is None else dr.data_ptr(), ld, dw.data_ptr() if need_w else None,
-                        workspace.data_ptr() if need else None, need, _stream(None, device)), device, L)
+                        workspace.data_ptr() if need else None, need, _stream(None, device)), device)
             if rc != TGEMM_OK:
                 raise TgemmError(rc, "rmsnorm_f16_backward")
             if need_r and dr is None:
