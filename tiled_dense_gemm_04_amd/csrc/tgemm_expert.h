@@ -57,33 +57,20 @@ enum ExpertForm { kExpertNT = 0, kExpertNN = 1, kExpertTN = 2 };
 // edges).
 enum ExpertConfig { kExpertGeneric = 0, kExpert32 = 1, kExpert128 = 2, kExpert256 = 3, kExpertTiles = 4, kExpert64 = 5, kExpertConfigs = 6 };
 enum ExpertTileMode { kTilesAuto = 0, kTilesSmall = 1, kTilesBig = 2 };
-constexpr int kExpertTileGroups = 256;  // workgroups of the tile kernel's rows' form, each of which goes over tiles: one a compute unit
-// Whether tiles of the weights' form may be in quarters: where the big ones are few (three rounds) and
-// long (512 rows on average). The launch then has a workgroup for every quarter, and the ones not needed
-// cost 2 us in 256 (4096 rows, 32 experts, 1024 x 512: 19.7 us without, 25.4 with them; 8190 rows, 8
-// experts, 1032 x 2048: 71 and 61).
-inline bool expert_may_quarter(int64_t rows, int64_t experts, int64_t M, int64_t N) {
-  return experts <= 64 && rows >= 512 * experts && experts * ((M + 127) / 256) * ((N + 127) / 256) <= 768;
-}
+constexpr int kExpertTileGroups = 256;  // workgroups of the tile kernel, each of which goes over tiles: one a compute unit
 constexpr int expert_tile_m(int cfg) { return cfg == kExpert32 ? 32 : cfg == kExpert64 ? 64 : 128; }
 // Workgroups of a launch. The rows' form of the others has one a tile: c rows of an expert need ceil(c
 // / BM) tile rows, so all of them at most rows / BM + the number of experts that have one; and one
 // tile row more where the rows behind the last group are to be zeroed by workgroups of no tile.
 inline int64_t expert_gemm_groups(int cfg, int form, int64_t rows, int64_t experts, int64_t M, int64_t N) {
   const int64_t tn = ceil_div(N, 128);
-  if (form == kExpertTN) {
-    if (cfg < kExpert128) return experts * ceil_div(M, 128) * tn;
-    // big tiles (in quarters, where some may be) and the small ones of the lower and the right edge
-    const int64_t mb = (M + 127) / 256, nb = (N + 127) / 256, big = experts * mb * nb;
-    const int64_t low = M > mb * 256 ? tn : 0, right = N > nb * 256 ? ceil_div(M < mb * 256 ? M : mb * 256, 128) : 0;
-    const bool quarters = cfg == kExpert128 || (cfg == kExpertTiles && expert_may_quarter(rows, experts, M, N));
-    return (quarters ? 4 : 1) * big + experts * (low + right);
-  }
   if (cfg == kExpert128 || cfg == kExpert256 || cfg == kExpertTiles) return kExpertTileGroups;
+  if (form == kExpertTN) return experts * ceil_div(M, 128) * tn;
   return (rows / expert_tile_m(cfg) + (experts < rows ? experts : rows) + 1) * tn;
 }
-// The most 128 x 128 tiles that any division of the rows gives the tile kernel's rows' form.
-inline int64_t expert_max_tiles(int64_t rows, int64_t experts, int64_t N) {
+// The most 128 x 128 tiles that the tile kernel has, whatever the division of the rows.
+inline int64_t expert_max_tiles(int form, int64_t rows, int64_t experts, int64_t M, int64_t N) {
+  if (form == kExpertTN) return experts * (ceil_div(M, 128) + 1) * (ceil_div(N, 128) + 1);
   return (rows / 128 + 2 * (experts < rows ? experts : rows)) * (ceil_div(N, 128) + 1);
 }
 hipError_t launch_expert_gemm(int cfg, ExpertForm form, const ExpertGemmArgs& g, hipStream_t s, int device);

@@ -107,7 +107,7 @@ int run(int force, int form, int64_t rows, int64_t experts, int64_t M, int64_t N
   // the runtime takes fewer than 2^32 threads per launch, 512 a workgroup at most; the tile kernel counts
   // its tiles in 32 bits
   if (tgemm::expert_gemm_groups(cfg, form, rows, experts, M, N) >= ((int64_t)1 << 23) ||
-      (form != tgemm::kExpertTN && tgemm::expert_max_tiles(rows, experts, N) >= ((int64_t)1 << 31)))
+      tgemm::expert_max_tiles(form, rows, experts, M, N) >= ((int64_t)1 << 31))
     return TGEMM_EINVAL_DIM;
   int dev = -1;
   const int d = tgemm::current_device(&dev);

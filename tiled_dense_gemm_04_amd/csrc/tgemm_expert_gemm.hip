@@ -3,11 +3,15 @@
 //
 //   rows (NT, NN):  C[p, :] = ReLU?(A[p, :] op(B_e)) for offsets[e] <= p < offsets[e + 1];
 //   weights (TN):   C_e = A_e^T B_e, the sum over the expert's rows (zeros for an expert of none).
-// Nothing about the groups is known to the host, so a launch of the rows' form has a workgroup for
-// every tile that any division of the rows could need (rows / BM + E tile rows); a workgroup finds
-// its expert by a sum over the offsets, one lane per 1 / 64 of the experts, and those past the last
-// tile leave at once (or zero the rows behind the last group). Offsets are clamped to [0, rows]: no
-// value of theirs leads outside the operands.
+// Nothing about the groups is known to the host. The tile kernels run one workgroup a compute unit, each
+// of which finds the tiles it goes over from the offsets (expert_tiles, expert_tiles_weights); the ones
+// for few rows have a workgroup for every tile that any division of the rows could need, and those
+// past the last tile leave at once (or zero the rows behind the last group). Offsets are clamped to [0,
+// rows]: no value of theirs leads outside the operands.
+// What bounds them: the binary16 MFMAs at their power limit and the rounds of tiles (uneven experts, 16384
+// rows on 16 of them, 4096 x 2048: rows' form 281 us with B N x K and 266 with K x N, weights' form 284, of
+// 275 GFLOP; one expert 264, the dense kernel of this library 271); with few rows an expert, reading the
+// weights (64 rows on 64 experts of 2048 x 4096, about 36 of them met: 109 us, 5.5 TB/s).
 #include "tgemm_expert.h"
 #include "tgemm_pingpong.h"
 #include "tgemm_rows.h"
@@ -398,70 +402,117 @@ __global__ __launch_bounds__(512) void expert_tiles(ExpertGemmArgs args) {
 }
 
 // ------------------------------------------------------------------------------------
-// The weights' form. Every expert has the same tiles, each as long as the expert has rows, so one
-// with many rows would hold up the launch: a workgroup per tile, the longest first, and where the
-// tiles are few those of the `q` experts of most rows in quarters. q is what makes least the tiles' time
-// spread over the compute units plus half of the longest tile's, in units of a row of a big tile: a big
-// tile of K rows takes K + 190, a quarter 0.47 K + 170 (measured: 5 us and 0.027 a row, 4.5 us and
-// 0.0125 a row). Workgroups past the last tile leave.
-__device__ __forceinline__ bool find_in_weights(const ExpertGemmArgs& g, uint32_t at, int lane, Tile& t) {
+// The weights' form. Every expert has the same tiles, each as long as the expert has rows, so the tiles
+// are taken in the order of their time, forth and back over the workgroups (those that had a long tile
+// in one round have a short one in the next), and the big ones of the `q` experts of most rows go in
+// quarters. In units of a row of a big tile, a big tile of K rows takes K + 170 and a small one 0.3 K +
+// 170 (measured: 4 us and 0.024 a row, 4 us and 0.0072 a row); q is what makes least the tiles' time spread
+// over the compute units plus half of the longest one's. (A workgroup per tile, which the hardware
+// hands to the next free compute unit, costs 5 us more a tile: 16384 rows, 16 experts, 2048 x 1024: 99 to
+// 123 us.) More than 64 experts are taken as they come, in big tiles.
+struct WeightTiles {
+  uint32_t total, q;
+  int expert[64];                                      // of rank r, most rows first
+  uint32_t big_at[64], bigs[64], small_at[64], smalls[64];  // where its tiles come in the list
+};
+// By the first wave (a barrier follows).
+__device__ __forceinline__ void init_weights(const ExpertGemmArgs& g, TG_LDS WeightTiles* f, int lane) {
   const Cut c(g.M, g.N);
   const uint32_t B = c.big(), S = c.small(), E = g.experts;
-  uint32_t q = g.mode == kTilesSmall ? E : 0, rank = lane;
-  if (E <= 64) {
-    const int mine = lane < (int)E ? expert_rows(g, lane).count : -1;
-    rank = 0;
-    for (uint32_t j = 0; j < E; ++j) {
-      const int other = __builtin_amdgcn_readlane(mine, (int)j);
-      rank += other > mine || (other == mine && (int)j < lane) ? 1 : 0;
-    }
-    if (lane >= (int)E) rank = lane;
-    if (g.mode == kTilesAuto) {
-      // lane r: the rows of the r-th longest expert, and of those longer
-      const float K = (float)max(__builtin_amdgcn_ds_permute((int)rank * 4, mine), 0);
-      float longer = K;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const float up = __shfl_up(longer, o, 64);
-        if (lane >= o) longer += up;
-      }
-      const float all = __shfl(longer, 63, 64), top = __shfl(K, 0, 64), n = (float)lane;
-      longer -= K;
-      // lane r prices q = r
-      const float spread = (B * (all - longer + 190.0f * (E - n)) + 4 * B * (0.47f * longer + 170.0f * n) +
-                            S * (0.47f * all + 170.0f * E)) * (1.0f / kExpertTileGroups);
-      const float longest = fmaxf(lane < (int)E ? K + 190.0f : 0.0f, lane > 0 || S > 0 ? 0.47f * top + 170.0f : 0.0f);
-      const float cost = lane > (int)E ? __builtin_inff() : spread + 0.5f * longest;
-      float least = cost;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) least = fminf(least, __shfl_xor(least, o, 64));
-      q = __builtin_ctzll(__builtin_amdgcn_ballot_w64(cost == least) | 1ull << 63);
-      if (q > E) q = E;
-    }
+  if (E > 64) {
+    if (lane == 0) f->total = E * ((g.mode == kTilesSmall ? 4 * B : B) + S);
+    return;
   }
-  const uint32_t big = (E - q) * B, quarters = 4 * q * B, edges = E * S;
-  uint32_t i, r, quarter = 4;
-  bool of_big = true;
-  if (at < big) {
-    i = xcd_id(at, big);
-    r = i / B;
-    i -= r * B;
-    r += q;
-  } else if (at < big + quarters) {
-    i = xcd_id(at - big, quarters);
-    r = i / (4 * B);
-    i -= r * 4 * B;
-    quarter = i & 3;
-    i /= 4;
-  } else if (at < big + quarters + edges) {
-    i = xcd_id(at - big - quarters, edges);
-    r = i / S;
-    i -= r * S;
-    of_big = false;
+  const bool real = lane < (int)E;
+  const int mine = real ? expert_rows(g, lane).count : -1;
+  uint32_t rank = 0;
+  for (uint32_t j = 0; j < E; ++j) {
+    const int other = __builtin_amdgcn_readlane(mine, (int)j);
+    rank += other > mine || (other == mine && (int)j < lane) ? 1 : 0;
+  }
+  if (!real) rank = lane;
+  f->expert[rank] = lane;
+  // lane r: the rows of the r-th longest expert
+  const float K = (float)max(__builtin_amdgcn_ds_permute((int)rank * 4, mine), 0);
+  uint32_t q = g.mode == kTilesSmall ? E : 0;
+  if (g.mode == kTilesAuto) {
+    float longer = K;  // rows of those longer
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const float up = __shfl_up(longer, o, 64);
+      if (lane >= o) longer += up;
+    }
+    const float all = __shfl(longer, 63, 64), top = __shfl(K, 0, 64), n = (float)lane;
+    longer -= K;
+    // lane r prices q = r
+    const float spread = (B * (all - longer + 170.0f * (E - n)) + 4 * B * (0.3f * longer + 170.0f * n) +
+                          S * (0.3f * all + 170.0f * E)) * (1.0f / kExpertTileGroups);
+    const float longest = fmaxf(real ? K + 170.0f : 0.0f, lane > 0 || S > 0 ? 0.3f * top + 170.0f : 0.0f);
+    const float cost = lane > (int)E ? __builtin_inff() : spread + 0.5f * longest;
+    float least = cost;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) least = fminf(least, __shfl_xor(least, o, 64));
+    q = min((uint32_t)__builtin_ctzll(__builtin_amdgcn_ballot_w64(cost == least) | 1ull << 63), E);
+  }
+  // Big and small tiles each lie in the order of their time, rank by rank: where a rank's come among
+  // those of the other kind is a search.
+  const float big_time = K + 170.0f, small_time = 0.3f * K + 170.0f;
+  auto bigs_before = [&](uint32_t r) { return r > q ? (r - q) * B : 0; };   // of the ranks below r
+  auto smalls_before = [&](uint32_t r) { return 4 * B * min(r, q) + S * r; };
+  uint32_t smalls_longer = 0, bigs_longer = 0;  // ranks whose small (big) tiles come before this one's big (small)
+  for (int step = 32, last = 0; last < 2; last += step == 1, step = step > 1 ? step / 2 : 1) {
+    const uint32_t a = smalls_longer + step - 1, b = bigs_longer + step - 1;
+    const float ta = __shfl(small_time, (int)(a & 63), 64), tb = __shfl(big_time, (int)(b & 63), 64);
+    smalls_longer += a < E && ta > big_time ? step : 0;
+    bigs_longer += b < E && tb >= small_time ? step : 0;
+  }
+  f->big_at[lane] = bigs_before(lane) + smalls_before(smalls_longer);
+  f->bigs[lane] = real && (uint32_t)lane >= q ? B : 0;
+  f->small_at[lane] = smalls_before(lane) + bigs_before(bigs_longer);
+  f->smalls[lane] = real ? ((uint32_t)lane < q ? 4 * B : 0) + S : 0;
+  if (lane == 0) {
+    f->total = bigs_before(E) + smalls_before(E);
+    f->q = q;
+  }
+}
+
+// The tile of workgroup blockIdx.x in round `round` into t (uniform); false past the last.
+__device__ __forceinline__ bool find_in_weights(const ExpertGemmArgs& g, const TG_LDS WeightTiles* f, uint32_t round, int lane,
+                                                Tile& t) {
+  constexpr uint32_t G = kExpertTileGroups;
+  const Cut c(g.M, g.N);
+  const uint32_t B = c.big(), S = c.small(), total = uniform(f->total), first = round * G;
+  if (first + blockIdx.x >= total) return false;
+  uint32_t at = xcd_id(first + blockIdx.x, total);
+  if (round & 1) at = first + min(G, total - first) - 1 - (at - first);
+  uint32_t i, quarter = 4, quarters;  // quarters of the tile's expert
+  bool of_big;
+  if (g.experts > 64) {
+    quarters = g.mode == kTilesSmall ? 4 * B : 0;
+    const uint32_t each = (quarters > 0 ? quarters : B) + S;
+    t.e = (int)(at / each);
+    i = at - t.e * each;
+    of_big = quarters == 0 && i < B;
+    if (quarters == 0 && !of_big) i -= B;
   } else {
-    return false;
+    const uint32_t big_at = f->big_at[lane], small_at = f->small_at[lane];
+    const uint64_t in_big = __builtin_amdgcn_ballot_w64(at - big_at < f->bigs[lane]);  // (unsigned: from its start on)
+    const uint64_t in_small = __builtin_amdgcn_ballot_w64(at - small_at < f->smalls[lane]);
+    of_big = in_big != 0;
+    const int r = (int)__builtin_ctzll((of_big ? in_big : in_small) | 1ull << 63);
+    i = at - (uint32_t)__builtin_amdgcn_readlane((int)(of_big ? big_at : small_at), r);
+    quarters = (uint32_t)r < uniform(f->q) ? 4 * B : 0;
+    t.e = f->expert[r];
   }
-  t.e = E <= 64 ? (int)__builtin_ctzll(__builtin_amdgcn_ballot_w64(rank == r && lane < (int)E) | 1ull << 63) : (int)r;
+  if (!of_big) {
+    of_big = i < quarters;
+    if (of_big) {
+      quarter = i & 3;
+      i /= 4;
+    } else {
+      i -= quarters;
+    }
+  }
   t.e = min(t.e, g.experts - 1);
   t.rows = expert_rows(g, t.e);
   t.place(c, i, of_big, quarter);
@@ -469,25 +520,37 @@ __device__ __forceinline__ bool find_in_weights(const ExpertGemmArgs& g, uint32_
   return true;
 }
 
-__global__ __launch_bounds__(512) void expert_tiles_weights(ExpertGemmArgs g) {
+__global__ __launch_bounds__(512) void expert_tiles_weights(ExpertGemmArgs args) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  Tile t;
-  if (!find_in_weights(g, blockIdx.x, threadIdx.x & 63, t)) return;
-  const int64_t first = t.rows.first;
-  const _Float16* const A = g.A + first * g.lda + t.row0;
-  const _Float16* const B = g.B + first * g.ldb + t.col0;
-  _Float16* const C = g.C + t.e * g.stride_c + (int64_t)t.row0 * g.ldc + t.col0;
-  if (t.big)
-    tile_product<256, kExpertTN>(g, smem, A, B, C, g.M - t.row0, g.N - t.col0, t.rows.count);
-  else
-    tile_product<128, kExpertTN>(g, smem, A, B, C, g.M - t.row0, g.N - t.col0, t.rows.count);
+  const int lane = threadIdx.x & 63;
+  TG_LDS WeightTiles* const tiles = (TG_LDS WeightTiles*)(smem + kTileLds);
+  if (threadIdx.x < 64) init_weights(args, tiles, lane);
+  typedef const __attribute__((address_space(4))) ExpertGemmArgs KernelArgs;  // (as in expert_tiles)
+  KernelArgs* source = (KernelArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  for (uint32_t round = 0;; ++round) {
+    asm volatile("" : "+s"(source));
+    ExpertGemmArgs g;
+    __builtin_memcpy(&g, (const void*)source, sizeof(g));
+    __syncthreads();  // the list is there, and every wave has stored its part of the tile before
+    Tile t;
+    if (!find_in_weights(g, tiles, round, lane, t)) break;
+    const int64_t first = t.rows.first;
+    const _Float16* const A = g.A + first * g.lda + t.row0;
+    const _Float16* const B = g.B + first * g.ldb + t.col0;
+    _Float16* const C = g.C + t.e * g.stride_c + (int64_t)t.row0 * g.ldc + t.col0;
+    if (t.big)
+      tile_product<256, kExpertTN>(g, smem, A, B, C, g.M - t.row0, g.N - t.col0, t.rows.count);
+    else
+      tile_product<128, kExpertTN>(g, smem, A, B, C, g.M - t.row0, g.N - t.col0, t.rows.count);
+  }
 }
 
 // ------------------------------------------------------------------------------------
 // Few rows an expert: 32 x 128 or 64 x 128 tiles, four waves of 32 columns, k-tiles of 64 through a ring
 // of STAGES slots, one barrier each: after the barrier of tile t the copies of tile t + STAGES - 1 go
 // into the slot of tile t - 1, which every wave has read. Bound by reading the weights of the
-// experts that are met.
+// experts that are met: 2048 rows on 64 experts of 2048 x 2048 (32 rows a tile) 111 us, 4096 rows (64 rows
+// a tile) 127, of 537 MB of weights (98 us at a copy's rate).
 template <int BM>
 constexpr int kSmallStages = BM == 32 ? 4 : 3;  // two workgroups a compute unit
 template <int BM_, ExpertForm F>
@@ -576,7 +639,7 @@ __global__ __launch_bounds__(256) void expert_small(ExpertGemmArgs g) {
 
 // ------------------------------------------------------------------------------------
 // Any alignment, stride and size: 128 x 128 tiles, four waves of 64 x 64, 32 k at a time through a
-// double-buffered LDS tile filled through registers.
+// double-buffered LDS tile filled through registers. Bound by those loads.
 template <ExpertForm F>
 __global__ __launch_bounds__(256) void expert_generic(ExpertGemmArgs g) {
   constexpr int BM = 128, ROW = 40;  // halves per LDS row: 16-byte aligned, rows spread over the banks
@@ -713,7 +776,7 @@ hipError_t launch_form(int cfg, const ExpertGemmArgs& g, unsigned grid, hipStrea
     case kExpert256: {
       static std::atomic<uint64_t> ready{0};
       if constexpr (F == kExpertTN)
-        return launch(expert_tiles_weights, 512, kTileLds, ready, g, grid, s, device);
+        return launch(expert_tiles_weights, 512, kTileLds + (int)sizeof(WeightTiles), ready, g, grid, s, device);
       else
         return launch(expert_tiles<F>, 512, kTileLds + (int)sizeof(TileFinder), ready, g, grid, s, device);
     }
@@ -734,8 +797,7 @@ hipError_t launch_form(int cfg, const ExpertGemmArgs& g, unsigned grid, hipStrea
 hipError_t launch_expert_gemm(int cfg, ExpertForm form, const ExpertGemmArgs& args, hipStream_t s, int device) {
   ExpertGemmArgs g = args;
   g.mode = cfg == kExpert128 ? kTilesSmall : cfg == kExpert256 ? kTilesBig : kTilesAuto;
-  if (form == kExpertTN && cfg == kExpertTiles && !expert_may_quarter(g.rows, g.experts, g.M, g.N)) g.mode = kTilesBig;
-  g.max_tiles = (uint32_t)expert_max_tiles(g.rows, g.experts, g.N);
+  g.max_tiles = (uint32_t)expert_max_tiles(form, g.rows, g.experts, g.M, g.N);
   const int64_t grid = expert_gemm_groups(cfg, form, g.rows, g.experts, g.M, g.N);
   g.tiles_m = form == kExpertTN ? (int)ceil_div(g.M, 128) : 0;
   g.tiles_n = (int)ceil_div(g.N, 128);
