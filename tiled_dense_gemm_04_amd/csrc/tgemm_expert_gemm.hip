@@ -638,14 +638,19 @@ __global__ __launch_bounds__(256) void expert_small(ExpertGemmArgs g) {
 }
 
 // ------------------------------------------------------------------------------------
-// Any alignment, stride and size: 128 x 128 tiles, four waves of 64 x 64, 32 k at a time through a
-// double-buffered LDS tile filled through registers. Bound by those loads.
+// Any alignment, stride and size: 128 x 128 tiles, four waves of 64 x 64, k-tiles of 64 through two LDS
+// slots in the layout of the tile kernels (PpOperand), but filled through registers: loads of any
+// address, cut by the rows' ends. Bound by their latency, of which one k-tile's products cover a part.
 template <ExpertForm F>
 __global__ __launch_bounds__(256) void expert_generic(ExpertGemmArgs g) {
-  constexpr int BM = 128, ROW = 40;  // halves per LDS row: 16-byte aligned, rows spread over the banks
-  __shared__ __attribute__((aligned(16))) _Float16 at[2][BM * ROW], bt[2][BM * ROW];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64, lrow = lane & 15, lkg = lane >> 4;
+  constexpr int BM = 128, BK = 64;
+  using OpA = PpOperand<BM, BK, 16, F != kExpertTN, 4>;
+  using OpB = PpOperand<BM, BK, 16, F == kExpertNT, 4>;
+  constexpr int UNITS = OpA::UNITS / 256;  // 16-byte units a thread and operand
+  static_assert(OpA::UNITS == 1024 && OpB::UNITS == 1024, "units split evenly");
+  __shared__ __attribute__((aligned(16))) char smem[2 * (OpA::BYTES + OpB::BYTES)];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   int row0, col0, mvalid, K;
   const _Float16 *A, *B;
   _Float16* C;
@@ -656,8 +661,8 @@ __global__ __launch_bounds__(256) void expert_generic(ExpertGemmArgs g) {
     col0 = t % g.tiles_n * BM;
     mvalid = g.M - row0;
     K = r.count;
-    A = g.A + (int64_t)r.first * g.lda;
-    B = g.B + (int64_t)r.first * g.ldb;
+    A = g.A + (int64_t)r.first * g.lda + row0;
+    B = g.B + (int64_t)r.first * g.ldb + col0;
     C = g.C + e * g.stride_c;
   } else {
     const RowTile t = find_tile<BM, 4>(g, lane);
@@ -666,88 +671,81 @@ __global__ __launch_bounds__(256) void expert_generic(ExpertGemmArgs g) {
     col0 = t.tn * BM;
     mvalid = t.rows.count - row0;
     K = g.K;
-    A = g.A + (int64_t)t.rows.first * g.lda;
-    B = g.B + t.e * g.stride_b;
+    A = g.A + ((int64_t)t.rows.first + row0) * g.lda;
+    B = g.B + t.e * g.stride_b + (F == kExpertNT ? (int64_t)col0 * g.ldb : col0);
     C = g.C + (int64_t)t.rows.first * g.ldc;
   }
   const int nvalid = g.N - col0;
-  // An operand's tile, two chunks of eight values a thread: along k of row tid / 2 where k is
-  // contiguous, else along the rows of k = (2 tid + h) / 16.
-  half8 av[2], bv[2];
-  auto fetch = [&](auto kmaj, const _Float16* X, int64_t ld, int r0, int valid, int kt, half8 (&v)[2]) {
+  // Unit u of a k-tile lies at byte 16 u of the slot and holds the chunk that the swizzle puts there.
+  auto fetch = [&](auto op, const _Float16* X, int64_t ld, int valid, int kt, half8 (&v)[UNITS]) __attribute__((always_inline)) {
+    using Op = decltype(op);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if constexpr (decltype(kmaj)::value) {
-        const int r = tid >> 1, k = 32 * kt + 16 * (tid & 1) + 8 * h;
-        v[h] = load_half8(X + (int64_t)(r0 + r) * ld + k, r < valid ? K - k : 0);
-      } else {
-        const int u = 2 * tid + h, k = 32 * kt + u / 16, r = 8 * (u % 16);
-        v[h] = load_half8(X + (int64_t)k * ld + r0 + r, k < K ? valid - r : 0);
-      }
+    for (int i = 0; i < UNITS; ++i) {
+      const int u = i * 256 + tid, line = u / Op::CPR, c = 8 * ((u % Op::CPR) ^ Op::swz(line));
+      const int k = BK * kt + (Op::KMAJOR ? c : line), r = Op::KMAJOR ? line : c;
+      v[i] = Op::KMAJOR ? load_half8(X + (int64_t)r * ld + k, r < valid ? K - k : 0)
+                        : load_half8(X + (int64_t)k * ld + r, k < K ? valid - r : 0);
     }
   };
-  auto put = [&](auto kmaj, _Float16* tile, const half8 (&v)[2]) {
+  auto put = [&](char* slot, const half8 (&v)[UNITS]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if constexpr (decltype(kmaj)::value) {
-        *(half8*)&tile[(tid >> 1) * ROW + 16 * (tid & 1) + 8 * h] = v[h];
-      } else {
-        const int u = 2 * tid + h;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) tile[(8 * (u % 16) + e) * ROW + u / 16] = v[h][e];
-      }
-    }
+    for (int i = 0; i < UNITS; ++i) *(TG_LDS half8*)(slot + (i * 256 + tid) * 16) = v[i];
   };
-  using KA = std::integral_constant<bool, F != kExpertTN>;
-  using KB = std::integral_constant<bool, F == kExpertNT>;
+  OpA opa;
+  OpB opb;
+  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 64;
+  opa.init_frags(wm, lane);
+  opb.init_frags(wn, lane);
   float4v acc[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
-  const int nk = (K + 31) / 32;
+  half8 av[UNITS], bv[UNITS];
+  const int nk = (K + BK - 1) / BK;
   if (nk > 0) {
-    fetch(KA{}, A, g.lda, row0, mvalid, 0, av);
-    fetch(KB{}, B, g.ldb, col0, nvalid, 0, bv);
-    put(KA{}, at[0], av);
-    put(KB{}, bt[0], bv);
+    fetch(OpA{}, A, g.lda, mvalid, 0, av);
+    fetch(OpB{}, B, g.ldb, nvalid, 0, bv);
+    put(smem, av);
+    put(smem + OpA::BYTES, bv);
   }
   __syncthreads();
   for (int kt = 0; kt < nk; ++kt) {
-    const int buf = kt & 1;
+    char* const As = smem + (kt & 1) * (OpA::BYTES + OpB::BYTES);
+    char* const next = smem + (~kt & 1) * (OpA::BYTES + OpB::BYTES);
     if (kt + 1 < nk) {
-      fetch(KA{}, A, g.lda, row0, mvalid, kt + 1, av);
-      fetch(KB{}, B, g.ldb, col0, nvalid, kt + 1, bv);
-    }
-    half8 fa[4], fb[4];
-#pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      fa[f] = *(const half8*)&at[buf][(wm + 16 * f + lrow) * ROW + 8 * lkg];
-      fb[f] = *(const half8*)&bt[buf][(wn + 16 * f + lrow) * ROW + 8 * lkg];
+      fetch(OpA{}, A, g.lda, mvalid, kt + 1, av);
+      fetch(OpB{}, B, g.ldb, nvalid, kt + 1, bv);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int ks = 0; ks < 2; ++ks) {
+      half8 fa[4], fb[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+      for (int f = 0; f < 4; ++f) {
+        fa[f] = opa.frag(As, f, ks);
+        fb[f] = opb.frag(As + OpA::BYTES, f, ks);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+    }
     if (kt + 1 < nk) {
-      put(KA{}, at[buf ^ 1], av);
-      put(KB{}, bt[buf ^ 1], bv);
+      put(next, av);
+      put(next + OpA::BYTES, bv);
     }
     __syncthreads();
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int m = wm + 16 * i + lrow;
-    if (m >= mvalid) continue;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int c = wn + 16 * j + 4 * lkg + e;
-        if (c < nvalid)
-          C[(int64_t)(row0 + m) * g.ldc + col0 + c] = (_Float16)(g.relu ? relu_f(acc[i][j][e]) : acc[i][j][e]);
-      }
-  }
+  using ST = StagedTile<64, 64>;
+  static_assert(4 * ST::BYTES <= (int)sizeof(smem), "staged tiles");
+  char* const stage = smem + wave * ST::BYTES;
+  if (g.relu)
+    ST::template stage<true>(stage, acc, lane);
+  else
+    ST::template stage<false>(stage, acc, lane);
+  ST::wave_fence();
+  store_staged<ST, 64, false>(stage, lane, C + (int64_t)(row0 + wm) * g.ldc + col0 + wn, g.ldc, mvalid - wm, nvalid - wn,
+                              g.vec_c);
 }
 
 // A kernel with more than the default dynamic LDS: the limit is raised once per kernel and device.
