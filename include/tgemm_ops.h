@@ -130,8 +130,7 @@ TGEMM_API int orthogonalize_f16(int64_t batch, int64_t R, int64_t C, int dtype,
  *                      E4M3(y / s) to nearest even. A block of magnitudes below 2^-100 has codes 0
  *                      and scale 1; one that holds an infinity or a NaN codes 0 and scale NaN;
  *   residual_out     : h, in the residual's type (residual itself, with its stride, to update it in
- *                      place). Y may be X with its stride; no other overlap;
- *   rstd             : R float32, 1 / sqrt(mean(h^2) + eps), for the backward pass.
+ *                      place). Y may be X with its stride; no other overlap.
  * Each may be NULL, but not Y and Q both; Q and scale go together and residual_out needs a residual
  * (else TGEMM_ENULL). residual_dtype and w_dtype are TGEMM_DTYPE_F16 or TGEMM_DTYPE_F32 (residual
  * NULL: none, its type is not looked at). K is at most TGEMM_NORM_MAX_K, R times the threads of a row
@@ -143,12 +142,12 @@ TGEMM_API int orthogonalize_f16(int64_t batch, int64_t R, int64_t C, int dtype,
 TGEMM_API int rmsnorm_f16(int64_t R, int64_t K, const void* X, int64_t ldx,
                           const void* residual, int64_t ldr, int residual_dtype, const void* W, int w_dtype, float eps,
                           void* residual_out, int64_t ldro, void* Y, int64_t ldy,
-                          void* Q, int64_t ldq, float* scale, float* rstd, void* stream);
+                          void* Q, int64_t ldq, float* scale, void* stream);
 
 /*
  * Its gradient, from dY (the gradient of y), H (h as it was stored: residual_out, or X where there
- * was no residual; h_dtype its type), W, rstd and dH (the gradient of residual_out, of H's type;
- * NULL: none), with xhat = h rstd:
+ * was no residual; h_dtype its type), W, eps and dH (the gradient of residual_out, of H's type;
+ * NULL: none), with rstd = 1 / sqrt(mean(h^2) + eps) and xhat = h rstd:
  *   dX = rstd (W dY - xhat mean(W dY xhat)) + dH as binary16; dR the same in H's type (the
  *   residual's gradient; NULL: not wanted); dW = the sum over the rows of dY xhat in W's type (NULL:
  *   not wanted), float32 partial sums added in a fixed order.
@@ -160,7 +159,7 @@ TGEMM_API int rmsnorm_f16(int64_t R, int64_t K, const void* X, int64_t ldx,
 TGEMM_API int64_t rmsnorm_f16_backward_workspace_bytes(int64_t R, int64_t K);
 TGEMM_API int rmsnorm_f16_backward(int64_t R, int64_t K, const void* dY, int64_t lddy,
                                    const void* H, int64_t ldh, int h_dtype, const void* W, int w_dtype,
-                                   const float* rstd, const void* dH, int64_t lddh, void* dX, int64_t lddx,
+                                   float eps, const void* dH, int64_t lddh, void* dX, int64_t lddx,
                                    void* dR, int64_t lddr, void* dW, void* workspace, int64_t workspace_bytes,
                                    void* stream);
 

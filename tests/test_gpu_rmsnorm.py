@@ -313,29 +313,27 @@ def test_saved_tensor_hooks(gpu):
 
 
 def test_entry_points_in_place_and_with_every_output(gpu):
-    """The C entry points: y, codes and rstd in one pass, y over x, the residual updated in place; dX over dY
-    and dR over H in the backward pass."""
+    """The C entry points: y and codes in one pass, y over x, the residual updated in place; dX over dY and
+    dR over H in the backward pass."""
     R, K = 37, 1000
     x, r, w = case(R, K, np.float32)
     h = ref.stored(x, r)
-    want, rstd = ref.norm(h, w, EPS)
     xd, rd, wd = to_dev(x), to_dev(r), to_dev(w)
     q = gpu.empty((R, K), dtype=gpu.uint8, device="cuda")
-    s, rs = gpu.empty((R, 8), device="cuda"), gpu.empty(R, device="cuda")
+    s = gpu.empty((R, 8), device="cuda")
     L, st = tg.lib(), gpu.cuda.current_stream().cuda_stream
     assert L.rmsnorm_f16(R, K, xd.data_ptr(), K, rd.data_ptr(), K, 1, wd.data_ptr(), 0, EPS, rd.data_ptr(), K, xd.data_ptr(), K,
-                         q.data_ptr(), K, s.data_ptr(), rs.data_ptr(), st) == 0
+                         q.data_ptr(), K, s.data_ptr(), st) == 0
     assert np.array_equal(rd.cpu().numpy(), h)
     check_y(xd, h, w)
     check_codes(q, s, h, w)
-    assert (np.abs(rs.cpu().numpy() - rstd) <= rstd * ref.Y_REL).all()
     rng = np.random.default_rng(4)
     dy, dh = (0.1 * rng.standard_normal((R, K))).astype(np.float16), (0.1 * rng.standard_normal((R, K))).astype(np.float32)
     dx, bound, dw, size = ref.gradient(dy, h, w, EPS, dh)
     dyd, dhd, dwd = to_dev(dy), to_dev(dh), gpu.empty(K, dtype=gpu.float16, device="cuda")
     need = L.rmsnorm_f16_backward_workspace_bytes(R, K)
     ws = gpu.empty(need, dtype=gpu.uint8, device="cuda")
-    assert L.rmsnorm_f16_backward(R, K, dyd.data_ptr(), K, rd.data_ptr(), K, 1, wd.data_ptr(), 0, rs.data_ptr(), dhd.data_ptr(), K,
+    assert L.rmsnorm_f16_backward(R, K, dyd.data_ptr(), K, rd.data_ptr(), K, 1, wd.data_ptr(), 0, EPS, dhd.data_ptr(), K,
                                   dyd.data_ptr(), K, rd.data_ptr(), K, dwd.data_ptr(), ws.data_ptr(), need, st) == 0
     tol = bound + np.abs(dx) * (ref.HALF16 + 2.0 ** -18) + ref.TINY16
     assert (np.abs(dyd.cpu().numpy() - dx) <= tol).all() and (np.abs(rd.cpu().numpy() - dx) <= bound + np.abs(dx) * 2.0 ** -18).all()

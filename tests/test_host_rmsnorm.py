@@ -15,8 +15,8 @@ F16, F32 = 0, 1
 
 
 def norm(R=4, K=64, X=P, ldx=64, r=None, ldr=64, rt=F16, W=P, wt=F16, eps=1e-6, ro=None, ldro=64, Y=P, ldy=64, Q=None,
-         ldq=64, s=None, rstd=None):
-    return tg.lib().rmsnorm_f16(R, K, X, ldx, r, ldr, rt, W, wt, eps, ro, ldro, Y, ldy, Q, ldq, s, rstd, None)
+         ldq=64, s=None):
+    return tg.lib().rmsnorm_f16(R, K, X, ldx, r, ldr, rt, W, wt, eps, ro, ldro, Y, ldy, Q, ldq, s, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -29,16 +29,16 @@ def norm(R=4, K=64, X=P, ldx=64, r=None, ldr=64, rt=F16, W=P, wt=F16, eps=1e-6, 
     (dict(X=None), tg.TGEMM_ENULL), (dict(W=None), tg.TGEMM_ENULL), (dict(Y=None), tg.TGEMM_ENULL),
     (dict(Q=P), tg.TGEMM_ENULL), (dict(s=P), tg.TGEMM_ENULL), (dict(ro=P), tg.TGEMM_ENULL),
     (dict(X=P + 1), tg.TGEMM_EALIGN), (dict(W=P + 2, wt=F32), tg.TGEMM_EALIGN), (dict(r=P + 2, rt=F32), tg.TGEMM_EALIGN),
-    (dict(r=P, ro=P + 1), tg.TGEMM_EALIGN), (dict(Q=P + 1, s=P + 2), tg.TGEMM_EALIGN), (dict(rstd=P + 1), tg.TGEMM_EALIGN),
+    (dict(r=P, ro=P + 1), tg.TGEMM_EALIGN), (dict(Q=P + 1, s=P + 2), tg.TGEMM_EALIGN),
     (dict(R=0, X=None), tg.TGEMM_OK), (dict(K=0, X=None), tg.TGEMM_OK),
 ])
 def test_refusals(kw, code):
     assert norm(**kw) == code
 
 
-def backward(R=4, K=64, dY=P, lddy=64, H=P, ldh=64, ht=F16, W=P, wt=F16, rstd=P, dH=None, lddh=64, dX=P, lddx=64, dR=None,
+def backward(R=4, K=64, dY=P, lddy=64, H=P, ldh=64, ht=F16, W=P, wt=F16, eps=1e-6, dH=None, lddh=64, dX=P, lddx=64, dR=None,
              lddr=64, dW=P, ws=P, nws=1 << 20):
-    return tg.lib().rmsnorm_f16_backward(R, K, dY, lddy, H, ldh, ht, W, wt, rstd, dH, lddh, dX, lddx, dR, lddr, dW, ws, nws, None)
+    return tg.lib().rmsnorm_f16_backward(R, K, dY, lddy, H, ldh, ht, W, wt, eps, dH, lddh, dX, lddx, dR, lddr, dW, ws, nws, None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -46,7 +46,7 @@ def backward(R=4, K=64, dY=P, lddy=64, H=P, ldh=64, ht=F16, W=P, wt=F16, rstd=P,
     (dict(wt=-1), tg.TGEMM_EINVAL_DIM), (dict(lddy=63), tg.TGEMM_EINVAL_LD), (dict(ldh=1), tg.TGEMM_EINVAL_LD),
     (dict(lddx=63), tg.TGEMM_EINVAL_LD), (dict(dH=P, lddh=63), tg.TGEMM_EINVAL_LD), (dict(dR=P, lddr=63), tg.TGEMM_EINVAL_LD),
     (dict(dY=None), tg.TGEMM_ENULL), (dict(H=None), tg.TGEMM_ENULL), (dict(W=None), tg.TGEMM_ENULL),
-    (dict(rstd=None), tg.TGEMM_ENULL), (dict(dX=None), tg.TGEMM_ENULL), (dict(ws=None), tg.TGEMM_ENULL),
+    (dict(eps=-1.0), tg.TGEMM_EINVAL_DIM), (dict(dX=None), tg.TGEMM_ENULL), (dict(ws=None), tg.TGEMM_ENULL),
     (dict(ws=P + 4), tg.TGEMM_EALIGN), (dict(H=P + 2, ht=F32), tg.TGEMM_EALIGN), (dict(dW=P + 1), tg.TGEMM_EALIGN),
     (dict(dR=P + 2, ht=F32), tg.TGEMM_EALIGN), (dict(nws=2 * 64 * 4 - 1, R=33), tg.TGEMM_EWORKSPACE),
     (dict(K=0), tg.TGEMM_OK), (dict(R=0, dW=None), tg.TGEMM_OK),

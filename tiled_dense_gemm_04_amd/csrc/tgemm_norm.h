@@ -17,9 +17,9 @@ struct NormArgs {
   const _Float16* X;
   const void *Rin, *W;
   void* Rout;
-  _Float16* Y;     // any of Rout, Y, Q and S (together) and rstd may be null
+  _Float16* Y;     // any of Rout, Y, and Q and S together may be null
   uint8_t* Q;
-  float *S, *rstd;
+  float* S;
   int64_t ldx, ldr, ldro, ldy, ldq;  // elements
   int R, K, KB, w_f32;
   float eps;
@@ -29,12 +29,12 @@ hipError_t launch_rmsnorm(const NormArgs& g, int residual, hipStream_t s);
 struct NormGradArgs {
   const _Float16* dY;
   const void *H, *W, *dH;  // dH may be null; H and dH have the residual's type
-  const float* rstd;
   _Float16* dX;
   void *dR, *dW;           // dR (the residual's type) and dW (W's type) may be null
   float* parts;            // groups x K partial sums of dW
   int64_t lddy, ldh, lddh, lddx, lddr;
   int R, K, w_f32, groups;
+  float eps;
 };
 // Workgroups of the backward kernel (each leaves one row of partial sums).
 int norm_grad_groups(int64_t R, int64_t K);

@@ -15,21 +15,27 @@
 namespace tgemm {
 namespace {
 
-// Sum over the TPR threads of a row (up to 64: lanes of one wave; else the workgroup, every thread
-// adding the waves' sums in wave order). `lds` holds a float per wave; a slow wave may still read it
-// when the call returns, so calls that follow each other alternate between two arrays.
-template <int TPR>
-__device__ __forceinline__ float row_sum(float v, float* lds) {
+// N sums over the TPR threads of a row (up to 64: lanes of one wave; else the workgroup, every thread
+// adding the waves' sums in wave order). `lds` holds a float per wave and sum; a slow wave may still read
+// it when the call returns, so calls that follow each other alternate between two arrays.
+template <int TPR, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*lds)[N]) {
 #pragma unroll
-  for (int o = 1; o < (TPR < 64 ? TPR : 64); o <<= 1) v += __shfl_xor(v, o, 64);
+  for (int o = 1; o < (TPR < 64 ? TPR : 64); o <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], o, 64);
   if constexpr (TPR > 64) {
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = 0.0f;
+    if ((threadIdx.x & 63) == 0)
 #pragma unroll
-    for (int w = 0; w < TPR / 64; ++w) v += lds[w];
+      for (int i = 0; i < N; ++i) lds[threadIdx.x >> 6][i] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < TPR / 64; ++w)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += lds[w][i];
   }
-  return v;
 }
 
 // Two floats to two E4M3 codes in the low or high half of a word (round to nearest even).
@@ -72,7 +78,7 @@ __device__ __forceinline__ float block_codes(const float (&y)[8], uint2v& codes)
 // 4096 3.5 and 4.1 with its launch.
 template <int TPR, int CH, int RES>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_rows(NormArgs g) {
-  __shared__ float lds[TPR > 64 ? TPR / 64 : 1];
+  __shared__ float lds[TPR > 64 ? TPR / 64 : 1][1];
   constexpr int RPG = TPR < 256 ? 256 / TPR : 1;  // rows per workgroup
   const int t = threadIdx.x % TPR;
   const int64_t row = (int64_t)blockIdx.x * RPG + threadIdx.x / TPR;
@@ -99,7 +105,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_rows(NormArgs g
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[i][e] = RES == kResNone ? (float)x[e] : h[i][e] + (float)x[e];
   }
-  float ss = 0.0f;
+  float ss[1] = {0.0f};
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int k = 8 * (t + i * TPR), n = g.K - k;
@@ -116,10 +122,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_rows(NormArgs g
       if (live && g.Rout != nullptr) store_float8((float*)g.Rout + r * g.ldro + k, h[i], n);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[i][e], h[i][e], ss);
+    for (int e = 0; e < 8; ++e) ss[0] = __builtin_fmaf(h[i][e], h[i][e], ss[0]);
   }
-  const float rstd = 1.0f / sqrtf(row_sum<TPR>(ss, lds) / (float)g.K + g.eps);
-  if (live && t == 0 && g.rstd != nullptr) g.rstd[r] = rstd;
+  row_sums<TPR>(ss, lds);
+  const float rstd = 1.0f / sqrtf(ss[0] / (float)g.K + g.eps);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int k = 8 * (t + i * TPR), n = g.K - k;
@@ -141,13 +147,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_rows(NormArgs g
 }
 
 // ------------------------------------------------------------------------------------
-// Backward. A workgroup takes rows blockIdx.x, + gridDim.x, ... (times its rows at once); a thread
+// Backward; a row's rstd is computed again beside the other sum it needs, from the row that is there
+// anyway. A workgroup takes rows blockIdx.x, + gridDim.x, ... (times its rows at once); a thread
 // keeps its columns' weights and its sums of dw in registers over all of them, and the sums leave
 // as one row of partial sums per workgroup, added in a fixed order by norm_weight_grad. With that kernel
 // 8192 x 8192 takes 104 us (5.2 TB/s), 16384 x 4096 110, 16384 x 2048 52, 131072 x 128 18.5.
 template <int TPR, int CH, bool H32>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_grad_rows(NormGradArgs g) {
-  __shared__ float lds[2][TPR > 64 ? TPR / 64 : 1];
+  __shared__ float lds[2][TPR > 64 ? TPR / 64 : 1][2];
   constexpr int RPG = TPR < 256 ? 256 / TPR : 1;
   const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
   float w[CH][8], dw[CH][8];
@@ -169,32 +176,30 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_grad_rows(NormG
   for (int64_t first = (int64_t)blockIdx.x * RPG; first < g.R; first += (int64_t)gridDim.x * RPG, parity ^= 1) {
     const bool live = first + sub < g.R;
     const int64_t r = live ? first + sub : g.R - 1;
-    const float rstd = live ? g.rstd[r] : 0.0f;  // (a row past the last adds nothing to dw)
     half8 dy[CH];
-    float xh[CH][8];
-    float c = 0.0f;
+    float h[CH][8];
+    float sum[2] = {0.0f, 0.0f};  // of h^2 and of w dy h
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       const int k = 8 * (t + i * TPR), n = g.K - k;
       dy[i] = load_half8(g.dY + r * g.lddy + k, n);
       if constexpr (H32) {
-        load_float8((const float*)g.H + r * g.ldh + k, n, xh[i]);
+        load_float8((const float*)g.H + r * g.ldh + k, n, h[i]);
       } else {
         const half8 a = load_half8((const _Float16*)g.H + r * g.ldh + k, n);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) xh[i][e] = (float)a[e];
+        for (int e = 0; e < 8; ++e) h[i][e] = (float)a[e];
       }
     }
 #pragma unroll
     for (int i = 0; i < CH; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        xh[i][e] *= rstd;
-        const float p = (float)dy[i][e] * xh[i][e];
-        if (live) dw[i][e] += p;
-        c = __builtin_fmaf(p, w[i][e], c);
+        sum[0] = __builtin_fmaf(h[i][e], h[i][e], sum[0]);
+        sum[1] = __builtin_fmaf((float)dy[i][e] * w[i][e], h[i][e], sum[1]);
       }
-    c = row_sum<TPR>(c, lds[parity]) * inv_k;
+    row_sums<TPR>(sum, lds[parity]);
+    const float rstd = 1.0f / sqrtf(sum[0] * inv_k + g.eps), c = sum[1] * inv_k * rstd;
     if (live) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
@@ -214,7 +219,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_grad_rows(NormG
         half8 a;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          dx[e] = __builtin_fmaf(rstd, __builtin_fmaf(-xh[i][e], c, (float)dy[i][e] * w[i][e]), dh[e]);
+          const float xhat = h[i][e] * rstd;
+          dw[i][e] = __builtin_fmaf((float)dy[i][e], xhat, dw[i][e]);
+          dx[e] = __builtin_fmaf(rstd, __builtin_fmaf(-xhat, c, (float)dy[i][e] * w[i][e]), dh[e]);
           a[e] = (_Float16)dx[e];
         }
         store_half8(g.dX + r * g.lddx + k, a, n);

@@ -26,7 +26,7 @@ extern "C" {
 
 int rmsnorm_f16(int64_t R, int64_t K, const void* X, int64_t ldx, const void* residual, int64_t ldr, int residual_dtype,
                 const void* W, int w_dtype, float eps, void* residual_out, int64_t ldro, void* Y, int64_t ldy, void* Q,
-                int64_t ldq, float* scale, float* rstd, void* stream) {
+                int64_t ldq, float* scale, void* stream) {
   if (bad_dims(R, K)) return TGEMM_EINVAL_DIM;
   const bool has_r = residual != nullptr;
   if (bad_dtype(w_dtype) || (has_r && bad_dtype(residual_dtype)) || !(eps >= 0.0f)) return TGEMM_EINVAL_DIM;
@@ -38,7 +38,7 @@ int rmsnorm_f16(int64_t R, int64_t K, const void* X, int64_t ldx, const void* re
   if (X == nullptr || W == nullptr || (Y == nullptr && Q == nullptr) || (Q == nullptr) != (scale == nullptr) ||
       (residual_out != nullptr && !has_r))
     return TGEMM_ENULL;
-  if (off(X, 2) || off(Y, 2) || off(W, size_of(w_dtype)) || off(scale, 4) || off(rstd, 4) ||
+  if (off(X, 2) || off(Y, 2) || off(W, size_of(w_dtype)) || off(scale, 4) ||
       (has_r && (off(residual, size_of(residual_dtype)) || off(residual_out, size_of(residual_dtype)))))
     return TGEMM_EALIGN;
   int dev = -1;
@@ -52,7 +52,6 @@ int rmsnorm_f16(int64_t R, int64_t K, const void* X, int64_t ldx, const void* re
   g.Y = static_cast<_Float16*>(Y);
   g.Q = static_cast<uint8_t*>(Q);
   g.S = scale;
-  g.rstd = rstd;
   g.ldx = ldx;
   g.ldr = ldr;
   g.ldro = ldro;
@@ -73,18 +72,18 @@ int64_t rmsnorm_f16_backward_workspace_bytes(int64_t R, int64_t K) {
 }
 
 int rmsnorm_f16_backward(int64_t R, int64_t K, const void* dY, int64_t lddy, const void* H, int64_t ldh, int h_dtype,
-                         const void* W, int w_dtype, const float* rstd, const void* dH, int64_t lddh, void* dX,
+                         const void* W, int w_dtype, float eps, const void* dH, int64_t lddh, void* dX,
                          int64_t lddx, void* dR, int64_t lddr, void* dW, void* workspace, int64_t workspace_bytes,
                          void* stream) {
-  if (bad_dims(R, K) || bad_dtype(h_dtype) || bad_dtype(w_dtype)) return TGEMM_EINVAL_DIM;
+  if (bad_dims(R, K) || bad_dtype(h_dtype) || bad_dtype(w_dtype) || !(eps >= 0.0f)) return TGEMM_EINVAL_DIM;
   const int64_t kmin = K > 1 ? K : 1;
   if (lddy < kmin || ldh < kmin || lddx < kmin || (dH != nullptr && lddh < kmin) || (dR != nullptr && lddr < kmin))
     return TGEMM_EINVAL_LD;
   if (K == 0 || (R == 0 && dW == nullptr)) return TGEMM_OK;
-  if (R > 0 && (dY == nullptr || H == nullptr || rstd == nullptr || dX == nullptr)) return TGEMM_ENULL;
+  if (R > 0 && (dY == nullptr || H == nullptr || dX == nullptr)) return TGEMM_ENULL;
   if (W == nullptr || (R > 0 && dW != nullptr && workspace == nullptr)) return TGEMM_ENULL;
   const unsigned hs = size_of(h_dtype), ws = size_of(w_dtype);
-  if (off(dY, 2) || off(dX, 2) || off(H, hs) || off(dH, hs) || off(dR, hs) || off(W, ws) || off(dW, ws) || off(rstd, 4) ||
+  if (off(dY, 2) || off(dX, 2) || off(H, hs) || off(dH, hs) || off(dR, hs) || off(W, ws) || off(dW, ws) ||
       off(workspace, 256))
     return TGEMM_EALIGN;
   if (dW != nullptr && workspace_bytes < rmsnorm_f16_backward_workspace_bytes(R, K)) return TGEMM_EWORKSPACE;
@@ -96,7 +95,6 @@ int rmsnorm_f16_backward(int64_t R, int64_t K, const void* dY, int64_t lddy, con
   g.H = H;
   g.W = W;
   g.dH = dH;
-  g.rstd = rstd;
   g.dX = static_cast<_Float16*>(dX);
   g.dR = dR;
   g.dW = dW;
@@ -109,6 +107,7 @@ int rmsnorm_f16_backward(int64_t R, int64_t K, const void* dY, int64_t lddy, con
   g.R = (int)R;
   g.K = (int)K;
   g.w_f32 = w_dtype == TGEMM_DTYPE_F32;
+  g.eps = eps;
   g.groups = R == 0 ? 0 : tgemm::norm_grad_groups(R, K);
   return tgemm::launch_rmsnorm_backward(g, h_dtype == TGEMM_DTYPE_F32, static_cast<hipStream_t>(stream)) == hipSuccess
              ? TGEMM_OK

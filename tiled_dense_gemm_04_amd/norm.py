@@ -18,9 +18,9 @@ NORM_MAX_K = 16384           # TGEMM_NORM_MAX_K
 
 _i64, _p, _i32, _f = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_float
 SIGNATURES = {
-    "rmsnorm_f16": (_i32, [_i64, _i64, _p, _i64, _p, _i64, _i32, _p, _i32, _f, _p, _i64, _p, _i64, _p, _i64, _p, _p, _p]),
+    "rmsnorm_f16": (_i32, [_i64, _i64, _p, _i64, _p, _i64, _i32, _p, _i32, _f, _p, _i64, _p, _i64, _p, _i64, _p, _p]),
     "rmsnorm_f16_backward_workspace_bytes": (_i64, [_i64, _i64]),
-    "rmsnorm_f16_backward": (_i32, [_i64, _i64, _p, _i64, _p, _i64, _i32, _p, _i32, _p, _p, _i64, _p, _i64, _p, _i64, _p,
+    "rmsnorm_f16_backward": (_i32, [_i64, _i64, _p, _i64, _p, _i64, _i32, _p, _i32, _f, _p, _i64, _p, _i64, _p, _i64, _p,
                                     _p, _i64, _p]),
 }
 
@@ -90,7 +90,7 @@ def _residual(residual, residual_out, shape, device, stream):
     return dtype, ld, residual_out, ldo
 
 
-def _norm(x, ldx, weight, residual, eps, y, ldy, q, ldq, scale, rstd, residual_out, stream, library):
+def _norm(x, ldx, weight, residual, eps, y, ldy, q, ldq, scale, residual_out, stream, library):
     """One call on checked x and outputs; returns the updated residual (None without a residual)."""
     shape, device = x.shape, x.device
     R, K = shape
@@ -99,8 +99,7 @@ def _norm(x, ldx, weight, residual, eps, y, ldy, q, ldq, scale, rstd, residual_o
     rc = _call("rmsnorm_f16", (R, K, x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, r_dtype,
                                weight.data_ptr(), w_dtype, eps, None if residual is None else residual_out.data_ptr(), ldro,
                                None if y is None else y.data_ptr(), ldy, None if q is None else q.data_ptr(), ldq,
-                               None if q is None else scale.data_ptr(), None if rstd is None else rstd.data_ptr(),
-                               _stream(stream, device)), device, library)
+                               None if q is None else scale.data_ptr(), _stream(stream, device)), device, library)
     if rc != TGEMM_OK:
         raise TgemmError(rc, "rmsnorm_f16")
     return residual_out
@@ -121,7 +120,7 @@ def rmsnorm(x, weight, residual=None, eps: float = 1e-6, out=None, residual_out=
             raise ValueError(f"out has shape {tuple(out.shape)}, expected {(R, K)}")
         if out.device != x.device:
             raise ValueError("x and out must be on the same device")
-    h = _norm(x, ldx, weight, residual, eps, out, ldy, None, 0, None, None, residual_out, stream, library)
+    h = _norm(x, ldx, weight, residual, eps, out, ldy, None, 0, None, residual_out, stream, library)
     return out if residual is None else (out, h)
 
 
@@ -145,7 +144,7 @@ def rmsnorm_fp8_block(x, weight, residual=None, eps: float = 1e-6, q=None, scale
         _scale_operand(scale, (R, blocks), "scale")
     if q.device != x.device or scale.device != x.device:
         raise ValueError("x, q and scale must be on the same device")
-    h = _norm(x, ldx, weight, residual, eps, None, 0, q, ldq, scale, None, residual_out, stream, library)
+    h = _norm(x, ldx, weight, residual, eps, None, 0, q, ldq, scale, residual_out, stream, library)
     return (q, scale) if residual is None else (q, scale, h)
 
 
@@ -178,20 +177,20 @@ def autograd_functions():
 
     class RmsNormFunction(torch.autograd.Function):
         """(x, weight, residual or None, eps) -> y, or (y, h) with a residual, for fp16 x (R, K); the
-        backward pass reads h and a float32 number per row. The residual's gradient is x's in the
-        residual's type."""
+        backward pass reads h. The residual's gradient is x's in the residual's type."""
 
         @staticmethod
         def forward(ctx, x, weight, residual, eps):
             x = _row_major(x, "x")
-            y, rstd = _new(x, x.shape, f16, None), torch.empty(x.shape[0], dtype=f32, device=x.device)
+            y = _new(x, x.shape, f16, None)
             weight = weight.contiguous()
             if residual is not None:
                 residual = _rows(residual, "residual", (f16, f32))
-            h = _norm(x, _ld(x), weight, residual, eps, y, x.shape[1] or 1, None, 0, None, rstd, None, None, None)
+            h = _norm(x, _ld(x), weight, residual, eps, y, x.shape[1] or 1, None, 0, None, None, None, None)
             kept = x if h is None else h
-            ctx.save_for_backward(kept, weight, rstd)
-            ctx.saved = kept.shape, kept.dtype, weight.shape, weight.dtype, rstd.shape, x.device
+            ctx.save_for_backward(kept, weight)
+            ctx.saved = kept.shape, kept.dtype, kept.device, weight.shape, weight.dtype, weight.device
+            ctx.eps = eps
             ctx.set_materialize_grads(False)
             return y if h is None else (y, h)
 
@@ -199,11 +198,10 @@ def autograd_functions():
         def backward(ctx, dy, dh=None):
             if torch.is_grad_enabled():
                 raise RuntimeError("RmsNormFunction has no second derivative (create_graph=True)")
-            h, weight, rstd = ctx.saved_tensors
+            h, weight = ctx.saved_tensors
             shape, dtype, device = h.shape, h.dtype, h.device
             # the library takes addresses
-            if ((shape, dtype, weight.shape, weight.dtype, rstd.shape, device) != ctx.saved or rstd.dtype != f32
-                    or weight.device != device or rstd.device != device):
+            if (shape, dtype, device, weight.shape, weight.dtype, weight.device) != ctx.saved:
                 raise RuntimeError("a saved-tensor hook returned another tensor than the forward pass saved")
             need_x, need_w, need_r, _ = ctx.needs_input_grad
             if dy is None:  # nothing came back through y
@@ -211,7 +209,7 @@ def autograd_functions():
                     return None, None, None, None
                 return dh.to(f16) if need_x else None, torch.zeros_like(weight) if need_w else None, \
                     dh if need_r else None, None
-            h, weight, rstd, dy = _rows(h, "h", (dtype,)), weight.contiguous(), rstd.contiguous(), _rows(dy, "dy", (f16,))
+            h, weight, dy = _rows(h, "h", (dtype,)), weight.contiguous(), _rows(dy, "dy", (f16,))
             R, K = shape
             dx = torch.empty(shape, dtype=f16, device=device)
             dr = torch.empty(shape, dtype=f32, device=device) if need_r and dtype == f32 else None
@@ -226,7 +224,7 @@ def autograd_functions():
                 dh = _rows(dh, "dh", (dtype,))
             rc = _call("rmsnorm_f16_backward",
                        (R, K, dy.data_ptr(), _ld(dy), h.data_ptr(), _ld(h), DTYPE_F32 if dtype == f32 else DTYPE_F16,
-                        weight.data_ptr(), DTYPE_F32 if weight.dtype == f32 else DTYPE_F16, rstd.data_ptr(),
+                        weight.data_ptr(), DTYPE_F32 if weight.dtype == f32 else DTYPE_F16, ctx.eps,
                         None if dh is None else dh.data_ptr(), 0 if dh is None else _ld(dh), dx.data_ptr(), ld,
                         None if dr is None else dr.data_ptr(), ld, dw.data_ptr() if need_w else None,
                         workspace.data_ptr() if need else None, need, _stream(None, device)), device)
