@@ -640,7 +640,9 @@ __global__ __launch_bounds__(256) void expert_small(ExpertGemmArgs g) {
 // ------------------------------------------------------------------------------------
 // Any alignment, stride and size: 128 x 128 tiles, four waves of 64 x 64, k-tiles of 64 through two LDS
 // slots in the layout of the tile kernels (PpOperand), but filled through registers: loads of any
-// address, cut by the rows' ends. Bound by their latency, of which one k-tile's products cover a part.
+// address, cut by the rows' ends. Bound by their latency, of which one k-tile's products cover a part: 4096
+// rows, 8 experts, 2048 x 2048: 86 us in the rows' forms and 65 in the weights' (the tile kernels 46 to 53);
+// 16 rows, 8 experts of 2047 x 2047: 58 us.
 template <ExpertForm F>
 __global__ __launch_bounds__(256) void expert_generic(ExpertGemmArgs g) {
   constexpr int BM = 128, BK = 64;

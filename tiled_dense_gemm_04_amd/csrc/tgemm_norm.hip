@@ -151,7 +151,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_rows(NormArgs g
 // anyway. A workgroup takes rows blockIdx.x, + gridDim.x, ... (times its rows at once); a thread
 // keeps its columns' weights and its sums of dw in registers over all of them, and the sums leave
 // as one row of partial sums per workgroup, added in a fixed order by norm_weight_grad. With that kernel
-// 8192 x 8192 takes 104 us (5.2 TB/s), 16384 x 4096 110, 16384 x 2048 52, 131072 x 128 18.5.
+// 8192 x 8192 takes 104 us in a loop (5.2 TB/s) and 116 after other work; in a loop 16384 x 4096 110,
+// 16384 x 2048 52, 131072 x 128 18.5.
 template <int TPR, int CH, bool H32>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_grad_rows(NormGradArgs g) {
   __shared__ float lds[2][TPR > 64 ? TPR / 64 : 1][2];
