@@ -25,28 +25,33 @@ SIGNATURES = {
 }
 
 
+@functools.lru_cache(maxsize=None)
+def _types():
+    import torch
+    return torch.Tensor, {torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
+
+
 def _dtype(t, name):
     """The library's number of t's type (fp16 or fp32)."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+    tensor, numbers = _types()
+    if not isinstance(t, tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype == torch.float16:
-        return DTYPE_F16
-    if t.dtype == torch.float32:
-        return DTYPE_F32
-    raise TypeError(f"{name} must be float16 or float32, got {t.dtype}")
+    number = numbers.get(t.dtype)
+    if number is None:
+        raise TypeError(f"{name} must be float16 or float32, got {t.dtype}")
+    return number
 
 
 def _typed_operand(t, name, shape, device):
     """(type, row stride) of a 2-D fp16 or fp32 device tensor of `shape` with contiguous rows."""
     dtype = _dtype(t, name)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     rows, cols = shape
-    if t.numel() == 0:
-        return dtype, max(1, cols)
+    if t.is_contiguous():  # (an empty one is)
+        return dtype, cols or 1
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must be row-major (stride(1) == 1)")
     return dtype, t.stride(0) if rows > 1 else max(1, cols)
@@ -54,11 +59,11 @@ def _typed_operand(t, name, shape, device):
 
 def _weight(w, K, device):
     dtype = _dtype(w, "weight")
-    if tuple(w.shape) != (K,):
+    if w.shape != (K,):
         raise ValueError(f"weight has shape {tuple(w.shape)}, expected {(K,)}")
     if w.device != device:
         raise ValueError("weight must be on x's device")
-    if K > 1 and w.stride(0) != 1:
+    if not w.is_contiguous():
         raise ValueError("weight must be contiguous")
     return dtype
 
@@ -69,7 +74,7 @@ def _new(like, shape, dtype, stream):
     import torch
     if stream is None:
         if like.shape == shape and like.is_contiguous():
-            return torch.empty_like(like, dtype=dtype)
+            return torch.empty_like(like) if like.dtype == dtype else torch.empty_like(like, dtype=dtype)
         return torch.empty(shape, dtype=dtype, device=like.device)
     with _allocating(stream, like.device):
         return torch.empty(shape, dtype=dtype, device=like.device)
@@ -160,6 +165,8 @@ def _rows(t, name, dtypes):
     """t itself where its rows are contiguous and apart, else a copy (a broadcast gradient)."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.is_contiguous():
+        return t
     rows, cols = t.shape
     ld, step = t.stride()
     return t if (cols <= 1 or step == 1) and (rows <= 1 or ld >= cols) else t.contiguous()
@@ -168,7 +175,7 @@ def _rows(t, name, dtypes):
 def _ld(t):
     """Row stride of a 2-D tensor with contiguous rows, as the library takes it."""
     rows, cols = t.shape
-    return t.stride(0) if rows > 1 else cols or 1
+    return cols or 1 if rows <= 1 or t.is_contiguous() else t.stride(0)
 
 
 def autograd_functions():
@@ -189,7 +196,7 @@ def autograd_functions():
             h = _norm(x, _ld(x), weight, residual, eps, y, x.shape[1] or 1, None, 0, None, None, None, None)
             kept = x if h is None else h
             ctx.save_for_backward(kept, weight)
-            ctx.saved = kept.shape, kept.dtype, kept.device, weight.shape, weight.dtype, weight.device
+            ctx.saved = kept.shape, kept.dtype, kept.device, weight.dtype, weight.device
             ctx.eps = eps
             ctx.set_materialize_grads(False)
             return y if h is None else (y, h)
@@ -201,7 +208,7 @@ def autograd_functions():
             h, weight = ctx.saved_tensors
             shape, dtype, device = h.shape, h.dtype, h.device
             # the library takes addresses
-            if (shape, dtype, device, weight.shape, weight.dtype, weight.device) != ctx.saved:
+            if (shape, dtype, device, weight.dtype, weight.device) != ctx.saved or weight.shape != shape[1:]:
                 raise RuntimeError("a saved-tensor hook returned another tensor than the forward pass saved")
             need_x, need_w, need_r, _ = ctx.needs_input_grad
             if dy is None:  # nothing came back through y
@@ -211,8 +218,8 @@ def autograd_functions():
                     dh if need_r else None, None
             h, weight, dy = _rows(h, "h", (dtype,)), weight.contiguous(), _rows(dy, "dy", (f16,))
             R, K = shape
-            dx = torch.empty(shape, dtype=f16, device=device)
-            dr = torch.empty(shape, dtype=f32, device=device) if need_r and dtype == f32 else None
+            dx = _new(dy, shape, f16, None)
+            dr = _new(dy, shape, f32, None) if need_r and dtype == f32 else None
             dw = workspace = None
             need = 0
             if need_w:
