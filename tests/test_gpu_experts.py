@@ -271,6 +271,18 @@ def test_products_exact(gpu, form, cfg):
             assert np.array_equal(got, want), (name, N, K)
 
 
+@pytest.mark.parametrize("form", ["nt", "nn"])
+@pytest.mark.parametrize("counts, N", [([300, 0, 45, 129], 520), ([3000, 1400, 257], 1000), ([600, 520, 300, 129, 260], 2440),
+                                       ([2000, 2100, 1700, 1000, 1500], 2056)], ids=lambda v: str(v))
+def test_products_last_round_in_halves(gpu, form, counts, N):
+    """Lists of tiles whose last round is of halves: all of one, after a round of small tiles, edges among them,
+    and after a round of big tiles (quarters and edges)."""
+    offsets, rows = groups(counts, 5)
+    got, want = exact_product(form, np.random.default_rng(13), offsets, rows, N, 72, tg.EXPERT_TILES, relu=True,
+                              zero_rest=True)
+    assert np.array_equal(got, want)
+
+
 @pytest.mark.parametrize("form", FORMS)
 def test_products_debug_fill(gpu, form):
     """The build that fills every LDS copy's destination with NaN first: no read before its copy."""

@@ -115,7 +115,8 @@ def test_kernel_choice():
         assert f(form, 1, 64, N=2048, K=4096) == tg.EXPERT_32
         assert f(form, 16384, 16, N=4096, K=2048) == tg.EXPERT_TILES
         assert f(form, 1600, 16, N=512, K=512) == tg.EXPERT_TILES and f(form, 96, 16, N=512, K=512) == tg.EXPERT_32
-        assert f(form, 784, 16, N=512, K=512) == tg.EXPERT_64 and f(form, 783, 16, N=512, K=512) == tg.EXPERT_32
+        assert f(form, 784, 16, N=2048, K=512) == tg.EXPERT_64 and f(form, 783, 16, N=2048, K=512) == tg.EXPERT_32
+        assert f(form, 784, 16, N=1024, K=512) == tg.EXPERT_TILES and f(form, 784, 16, N=1032, K=512) == tg.EXPERT_64
         assert f(form, 64, 8, N=64, K=63) == tg.EXPERT_GENERIC      # K is contiguous in A
         assert f(form, 64, 8, N=64, K=64, A=P + 2) == tg.EXPERT_GENERIC
         assert f(form, 64, 8, N=64, K=64, stride_b=4097) == tg.EXPERT_GENERIC

@@ -53,7 +53,7 @@ struct ExpertGemmArgs {
 };
 enum ExpertForm { kExpertNT = 0, kExpertNN = 1, kExpertTN = 2 };
 // Kernels of a product, by index (tooling ABI: the _cfg entry point). kExpertTiles mixes tiles of 256 x
-// 256 and 128 x 128; kExpert128 and kExpert256 are the same kernel held to one of them (but for
+// 256, 128 x 128 and, in the rows' form, 64 x 128; kExpert128 and kExpert256 are the same kernel held to one of them (but for
 // edges).
 enum ExpertConfig { kExpertGeneric = 0, kExpert32 = 1, kExpert128 = 2, kExpert256 = 3, kExpertTiles = 4, kExpert64 = 5, kExpertConfigs = 6 };
 enum ExpertTileMode { kTilesAuto = 0, kTilesSmall = 1, kTilesBig = 2 };
@@ -68,10 +68,11 @@ inline int64_t expert_gemm_groups(int cfg, int form, int64_t rows, int64_t exper
   if (form == kExpertTN) return experts * ceil_div(M, 128) * tn;
   return (rows / expert_tile_m(cfg) + (experts < rows ? experts : rows) + 1) * tn;
 }
-// The most 128 x 128 tiles that the tile kernel has, whatever the division of the rows.
+// The most tiles that the tile kernel has, whatever the division of the rows: of 128 x 128, and in the
+// rows' form the halves of a last round.
 inline int64_t expert_max_tiles(int form, int64_t rows, int64_t experts, int64_t M, int64_t N) {
   if (form == kExpertTN) return experts * (ceil_div(M, 128) + 1) * (ceil_div(N, 128) + 1);
-  return (rows / 128 + 2 * (experts < rows ? experts : rows)) * (ceil_div(N, 128) + 1);
+  return (rows / 128 + 2 * (experts < rows ? experts : rows)) * (ceil_div(N, 128) + 1) + kExpertTileGroups;
 }
 hipError_t launch_expert_gemm(int cfg, ExpertForm form, const ExpertGemmArgs& g, hipStream_t s, int device);
 

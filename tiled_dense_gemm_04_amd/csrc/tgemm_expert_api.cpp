@@ -50,13 +50,16 @@ bool chunks(const void* p, int64_t ld, int64_t width) {
 
 // Kernel of a product whose operands the tiles take, by the rows an expert has on average (uneven
 // experts; microseconds of the tiles of 32 rows, of 64, and of 128 and 256):
-//   32 rows: 111, 119, 139 (64 experts, 2048 x 2048), 15, 19, 18 (8);
-//   64: 142, 127, 136 (64), 42, 39, 53 (16), 20.5, 19.6, 18.8 (8);   96: 176, 141, 144 (64);
-//   128: 212, -, 152 (64), 61, 50, 52 (16).
-int choose(int form, int64_t rows, int64_t experts) {
+//   32 rows: 112, 120, 137 (64 experts, 2048 x 2048), 15.6, 20.1, 16.0 (8);
+//   64: 142, 128, 136 (64), 42, 39, 51 (16), 20.6, 19.3, 17.3 (8), 14.1, 18.5, 13.9 (1);
+//   96: 174, 141, 144 (64), 51, 40, 48 (16), 20.1, 20.3, 19.7 (8);   128: 212, -, 152 (64), 61, 50, 52 (16).
+// So 64 rows where the small tiles would be more than one round of halves.
+int choose(int form, int64_t rows, int64_t experts, int64_t N) {
   const int64_t met = rows < experts ? at_least_1(rows) : experts, each = rows / met;
   if (form == tgemm::kExpertTN) return tgemm::kExpertTiles;
-  return each <= 48 ? tgemm::kExpert32 : each <= 96 ? tgemm::kExpert64 : tgemm::kExpertTiles;
+  if (each <= 48) return tgemm::kExpert32;
+  const bool one_round = met * tgemm::ceil_div(N, 128) <= tgemm::kExpertTileGroups / 2;
+  return each <= 96 && !one_round ? tgemm::kExpert64 : tgemm::kExpertTiles;
 }
 
 int validate(int form, int64_t rows, int64_t experts, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
@@ -90,7 +93,7 @@ int select(int form, int64_t rows, int64_t experts, int64_t M, int64_t N, int64_
   const int v = validate(form, rows, experts, M, N, K, A, lda, offsets, B, ldb, stride_b, C, ldc, stride_c);
   if (v != TGEMM_OK) return v;
   if (N == 0 || (form == tgemm::kExpertTN ? M == 0 : rows == 0)) return kSelectNoop;
-  return tiles_eligible(form, M, N, K, A, lda, B, ldb, stride_b) ? choose(form, rows, experts) : tgemm::kExpertGeneric;
+  return tiles_eligible(form, M, N, K, A, lda, B, ldb, stride_b) ? choose(form, rows, experts, N) : tgemm::kExpertGeneric;
 }
 
 int run(int force, int form, int64_t rows, int64_t experts, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,

@@ -103,11 +103,11 @@ __device__ void zero_rest(const ExpertGemmArgs& g, int part, int parts) {
 }
 
 // ------------------------------------------------------------------------------------
-// BM x BM tiles on the two-group ping-pong schedule (tgemm_pingpong.h): 256 x 256 with k-tiles of
-// 32, or 128 x 128 with k-tiles of 64 of which each wave group takes half, the groups' sums joined at
-// the end. A, B and C point at the tile's first row or column of each.
+// BM x BN tiles on the two-group ping-pong schedule (tgemm_pingpong.h): 256 x 256 with k-tiles of
+// 32, or 128 x 128 and 64 x 128 with k-tiles of 64 of which each wave group takes half, the groups' sums
+// joined at the end. A, B and C point at the tile's first row or column of each.
 template <int BM>
-constexpr int kTileKg = BM == 128 ? 2 : 1;
+constexpr int kTileKg = BM == 256 ? 1 : 2;
 template <int BM>
 constexpr int tile_lds_bytes() {
   constexpr int ring = 4 * 2 * BM * 64 * kTileKg<BM>, st = 8 * StagedTile<BM / 2 / kTileKg<BM>, BM * kTileKg<BM> / 4>::BYTES;
@@ -122,15 +122,15 @@ __device__ __forceinline__ auto& pick_sums(A& own, B& joined) {
     return own;
 }
 
-template <int BM, ExpertForm F>
+template <int BM, int BN, ExpertForm F>
 __device__ __forceinline__ void tile_product(const ExpertGemmArgs& g, char* smem, const _Float16* A, const _Float16* B,
                                              _Float16* C, int mvalid, int nvalid, int K) {
   constexpr int NW = 8, STAGES = 4, KG = kTileKg<BM>, WN = 4 / KG, BK = 32 * KG;
-  constexpr int WTN = BM / WN, FM = BM / 32, FN = WTN / 16;
+  constexpr int WTN = BN / WN, FM = BM / 32, FN = WTN / 16;
   constexpr int WTM = BM / 2 / KG, FE = FM / KG;  // after the groups are joined
   constexpr bool A_KMAJ = F != kExpertTN, B_KMAJ = F == kExpertNT;
   using OpA = PpOperand<BM, BK, 16, A_KMAJ, NW>;
-  using OpB = PpOperand<BM, BK, 16, B_KMAJ, NW>;
+  using OpB = PpOperand<BN, BK, 16, B_KMAJ, NW>;
   constexpr int A_BYTES = OpA::BYTES, B_BYTES = OpB::BYTES, PT = OpA::LD + OpB::LD;
   static_assert(OpA::REM == 0 && OpB::REM == 0, "copies split evenly");
 
@@ -143,7 +143,7 @@ __device__ __forceinline__ void tile_product(const ExpertGemmArgs& g, char* smem
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   mvalid = min(BM, mvalid);
-  nvalid = min(BM, nvalid);
+  nvalid = min(BN, nvalid);
   const int nk = (K + BK - 1) / BK, kin_last = K - (nk - 1) * BK;
 
   OpA opa;
@@ -226,10 +226,14 @@ struct Cut {
 // The tiles of the rows' form, in the order in which its workgroups take them (workgroup w those at w,
 // w + gridDim.x, ...): `kept` big tiles; the other big ones in quarters; the small ones. One big tile
 // takes about as long as three small ones, so big tiles that would fill less than half of the compute
-// units in a last round go in quarters. (Counts are of 32 bits: the host keeps those of offsets that
-// do not decrease below 2^31, and the length of the list below that bound whatever the offsets hold.)
+// units in a last round go in quarters; and the small ones that would fill no more than half of them
+// in a last round go in halves, 64 x 128, which take two thirds to four fifths of a small one's time
+// (4096 rows, 8 experts, 4096 x 2048: 88 to 85 us; 8190, 2048 x 1032: 55 to 52.5; 300 rows, one of 4096 x
+// 4096: 30 to 26). (Counts are of 32 bits: the host keeps those of offsets that do not decrease below
+// 2^31, and the length of the list below that bound whatever the offsets hold.)
 struct TileList {
   uint32_t kept, quarters, edges;  // big tiles, quarters (4 a tile), edge tiles
+  uint32_t halved;                 // of the last two, the ones that go in halves
   __device__ void cut(uint32_t big, uint32_t small, int mode) {
     constexpr uint32_t G = kExpertTileGroups;
     const uint32_t rest = big % G;
@@ -242,6 +246,8 @@ struct TileList {
     kept = mode == kTilesSmall ? 0 : keep ? big : big - rest;
     quarters = 4 * (big - kept);
     edges = small;
+    const uint32_t last = (quarters + edges) % G;
+    halved = mode == kTilesAuto && kept % G == 0 && last <= G / 2 ? last : 0;
   }
 };
 
@@ -250,7 +256,7 @@ struct Tile {
   int e;
   uint32_t row0, col0;
   RowRange rows;
-  bool big;
+  int size;  // its rows: 256, 128 or 64 (of 128 columns)
   // tile i of the big ones (or quarter 0 .. 3 of it) or of the small ones of a part cut by c
   __device__ void place(const Cut& c, uint32_t i, bool of_big, uint32_t quarter) {
     if (of_big) {  // panels of four tile rows, the tile rows of a panel first
@@ -263,7 +269,7 @@ struct Tile {
       row0 = lower ? c.low : 128 * (i - c.low_count);
       col0 = lower ? 128 * i : 256 * c.nb;
     }
-    big = of_big && quarter == 4;
+    size = of_big && quarter == 4 ? 256 : 128;
   }
   __device__ void make_uniform() {
     e = __builtin_amdgcn_readfirstlane(e);
@@ -327,20 +333,28 @@ __device__ __forceinline__ void init_finder(const ExpertGemmArgs& g, TG_LDS Tile
     f->list.kept = list.kept;
     f->list.quarters = list.quarters;
     f->list.edges = list.edges;
+    f->list.halved = list.halved;
   }
 }
 
 // Tile `at` of the list into t (uniform); false past its end.
 __device__ __forceinline__ bool find_in_rows(const ExpertGemmArgs& g, const TG_LDS TileFinder* f, uint32_t at, int lane, Tile& t) {
-  const uint32_t kept = uniform(f->list.kept), quarters = uniform(f->list.quarters), rest = quarters + uniform(f->list.edges);
-  if (at >= min(kept + rest, g.max_tiles)) return false;
+  const uint32_t kept = uniform(f->list.kept), quarters = uniform(f->list.quarters), halved = uniform(f->list.halved);
+  const uint32_t rest = quarters + uniform(f->list.edges) - halved;
+  if (at >= min(kept + rest + 2 * halved, g.max_tiles)) return false;
   // i: which of the big tiles, or of the small ones; a quarter names its big tile
-  uint32_t i, quarter = 4;
+  uint32_t i, quarter = 4, half = 2;
   bool big = true;
   if (at < kept) {
     i = xcd_id(at, kept);
   } else {
-    i = xcd_id(at - kept, rest);
+    if (at < kept + rest) {
+      i = xcd_id(at - kept, rest);
+    } else {
+      i = xcd_id(at - kept - rest, 2 * halved);
+      half = i & 1;
+      i = rest + i / 2;
+    }
     big = i < quarters;
     if (big) {
       quarter = i & 3;
@@ -366,6 +380,10 @@ __device__ __forceinline__ bool find_in_rows(const ExpertGemmArgs& g, const TG_L
     i -= n;
     ++t.e;
   }
+  if (half < 2) {
+    t.row0 += 64 * half;
+    t.size = 64;
+  }
   t.make_uniform();
   return true;
 }
@@ -387,16 +405,18 @@ __global__ __launch_bounds__(512) void expert_tiles(ExpertGemmArgs args) {
     __syncthreads();  // the list is there, and every wave has stored its part of the tile before
     Tile t;
     if (!find_in_rows(g, finder, at, lane, t)) break;
-    // (offsets that run backwards can leave no such tile)
+    // (a quarter or a half past the edge; offsets that run backwards can leave no such tile)
     if (t.row0 >= (uint32_t)t.rows.count || t.col0 >= (uint32_t)g.N) continue;
     const int64_t first = (int64_t)t.rows.first + t.row0;
     const _Float16* const A = g.A + first * g.lda;
     const _Float16* const B = g.B + t.e * g.stride_b + (F == kExpertNT ? (int64_t)t.col0 * g.ldb : t.col0);
     _Float16* const C = g.C + first * g.ldc + t.col0;
-    if (t.big)
-      tile_product<256, F>(g, smem, A, B, C, t.rows.count - t.row0, g.N - t.col0, g.K);
+    if (t.size == 256)
+      tile_product<256, 256, F>(g, smem, A, B, C, t.rows.count - t.row0, g.N - t.col0, g.K);
+    else if (t.size == 64)
+      tile_product<64, 128, F>(g, smem, A, B, C, t.rows.count - t.row0, g.N - t.col0, g.K);
     else
-      tile_product<128, F>(g, smem, A, B, C, t.rows.count - t.row0, g.N - t.col0, g.K);
+      tile_product<128, 128, F>(g, smem, A, B, C, t.rows.count - t.row0, g.N - t.col0, g.K);
   }
   zero_rest<512>(args, blockIdx.x, gridDim.x);
 }
@@ -538,10 +558,10 @@ __global__ __launch_bounds__(512) void expert_tiles_weights(ExpertGemmArgs args)
     const _Float16* const A = g.A + first * g.lda + t.row0;
     const _Float16* const B = g.B + first * g.ldb + t.col0;
     _Float16* const C = g.C + t.e * g.stride_c + (int64_t)t.row0 * g.ldc + t.col0;
-    if (t.big)
-      tile_product<256, kExpertTN>(g, smem, A, B, C, g.M - t.row0, g.N - t.col0, t.rows.count);
+    if (t.size == 256)
+      tile_product<256, 256, kExpertTN>(g, smem, A, B, C, g.M - t.row0, g.N - t.col0, t.rows.count);
     else
-      tile_product<128, kExpertTN>(g, smem, A, B, C, g.M - t.row0, g.N - t.col0, t.rows.count);
+      tile_product<128, 128, kExpertTN>(g, smem, A, B, C, g.M - t.row0, g.N - t.col0, t.rows.count);
   }
 }
 
