@@ -279,7 +279,7 @@ __global__ __launch_bounds__(256) void expert_gather(ExpertRowsArgs g, uint32_t 
   if (u >= (uint64_t)g.tokens * cpr) return;
   const uint32_t t = (uint32_t)u / cpr, c = (uint32_t)u - t * cpr;  // the host keeps the chunks below 2^32
   const int n = g.H - 8 * (int)c;
-  const half8 x = load_half8(g.src + (int64_t)t * g.lds_ + 8 * c, n);
+  const half8 x = load_half8(g.src + (int64_t)t * g.lds_ + 8 * c, (int)(8 * c), n);
   const int* const place = g.place + (int64_t)t * g.k;
   for (int j0 = 0; j0 < g.k; j0 += 4) {  // four places before the first store
     int p[4];
@@ -315,7 +315,7 @@ __global__ __launch_bounds__(256) void expert_combine(ExpertRowsArgs g) {
       y[q] = (half8){0, 0, 0, 0, 0, 0, 0, 0};
       w[q] = 0.0f;
       if (live) {
-        y[q] = load_half8(g.src + (int64_t)p * g.lds_ + 8 * c, n);
+        y[q] = load_half8(g.src + (int64_t)p * g.lds_ + 8 * c, (int)(8 * c), n);
         w[q] = slot_weight(g, s0 + j0 + q);
       }
     }
@@ -350,7 +350,7 @@ __global__ __launch_bounds__(256) void expert_combine_grad(ExpertRowsArgs g, uin
 #pragma unroll 4
     for (uint32_t c = lane; c < cpr; c += 64) {
       const int n = g.H - 8 * (int)c;
-      const half8 a = load_half8(d + 8 * c, n), b = g.dweights != nullptr ? load_half8(y + 8 * c, n) : a;
+      const half8 a = load_half8(d + 8 * c, (int)(8 * c), n), b = g.dweights != nullptr ? load_half8(y + 8 * c, (int)(8 * c), n) : a;
       half8 v;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {

@@ -705,8 +705,8 @@ __global__ __launch_bounds__(256) void expert_generic(ExpertGemmArgs g) {
     for (int i = 0; i < UNITS; ++i) {
       const int u = i * 256 + tid, line = u / Op::CPR, c = 8 * ((u % Op::CPR) ^ Op::swz(line));
       const int k = BK * kt + (Op::KMAJOR ? c : line), r = Op::KMAJOR ? line : c;
-      v[i] = Op::KMAJOR ? load_half8(X + (int64_t)r * ld + k, r < valid ? K - k : 0)
-                        : load_half8(X + (int64_t)k * ld + r, k < K ? valid - r : 0);
+      v[i] = Op::KMAJOR ? load_half8(X + (int64_t)r * ld + k, k, r < valid ? K - k : 0)
+                        : load_half8(X + (int64_t)k * ld + r, r, k < K ? valid - r : 0);
     }
   };
   auto put = [&](char* slot, const half8 (&v)[UNITS]) __attribute__((always_inline)) {

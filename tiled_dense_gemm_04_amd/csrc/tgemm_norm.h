@@ -8,7 +8,9 @@ namespace tgemm {
 
 constexpr int kNormMaxK = 16384;     // a row is held in one workgroup's registers
 // Threads that hold a row of K values.
-constexpr int norm_row_threads(int64_t K) { return K <= 128 ? 16 : K <= 256 ? 32 : K <= 1024 ? 64 : K <= 4096 ? 256 : K <= 8192 ? 512 : 1024; }
+constexpr int norm_row_threads(int64_t K) {
+  return K <= 128 ? 16 : K <= 256 ? 32 : K <= 1024 ? 64 : K <= 4096 ? 256 : K <= 8192 ? 512 : 1024;
+}
 
 // Residual types (kNone: no residual, the norm is of X itself).
 enum NormResidual { kResNone = 0, kResF16 = 1, kResF32 = 2 };

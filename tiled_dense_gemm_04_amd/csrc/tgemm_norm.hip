@@ -31,7 +31,7 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*lds)[N]) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = 0.0f;
-#pragma unroll
+#pragma unroll 8
     for (int w = 0; w < TPR / 64; ++w)
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] += lds[w][i];
@@ -88,17 +88,17 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_rows(NormArgs g
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int k = 8 * (t + i * TPR), n = g.K - k;
-    half8 x = load_half8(g.X + r * g.ldx + k, n);
-    if constexpr (RES == kResF32) load_float8((const float*)g.Rin + r * g.ldr + k, n, h[i]);
+    half8 x = load_half8(g.X + r * g.ldx + k, k, n);
+    if constexpr (RES == kResF32) load_float8((const float*)g.Rin + r * g.ldr + k, k, n, h[i]);
     if constexpr (RES == kResF16) {
-      const half8 a = load_half8((const _Float16*)g.Rin + r * g.ldr + k, n);
+      const half8 a = load_half8((const _Float16*)g.Rin + r * g.ldr + k, k, n);
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[i][e] = (float)a[e];
     }
     if (g.w_f32) {
-      load_float8((const float*)g.W + k, n, w[i]);
+      load_float8((const float*)g.W + k, k, n, w[i]);
     } else {
-      const half8 a = load_half8((const _Float16*)g.W + k, n);
+      const half8 a = load_half8((const _Float16*)g.W + k, k, n);
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[i][e] = (float)a[e];
     }
@@ -163,9 +163,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_grad_rows(NormG
   for (int i = 0; i < CH; ++i) {
     const int k = 8 * (t + i * TPR), n = g.K - k;
     if (g.w_f32) {
-      load_float8((const float*)g.W + k, n, w[i]);
+      load_float8((const float*)g.W + k, k, n, w[i]);
     } else {
-      const half8 a = load_half8((const _Float16*)g.W + k, n);
+      const half8 a = load_half8((const _Float16*)g.W + k, k, n);
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[i][e] = (float)a[e];
     }
@@ -177,17 +177,20 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_grad_rows(NormG
   for (int64_t first = (int64_t)blockIdx.x * RPG; first < g.R; first += (int64_t)gridDim.x * RPG, parity ^= 1) {
     const bool live = first + sub < g.R;
     const int64_t r = live ? first + sub : g.R - 1;
+    // (a column of the row's own: what follows from it, conditions above all, would spill if kept over the loop)
+    int column = t;
+    asm volatile("" : "+v"(column));
     half8 dy[CH];
     float h[CH][8];
     float sum[2] = {0.0f, 0.0f};  // of h^2 and of w dy h
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      const int k = 8 * (t + i * TPR), n = g.K - k;
-      dy[i] = load_half8(g.dY + r * g.lddy + k, n);
+      const int k = 8 * (column + i * TPR), n = g.K - k;
+      dy[i] = load_half8(g.dY + r * g.lddy + k, k, n);
       if constexpr (H32) {
-        load_float8((const float*)g.H + r * g.ldh + k, n, h[i]);
+        load_float8((const float*)g.H + r * g.ldh + k, k, n, h[i]);
       } else {
-        const half8 a = load_half8((const _Float16*)g.H + r * g.ldh + k, n);
+        const half8 a = load_half8((const _Float16*)g.H + r * g.ldh + k, k, n);
 #pragma unroll
         for (int e = 0; e < 8; ++e) h[i][e] = (float)a[e];
       }
@@ -204,15 +207,15 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_grad_rows(NormG
     if (live) {
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int k = 8 * (t + i * TPR), n = g.K - k;
+        const int k = 8 * (column + i * TPR), n = g.K - k;
         float dx[8], dh[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) dh[e] = 0.0f;
         if (g.dH != nullptr) {
           if constexpr (H32) {
-            load_float8((const float*)g.dH + r * g.lddh + k, n, dh);
+            load_float8((const float*)g.dH + r * g.lddh + k, k, n, dh);
           } else {
-            const half8 a = load_half8((const _Float16*)g.dH + r * g.lddh + k, n);
+            const half8 a = load_half8((const _Float16*)g.dH + r * g.lddh + k, k, n);
 #pragma unroll
             for (int e = 0; e < 8; ++e) dh[e] = (float)a[e];
           }
