@@ -187,6 +187,13 @@ def test_row_gradients(gpu, shape):
 
 
 # ------------------------------------------------------------------ products
+def test_every_row_end(gpu):
+    """Rows that end in every place of a chunk of eight, up to one chunk and past it."""
+    for H in range(2, 18):
+        test_gather_and_combine(gpu, (37, 3, 5, H))
+        test_row_gradients(gpu, (37, 3, 5, H))
+
+
 def small_ints(rng, *shape):
     """Integers of -2 .. 2: any sum of up to 2^22 products of two is exact in float32."""
     return rng.integers(-2, 3, shape).astype(np.float16)

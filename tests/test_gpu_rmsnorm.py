@@ -66,6 +66,22 @@ def test_norm(gpu, shape, residual):
         assert np.array_equal(rd.cpu().numpy(), r)
 
 
+@pytest.mark.parametrize("residual", [None, np.float16, np.float32], ids=lambda r: "none" if r is None else r.__name__)
+def test_every_row_end(gpu, residual):
+    """Rows that end in every place of a chunk of eight, up to one chunk, past it, and in the shapes of 4 and 6
+    waves a row; forward and backward."""
+    for K in [*range(2, 18), 2559, *range(2561, 2568), 3071, 3073]:
+        x, r, w = case(3, K, residual, w32=K % 2 == 1)
+        xd, wd, rd = to_dev(x), to_dev(w), None if r is None else to_dev(r)
+        h = ref.stored(x, r)
+        got, coded = tg.rmsnorm(xd, wd, rd, eps=EPS), tg.rmsnorm_fp8_block(xd, wd, rd, eps=EPS)
+        check_y(got if r is None else got[0], h, w)
+        check_codes(coded[0], coded[1], h, w)
+        if r is not None:
+            assert np.array_equal(got[1].cpu().numpy(), h), K
+        test_gradient(gpu, (3, K), residual)
+
+
 def test_strides_alignment_and_untouched_memory(gpu):
     for K in (1000, 129, 4100):
         x, r, w = case(6, K, np.float32)

@@ -74,7 +74,7 @@ __device__ __forceinline__ float block_codes(const float (&y)[8], uint2v& codes)
 // Forward. TPR threads a row, CH chunks of eight values a thread: thread t holds chunks t + i TPR,
 // so a 1 x 128 block is 16 neighbouring lanes. The residual, x and the weight of a row are all in
 // flight before the one reduction. 16384 x 4096 with a binary16 residual: 99 us (5.4 TB/s) to binary16, 87
-// to codes (5.4), where a copy of 1 GiB reaches 5.2; 4095 x 3000 with a float32 one 32 (4.6); one row of
+// to codes (5.4), where a copy of 1 GiB reaches 5.2; 4095 x 3000 with a float32 one 29 (5.1); one row of
 // 4096 3.5 and 4.1 with its launch.
 template <int TPR, int CH, int RES>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void rmsnorm_rows(NormArgs g) {
@@ -301,6 +301,9 @@ hipError_t launch_rows(const NormArgs& g, hipStream_t s) {
 template <int RES>
 hipError_t launch_forward(const NormArgs& g, hipStream_t s) {
 #define TGEMM_NORM_LAUNCH(TPR, CH) (launch_rows<TPR, CH, RES>(g, s))
+  // (six waves of one chunk: 4095 x 3000 with a float32 residual 31.7 us in four waves of two, so 29.2; 16384 x
+  // 3000 116 and 110; but 16384 x 2049 with a binary16 one 59 and 68. The runtime takes fewer than 2^32 threads.)
+  if (g.K >= 2560 && g.K <= 384 * 8 && g.R <= (1 << 23)) return launch_rows<384, 1, RES>(g, s);
   TGEMM_NORM_SHAPES(TGEMM_NORM_LAUNCH, g.K)
 #undef TGEMM_NORM_LAUNCH
 }
