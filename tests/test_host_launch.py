@@ -1,0 +1,64 @@
+"""What the expert layer's entry points launch, on the CPU: the host code of the kernels' file and of
+its entry points, linked with a HIP runtime that only records launches (tests/host_launch/)."""
+import os
+import subprocess
+
+import pytest
+
+import tiled_dense_gemm_04_amd as tg
+from tiled_dense_gemm_04_amd import build as libbuild
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HERE = os.path.join(ROOT, "tests", "host_launch")
+CSRC = os.path.join(ROOT, "tiled_dense_gemm_04_amd", "csrc")
+P = 256  # stands for an aligned device pointer; never dereferenced
+
+
+@pytest.fixture(scope="module")
+def driver(tmp_path_factory):
+    try:
+        hipcc = libbuild.hipcc()
+    except RuntimeError as e:
+        pytest.skip(str(e))
+    out = str(tmp_path_factory.mktemp("host_launch"))
+    include = ["-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
+    kernels = os.path.join(out, "expert.o")
+    for cmd in ([hipcc, "--offload-arch=" + libbuild.ARCH, "--offload-host-only", "-std=c++17", "-O1", *include, "-c",
+                 os.path.join(CSRC, "tgemm_expert.hip"), "-o", kernels],
+                ["/opt/rocm/llvm/bin/clang++", "-std=c++17", "-O1", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", *include,
+                 os.path.join(CSRC, "tgemm_expert_api.cpp"), os.path.join(HERE, "driver.cpp"), kernels,
+                 "-Wl,--unresolved-symbols=ignore-all",  # (the device code's image, whose name is the compiler's)
+                 "-o", os.path.join(out, "driver")]):
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        assert r.returncode == 0, r.stderr[-4000:]
+
+    def call(*args):
+        r = subprocess.run([os.path.join(out, "driver"), *map(str, args)], capture_output=True, text=True, timeout=60)
+        assert r.returncode == 0, r.stderr[-2000:]
+        *launches, rc = r.stdout.split("\n")[:-1]
+        return int(rc.split()[1]), [(name, int(groups), int(main)) for name, groups, main in map(str.split, launches)]
+
+    return call
+
+
+def test_gather_without_choices_reads_no_row(driver):
+    """Tokens of no slots: only the workgroups that zero rows run, so x and place, which may then be null,
+    are not read."""
+    for tokens, H in ((5, 64), (1, 1), (4096, 4096)):
+        rc, launches = driver("gather", tokens, 0, 20, H, 0, 0, P, P, 8)
+        assert rc == tg.TGEMM_OK and len(launches) == 1
+        name, groups, main = launches[0]
+        assert "expert_gather" in name and main == 0 and groups > 0
+        assert driver("gather", tokens, 0, 20, H, 0, 0, P, 0, 0) == (tg.TGEMM_OK, [])  # nothing to write
+    # with slots: a workgroup for 256 chunks of eight values, and those that zero rows
+    rc, launches = driver("gather", 5, 2, 10, 4096, P, P, P, P, 8)
+    zeroing = groups
+    assert rc == tg.TGEMM_OK and launches[0][1:] == (10 + zeroing, 10)
+    rc, launches = driver("gather", 5, 2, 10, 4096, P, P, P, 0, 0)
+    assert rc == tg.TGEMM_OK and launches[0][1:] == (10, 10)
+    assert driver("gather", 5, 2, 10, 4096, 0, P, P, P, 8) == (tg.TGEMM_ENULL, [])
+
+
+def test_combine_gradient_without_choices_reads_no_row(driver):
+    rc, launches = driver("combine_grad", 5, 0, 20, 64, 0, 0, 0, P, P, 8)
+    assert rc == tg.TGEMM_OK and len(launches) == 1 and launches[0][2] == 0 and launches[0][1] > 0

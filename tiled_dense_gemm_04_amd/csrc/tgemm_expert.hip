@@ -399,7 +399,8 @@ hipError_t launch_expert_sort(const ExpertSortArgs& g, hipStream_t s) {
 }
 
 hipError_t launch_expert_gather(const ExpertRowsArgs& g, hipStream_t s) {
-  const uint32_t main = chunk_groups(g), all = main + (g.offsets != nullptr ? kRestGroups : 0);
+  // (without slots no row goes anywhere, and src may be null: none is read)
+  const uint32_t main = g.k == 0 ? 0 : chunk_groups(g), all = main + (g.offsets != nullptr ? kRestGroups : 0);
   if (all == 0) return hipSuccess;
   hipLaunchKernelGGL(expert_gather, dim3(all), dim3(256), 0, s, g, main);
   return hipGetLastError();
