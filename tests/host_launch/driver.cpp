@@ -3,6 +3,7 @@
 // return code, then a line per launch: the kernel, its workgroups, and the count of `main` workgroups
 // that kernels of rows take as their second argument.
 //   driver gather TOKENS K ROWS H X PLACE XS OFFSETS EXPERTS      (pointers as numbers; never read)
+//   driver rows FIRST ROWS N          (no entry point: the rows that a zeroing workgroup goes over, one a line)
 //   driver combine_grad TOKENS K ROWS H DOUT Y PLACE DY OFFSETS EXPERTS
 #include <hip/hip_runtime.h>
 
@@ -77,6 +78,8 @@ int main(int argc, char** argv) {
     rc = expert_combine_f16_backward(number(argv[2]), number(argv[3]), number(argv[4]), H, pointer(argv[6]), ld, pointer(argv[7]),
                                      ld, pointer(argv[8]), nullptr, TGEMM_DTYPE_F32, pointer(argv[9]), ld, nullptr,
                                      pointer(argv[10]), number(argv[11]), nullptr);
+  } else if (argc == 5 && !std::strcmp(argv[1], "rows")) {
+    tgemm::every_nth_row(number(argv[2]), number(argv[3]), number(argv[4]), [](int64_t r) { std::printf("row %lld 0\n", (long long)r); });
   } else {
     return 2;
   }

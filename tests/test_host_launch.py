@@ -62,3 +62,11 @@ def test_gather_without_choices_reads_no_row(driver):
 def test_combine_gradient_without_choices_reads_no_row(driver):
     rc, launches = driver("combine_grad", 5, 0, 20, 64, 0, 0, 0, P, P, 8)
     assert rc == tg.TGEMM_OK and len(launches) == 1 and launches[0][2] == 0 and launches[0][1] > 0
+
+
+def test_rows_to_zero_near_the_largest_index(driver):
+    """The step behind the last row may pass 2^31."""
+    rows = (1 << 31) - 1
+    for first, n in ((rows - 100, 64), (rows - 1, 64), (rows - 64, 64), (rows, 64), (rows - 300, 256), (5, 1 << 30)):
+        rc, visited = driver("rows", first, rows, n)
+        assert rc == 0 and [int(r) for _, r, _ in visited] == list(range(first, rows, n))

@@ -9,6 +9,12 @@ namespace tgemm {
 
 constexpr int kMaxExperts = 1024;
 
+// f(row) for the rows first, first + n, ... before `rows` (64 bits: the row after the last may lie past 2^31).
+template <typename F>
+__host__ __device__ inline void every_nth_row(int64_t first, int64_t rows, int64_t n, F&& f) {
+  for (int64_t r = first; r < rows; r += n) f(r);
+}
+
 // Sorting. Slot s = t * k + j holds the id of choice j of token t.
 struct ExpertSortArgs {
   const void* ids;

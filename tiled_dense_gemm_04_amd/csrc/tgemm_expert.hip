@@ -267,9 +267,10 @@ __device__ __forceinline__ int rows_in_use(const ExpertRowsArgs& g) {
 constexpr int kRestGroups = 64;
 __device__ __forceinline__ void zero_rest_rows(const ExpertRowsArgs& g, int part, uint32_t cpr) {
   const half8 zero = {0, 0, 0, 0, 0, 0, 0, 0};
-  for (int r = rows_in_use(g) + part; r < g.rows; r += kRestGroups)
+  every_nth_row(rows_in_use(g) + (int64_t)part, g.rows, kRestGroups, [&](int64_t r) {
     for (uint32_t c = threadIdx.x; c < cpr; c += 256)
-      store_half8(g.dst + (int64_t)r * g.ldd + 8 * c, zero, g.H - 8 * (int)c);
+      store_half8(g.dst + r * g.ldd + 8 * c, zero, g.H - 8 * (int)c);
+  });
 }
 
 __global__ __launch_bounds__(256) void expert_gather(ExpertRowsArgs g, uint32_t main) {

@@ -97,9 +97,10 @@ template <int THREADS>
 __device__ void zero_rest(const ExpertGemmArgs& g, int part, int parts) {
   if (!g.zero_rest || parts == 0) return;
   const half8 zero = {0, 0, 0, 0, 0, 0, 0, 0};
-  const int chunks = (g.N + 7) / 8;
-  for (int64_t r = (int64_t)clamped(g, g.experts) + part; r < g.rows; r += parts)
-    for (int c = threadIdx.x; c < chunks; c += THREADS) store_half8(g.C + r * g.ldc + 8 * c, zero, g.N - 8 * c);
+  const uint32_t chunks = ((uint32_t)g.N + 7) / 8;
+  every_nth_row(clamped(g, g.experts) + (int64_t)part, g.rows, parts, [&](int64_t r) {
+    for (uint32_t c = threadIdx.x; c < chunks; c += THREADS) store_half8(g.C + r * g.ldc + 8 * c, zero, g.N - 8 * (int)c);
+  });
 }
 
 // ------------------------------------------------------------------------------------
