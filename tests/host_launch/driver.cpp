@@ -4,6 +4,7 @@
 // that kernels of rows take as their second argument.
 //   driver gather TOKENS K ROWS H X PLACE XS OFFSETS EXPERTS      (pointers as numbers; never read)
 //   driver rows FIRST ROWS N          (no entry point: the rows that a zeroing workgroup goes over, one a line)
+//   driver k_tiles K BK               (no entry point: the k-tiles of a product, and k values in the last)
 //   driver combine_grad TOKENS K ROWS H DOUT Y PLACE DY OFFSETS EXPERTS
 #include <hip/hip_runtime.h>
 
@@ -80,6 +81,9 @@ int main(int argc, char** argv) {
                                      pointer(argv[10]), number(argv[11]), nullptr);
   } else if (argc == 5 && !std::strcmp(argv[1], "rows")) {
     tgemm::every_nth_row(number(argv[2]), number(argv[3]), number(argv[4]), [](int64_t r) { std::printf("row %lld 0\n", (long long)r); });
+  } else if (argc == 4 && !std::strcmp(argv[1], "k_tiles")) {
+    const int K = (int)number(argv[2]), BK = (int)number(argv[3]), nk = tgemm::k_tiles(K, BK);
+    std::printf("k_tiles %d %d\n", nk, nk > 0 ? K - (nk - 1) * BK : 0);
   } else {
     return 2;
   }

@@ -70,3 +70,11 @@ def test_rows_to_zero_near_the_largest_index(driver):
     for first, n in ((rows - 100, 64), (rows - 1, 64), (rows - 64, 64), (rows, 64), (rows - 300, 256), (5, 1 << 30)):
         rc, visited = driver("rows", first, rows, n)
         assert rc == 0 and [int(r) for _, r, _ in visited] == list(range(first, rows, n))
+
+
+def test_k_tiles_of_the_longest_sums(driver):
+    """An expert's rows, which the weights' form sums over, may be any number below 2^31."""
+    for K in (0, 1, 31, 32, 33, 64, 65, 5000, (1 << 31) - 65, (1 << 31) - 64, (1 << 31) - 63, (1 << 31) - 31, (1 << 31) - 1):
+        for BK in (32, 64):
+            nk = -(-K // BK)
+            assert driver("k_tiles", K, BK)[1] == [("k_tiles", nk, K - (nk - 1) * BK if nk else 0)]

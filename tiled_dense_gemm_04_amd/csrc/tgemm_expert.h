@@ -57,6 +57,8 @@ struct ExpertGemmArgs {
   int mode;                                   // of the tile kernel, and the most tiles its rows' form goes over
   uint32_t max_tiles;
 };
+// k-tiles of BK of K values (an expert's rows in the weights' form: up to 2^31 - 1).
+__host__ __device__ constexpr int k_tiles(int K, int BK) { return (int)(((uint32_t)K + (uint32_t)BK - 1) / (uint32_t)BK); }
 enum ExpertForm { kExpertNT = 0, kExpertNN = 1, kExpertTN = 2 };
 // Kernels of a product, by index (tooling ABI: the _cfg entry point). kExpertTiles mixes tiles of 256 x
 // 256, 128 x 128 and, in the rows' form, 64 x 128; kExpert128 and kExpert256 are the same kernel held to one of them (but for

@@ -145,7 +145,7 @@ __device__ __forceinline__ void tile_product(const ExpertGemmArgs& g, char* smem
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   mvalid = min(BM, mvalid);
   nvalid = min(BN, nvalid);
-  const int nk = (K + BK - 1) / BK, kin_last = K - (nk - 1) * BK;
+  const int nk = k_tiles(K, BK), kin_last = K - (nk - 1) * BK;
 
   OpA opa;
   OpB opb;
@@ -596,7 +596,7 @@ __global__ __launch_bounds__(256) void expert_small(ExpertGemmArgs g) {
   if (t.e < 0) return zero_rest<256>(g, t.past, t.past_count);
   const int row0 = t.tm * BM, col0 = t.tn * BN;
   const int mvalid = min(BM, t.rows.count - row0), nvalid = min(BN, g.N - col0);
-  const int nk = (g.K + BK - 1) / BK, kin_last = g.K - (nk - 1) * BK;
+  const int nk = k_tiles(g.K, BK), kin_last = g.K - (nk - 1) * BK;
   OpA opa;
   OpB opb;
   opa.init_copies(g.A + (int64_t)t.rows.first * g.lda, g.lda, row0, mvalid, kin_last, wave, lane);
@@ -725,7 +725,7 @@ __global__ __launch_bounds__(256) void expert_generic(ExpertGemmArgs g) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = (float4v){0.0f, 0.0f, 0.0f, 0.0f};
   half8 av[UNITS], bv[UNITS];
-  const int nk = (K + BK - 1) / BK;
+  const int nk = k_tiles(K, BK);
   if (nk > 0) {
     fetch(OpA{}, A, g.lda, mvalid, 0, av);
     fetch(OpB{}, B, g.ldb, nvalid, 0, bv);
