@@ -47,3 +47,39 @@ def test_zeroed_rows_near_the_largest_index(gpu):
     assert L.expert_combine_f16_backward(0, 0, rows, 1, None, 1, None, 1, None, None, 1, out.data_ptr(), 1, None,
                                          offsets.data_ptr(), 2, stream) == tg.TGEMM_OK
     assert (out[used:] == 0).all() and (out[used - 1000:used] == 3).all() and (out[:4096] == 3).all()
+
+
+def saved_by(gpu, call):
+    """(outputs of call, the shapes of what its functions keep for their backward passes)."""
+    shapes = []
+
+    def pack(t):
+        shapes.append(tuple(t.shape))
+        return t
+
+    with gpu.autograd.graph.saved_tensors_hooks(pack, lambda t: t):
+        return call(), sorted(shapes)
+
+
+def test_combine_keeps_its_rows_for_the_weights_gradient_only(gpu):
+    """The rows (T k x H) are held, and may not be changed in place, only where a weight's gradient reads them."""
+    rng = np.random.default_rng(1)
+    T, k, E, H = 40, 3, 8, 264
+    plan = tg.expert_sort(to_dev(rng.integers(0, E, (T, k))), E)
+    y, w = to_dev(rng.standard_normal((T * k, H)).astype(np.float16)), to_dev(rng.random((T, k)).astype(np.float32))
+    dout = to_dev(rng.standard_normal((T, H)).astype(np.float16))
+    full = [y.clone().requires_grad_(), w.clone().requires_grad_()]
+    out, kept = saved_by(gpu, lambda: tg.ExpertCombineFunction.apply(*full, *plan))
+    assert (T * k, H) in kept
+    dy, dw = gpu.autograd.grad(out, full, dout)
+    rows = y.clone().requires_grad_()
+    inner = rows * 1
+    out, kept = saved_by(gpu, lambda: tg.ExpertCombineFunction.apply(inner, w, *plan))
+    assert kept == sorted([(E + 1,), (T, k), (T, k)])
+    inner.detach().zero_()  # what the backward pass does not read may change
+    assert gpu.equal(gpu.autograd.grad(out, rows, dout)[0], dy)
+    out, kept = saved_by(gpu, lambda: tg.ExpertCombineFunction.apply(rows, None, *plan))
+    assert kept == sorted([(E + 1,), (T, k)])
+    gate = w.clone().requires_grad_()
+    out, kept = saved_by(gpu, lambda: tg.ExpertCombineFunction.apply(y, gate, *plan))
+    assert (T * k, H) in kept and gpu.equal(gpu.autograd.grad(out, gate, dout)[0], dw)

@@ -302,8 +302,9 @@ def autograd_functions():
             y = _row_major(y, "y")
             weights = None if weights is None else weights.contiguous()
             out = expert_combine(y, ExpertOrder(offsets, order, place), weights)
-            ctx.experts = _offsets(offsets, y.device)
-            kept = (offsets, place, y) if weights is None else (offsets, place, y, weights)
+            ctx.experts, ctx.rows = _offsets(offsets, y.device), y.shape
+            # (y is read for the weights' gradient only)
+            kept = (offsets, place) + (() if weights is None else (weights,)) + ((y,) if ctx.needs_input_grad[1] else ())
             ctx.save_for_backward(*kept)
             ctx.saved = _like(*kept)
             return out
@@ -311,17 +312,18 @@ def autograd_functions():
         @staticmethod
         def backward(ctx, dout):
             _once()
-            offsets, place, y, *weights = (t.contiguous() for t in _saved(ctx))
-            (T, k), (rows, H), device = place.shape, y.shape, y.device
-            dout = _grad(dout, "dout", (T, H), device)
             need_y, need_w = ctx.needs_input_grad[:2]
+            offsets, place, *rest = (t.contiguous() for t in _saved(ctx))
+            y, weights = rest.pop() if need_w else None, rest[0] if rest else None
+            (T, k), (rows, H), device = place.shape, ctx.rows, place.device
+            dout = _grad(dout, "dout", (T, H), device)
             dy = torch.empty((rows, H), dtype=f16, device=device) if need_y else None
-            dw = torch.empty_like(weights[0]) if need_w else None
-            w, w_dtype = _weights(weights[0], (T, k), device) if weights else (None, DTYPE_F32)
+            dw = torch.empty_like(weights) if need_w else None
+            w, w_dtype = _weights(weights, (T, k), device)
             ld = H or 1
             _ran(_call("expert_combine_f16_backward",
-                       (T, k, rows, H, dout.data_ptr(), _ld(dout), y.data_ptr(), ld, place.data_ptr(), w, w_dtype,
-                        dy.data_ptr() if need_y else None, ld, dw.data_ptr() if need_w else None, offsets.data_ptr(),
+                       (T, k, rows, H, dout.data_ptr(), _ld(dout), y.data_ptr() if need_w else None, ld, place.data_ptr(), w,
+                        w_dtype, dy.data_ptr() if need_y else None, ld, dw.data_ptr() if need_w else None, offsets.data_ptr(),
                         ctx.experts, _stream(None, device)), device), "expert_combine_f16_backward")
             return dy, dw, None, None, None
 
