@@ -83,3 +83,26 @@ def test_combine_keeps_its_rows_for_the_weights_gradient_only(gpu):
     gate = w.clone().requires_grad_()
     out, kept = saved_by(gpu, lambda: tg.ExpertCombineFunction.apply(y, gate, *plan))
     assert (T * k, H) in kept and gpu.equal(gpu.autograd.grad(out, gate, dout)[0], dw)
+
+
+def test_products_keep_an_operand_for_the_others_gradient_only(gpu):
+    """Frozen experts need no rows kept, and rows without a gradient no experts."""
+    rng = np.random.default_rng(2)
+    rows, E, N, K = 50, 3, 40, 64
+    a, b, dc = (to_dev(rng.integers(-2, 3, s).astype(np.float16)) for s in ((rows, K), (E, N, K), (rows, N)))
+    offsets = to_dev(np.array([0, 20, 20, 47], dtype=np.int32))
+    both = [a.clone().requires_grad_(), b.clone().requires_grad_()]
+    out, kept = saved_by(gpu, lambda: tg.ExpertGemmFunction.apply(*both, offsets))
+    assert kept == sorted([(E + 1,), (rows, K), (E, N, K)])
+    da, db = gpu.autograd.grad(out, both, dc)
+    out, kept = saved_by(gpu, lambda: tg.ExpertGemmFunction.apply(both[0], b, offsets))
+    assert kept == sorted([(E + 1,), (E, N, K)])
+    assert gpu.equal(gpu.autograd.grad(out, both[0], dc)[0], da)
+    inner = a.clone()
+    out, kept = saved_by(gpu, lambda: tg.ExpertGemmFunction.apply(inner, both[1], offsets))
+    assert kept == sorted([(E + 1,), (rows, K)])
+    assert gpu.equal(gpu.autograd.grad(out, both[1], dc)[0], db)
+    # both operands strided where the hooks give them back
+    with gpu.autograd.graph.saved_tensors_hooks(lambda t: t, lambda t: t.repeat_interleave(2, dim=-1)[..., ::2]):
+        out = tg.ExpertGemmFunction.apply(*both, offsets)
+    assert all(gpu.equal(g, w) for g, w in zip(gpu.autograd.grad(out, both, dc), (da, db)))

@@ -337,28 +337,35 @@ def autograd_functions():
             if b.dim() == 3 and b.numel() and (b.stride(2) != 1 or b.stride(1) < b.shape[2]):  # a broadcast weight
                 b = b.contiguous()
             c = expert_gemm_f16(a, b, offsets, zero_rest=True)
-            ctx.save_for_backward(a, b, offsets)
-            ctx.saved = _like(a, b, offsets)
+            need_a, need_b, _ = ctx.needs_input_grad
+            # (a is read for b's gradient and b for a's)
+            kept = (offsets,) + ((b,) if need_a else ()) + ((a,) if need_b else ())
+            ctx.save_for_backward(*kept)
+            ctx.saved = _like(*kept)
+            ctx.shapes = a.shape, b.shape
             return c
 
         @staticmethod
         def backward(ctx, dc):
             _once()
-            a, b, offsets = _saved(ctx)
-            a, offsets = _row_major(a, "a"), offsets.contiguous()
-            if b.stride(-1) != 1 or b.stride(1) < b.shape[2]:
-                b = b.contiguous()
-            (rows, K), (E, N, _), device = a.shape, b.shape, a.device
-            dc = _grad(dc, "dc", (rows, N), device)
             need_a, need_b, _ = ctx.needs_input_grad
+            offsets, *operands = _saved(ctx)
+            offsets = offsets.contiguous()
+            (rows, K), (E, N, _) = ctx.shapes
+            device = offsets.device
+            dc = _grad(dc, "dc", (rows, N), device)
             da = db = None
             stream = _stream(None, device)
             if need_a:
+                b = operands[0]
+                if b.stride(-1) != 1 or b.stride(1) < K:
+                    b = b.contiguous()
                 da = torch.empty((rows, K), dtype=f16, device=device)
                 _ran(_call("expert_gemm_f16", (0, rows, E, K, N, dc.data_ptr(), _ld(dc), offsets.data_ptr(), b.data_ptr(),
                                                b.stride(1) if N > 1 else K or 1, b.stride(0) if E > 1 else 0, da.data_ptr(),
                                                K or 1, 0, 1, stream), device), "expert_gemm_f16")
             if need_b:
+                a = _row_major(operands[-1], "a")
                 db = torch.empty((E, N, K), dtype=f16, device=device)
                 _ran(_call("expert_gemm_f16_tn", (rows, E, N, K, dc.data_ptr(), _ld(dc), a.data_ptr(), _ld(a),
                                                   offsets.data_ptr(), db.data_ptr(), K or 1, N * (K or 1), stream), device),
