@@ -135,8 +135,12 @@ TGEMM_API int orthogonalize_f16(int64_t batch, int64_t R, int64_t C, int dtype,
  * (else TGEMM_ENULL). residual_dtype and w_dtype are TGEMM_DTYPE_F16 or TGEMM_DTYPE_F32 (residual
  * NULL: none, its type is not looked at). K is at most TGEMM_NORM_MAX_K, R times the threads of a row
  * (16 up to K = 128, 32 up to 256, 64 up to 1024, 256 up to 4096, 512 up to 8192, else 1024) at most
- * 2^32 - 2048, eps at least 0 (with 0, a row of zeros gives NaN); else TGEMM_EINVAL_DIM. Pointers need the alignment of their type; no stride or K needs more.
- * Values of h past 1.8e19 (their squares leave float32) give zeros.
+ * 2^32 - 2048, eps at least 0; else TGEMM_EINVAL_DIM. Pointers need the alignment of their type; no stride
+ * or K needs more.
+ * Rows at the ends of float32: the squares are summed before the division by K, so a row whose sum of
+ * squares passes 3.4e38 (a root mean square of 1.8e19 / sqrt(K): 2.9e17 for K = 4096) gives y = 0, codes 0
+ * and scale 1 (and the gradient dX = dH). With eps = 0, rows of zeros give NaN, and rows whose squares fall below 1.2e-38 (values
+ * below 1e-19) lose digits, down to infinities where all of them are 0 (values below 2.6e-23).
  */
 #define TGEMM_NORM_MAX_K 16384
 TGEMM_API int rmsnorm_f16(int64_t R, int64_t K, const void* X, int64_t ldx,
