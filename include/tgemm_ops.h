@@ -139,8 +139,9 @@ TGEMM_API int orthogonalize_f16(int64_t batch, int64_t R, int64_t C, int dtype,
  * or K needs more.
  * Rows at the ends of float32: the squares are summed before the division by K, so a row whose sum of
  * squares passes 3.4e38 (a root mean square of 1.8e19 / sqrt(K): 2.9e17 for K = 4096) gives y = 0, codes 0
- * and scale 1 (and the gradient dX = dH). With eps = 0, rows of zeros give NaN, and rows whose squares fall below 1.2e-38 (values
- * below 1e-19) lose digits, down to infinities where all of them are 0 (values below 2.6e-23).
+ * and scale 1, and the gradient dX = dH. With eps = 0, rows of zeros give NaN, and rows whose squares fall
+ * below 1.2e-38 (values below 1e-19) lose digits, down to infinities where all of them are 0 (values below
+ * 2.6e-23).
  */
 #define TGEMM_NORM_MAX_K 16384
 TGEMM_API int rmsnorm_f16(int64_t R, int64_t K, const void* X, int64_t ldx,

@@ -1,4 +1,5 @@
-"""The norm at the ends of its ranges: rows whose squares approach the ends of float32."""
+"""The norm at the ends of its ranges: rows whose squares approach the ends of float32, and gradients
+of so many rows that every workgroup goes over several in turn."""
 import numpy as np
 import pytest
 
@@ -50,6 +51,9 @@ def test_rows_on_either_side_of_the_largest_sum_of_squares(gpu, K):
     q, s, _ = tg.rmsnorm_fp8_block(to_dev(x), to_dev(w), to_dev(r), eps=EPS)
     assert np.array_equal(h.cpu().numpy(), r)
     assert (y == 0).all() and (q.cpu().numpy() & 127 == 0).all() and (s == 1).all()
+    leaves = [to_dev(t).requires_grad_() for t in (x, w, r)]
+    dx, dw, dr = gpu.autograd.grad(tg.RmsNormFunction.apply(*leaves, EPS), leaves, (to_dev(dy), to_dev(dy.astype(np.float32))))
+    assert np.array_equal(dx.cpu().numpy(), dy) and (dw == 0).all() and np.array_equal(dr.cpu().numpy(), dy.astype(np.float32))
 
 
 def test_rows_without_eps(gpu):
@@ -64,3 +68,43 @@ def test_rows_without_eps(gpu):
     assert (np.abs(tg.rmsnorm(to_dev(x), to_dev(w), to_dev(r), eps=0.0)[0].cpu().numpy() - want) <= ref.y_bound(want)).all()
     r = np.full((1, K), 2.5e-23, dtype=np.float32)
     assert gpu.isinf(tg.rmsnorm(to_dev(x), to_dev(w), to_dev(r), eps=0.0)[0]).all()
+
+
+# (rows, columns, turns of the longest workgroup, rows it holds at once): past the most workgroups that the
+# backward kernel has (1024 of 256 threads, 512 of 512, 256 of 1024), with a last turn that is not full,
+# for every number of threads a row.
+MANY_ROWS = [(40000, 128, 3, 16), (16391, 200, 3, 8), (12290, 520, 4, 4), (9001, 777, 3, 4), (5125, 1032, 6, 1), (3077, 1100, 4, 1),
+             (3077, 2100, 4, 1), (1539, 4104, 4, 1), (769, 8200, 4, 1), (2049, 16383, 9, 1)]
+
+
+@pytest.mark.parametrize("residual", [None, np.float16, np.float32], ids=lambda r: "none" if r is None else r.__name__)
+@pytest.mark.parametrize("R, K, turns, at_once", MANY_ROWS, ids=str)
+def test_gradient_of_many_rows(gpu, R, K, turns, at_once, residual):
+    groups = tg.lib().rmsnorm_f16_backward_workspace_bytes(R, K) // (4 * K)
+    assert -(-R // (groups * at_once)) == turns and groups < -(-R // (2 * at_once))
+    rng = np.random.default_rng(R + K)
+    x, dy = (rng.standard_normal((R, K), dtype=np.float32).astype(np.float16) for _ in range(2))
+    r, dh = (None, None) if residual is None else (rng.standard_normal((R, K), dtype=np.float32).astype(residual) for _ in range(2))
+    w = (1 + 0.2 * rng.standard_normal(K)).astype(np.float32 if K % 2 else np.float16)
+    leaves = [to_dev(t).requires_grad_() for t in (x, w)] + ([] if r is None else [to_dev(r).requires_grad_()])
+
+    def grads():
+        if r is None:
+            return gpu.autograd.grad(tg.RmsNormFunction.apply(*leaves, None, EPS), leaves, to_dev(dy))
+        return gpu.autograd.grad(tg.RmsNormFunction.apply(*leaves, EPS), leaves, (to_dev(dy), to_dev(dh)))
+
+    got = grads()
+    h = ref.stored(x, r)
+    dx, bound, dw, size = ref.gradient(dy, h, w, EPS, dh)
+    assert (np.abs(got[0].cpu().numpy() - dx) <= bound + np.abs(dx) * (ref.HALF16 + 2.0 ** -18) + ref.TINY16).all()
+    if r is not None:
+        step, tiny = (ref.HALF16, ref.TINY16) if residual == np.float16 else (2.0 ** -24, 0.0)
+        assert (np.abs(got[2].cpu().numpy() - dx) <= bound + np.abs(dx) * (step + 2.0 ** -18) + tiny).all()
+    # a thread adds up to 9 rows, up to 16 of its workgroup's threads are joined, then up to 1024 / 16 partial
+    # sums a wave and 16 waves: 105 roundings of 2^-24; the product, xhat and rstd (28) 30 more: below 2^-16
+    tol = size * 2.0 ** -16 + (0.0 if w.dtype == np.float32 else 1.0) * (np.abs(dw) * ref.HALF16 + ref.TINY16)
+    assert (np.abs(got[1].cpu().numpy() - dw) <= tol).all()
+    # which sees a row of the last turn left out
+    xhat = h[-1].astype(np.float64) / np.sqrt((h[-1].astype(np.float64) ** 2).mean() + EPS)
+    assert (np.abs(dy[-1] * xhat) > size * 2.0 ** -16 + (0.0 if w.dtype == np.float32 else 1.0) * np.abs(dw) * ref.HALF16).any()
+    assert all(gpu.equal(a, b) for a, b in zip(got, grads()))  # sums in a fixed order
