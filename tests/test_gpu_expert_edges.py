@@ -2,7 +2,9 @@
 import numpy as np
 import pytest
 
+import expert_reference as ref
 from gpu_util import to_dev, torch_cuda
+from test_gpu_experts import ROWS_ONLY, exact_product, groups, small_ints
 
 import tiled_dense_gemm_04_amd as tg
 
@@ -106,3 +108,28 @@ def test_products_keep_an_operand_for_the_others_gradient_only(gpu):
     with gpu.autograd.graph.saved_tensors_hooks(lambda t: t, lambda t: t.repeat_interleave(2, dim=-1)[..., ::2]):
         out = tg.ExpertGemmFunction.apply(*both, offsets)
     assert all(gpu.equal(g, w) for g, w in zip(gpu.autograd.grad(out, both, dc), (da, db)))
+
+
+def uneven(E, seed):
+    """Counts of E experts, a few with most of the rows, some with none."""
+    rng = np.random.default_rng(seed)
+    counts = rng.integers(0, 40, E)
+    counts[rng.integers(0, E, max(1, E // 8))] = rng.integers(300, 900, max(1, E // 8))
+    return counts
+
+
+@pytest.mark.parametrize("cfg", [None, tg.EXPERT_GENERIC, tg.EXPERT_128, tg.EXPERT_256, tg.EXPERT_TILES], ids=lambda c: f"cfg{c}")
+@pytest.mark.parametrize("E", [7, 8, 33, 63, 64, 65, 130])
+def test_weights_form_of_many_experts(gpu, E, cfg):
+    """Experts ranked by their rows, one a lane, up to 64 of them, and more than that: equal ones, one that
+    has all rows, and uneven ones, where there are big tiles, quarters and edges."""
+    rng = np.random.default_rng(E)
+    one = np.zeros(E, dtype=np.int64)
+    one[E // 2] = 700
+    for name, counts in (("equal", np.full(E, 33)), ("one", one), ("uneven", uneven(E, 1)), ("longest first", -np.sort(-uneven(E, 2))),
+                         ("longest last", np.sort(uneven(E, 3)))):
+        offsets, rows = groups(counts, 3)
+        for N, M in ((520, 1000), (264, 136)) if name == "uneven" else ((520, 1000),) if E < 100 else ((264, 392),):
+            print(f"E {E} cfg {cfg} {name} {rows} rows {M} x {N}", flush=True)
+            got, want = exact_product("tn", rng, offsets, rows, N, M, cfg)
+            assert np.array_equal(got, want), (name, M, N)
