@@ -133,3 +133,71 @@ def test_weights_form_of_many_experts(gpu, E, cfg):
             print(f"E {E} cfg {cfg} {name} {rows} rows {M} x {N}", flush=True)
             got, want = exact_product("tn", rng, offsets, rows, N, M, cfg)
             assert np.array_equal(got, want), (name, M, N)
+
+
+def padded(gpu, x, ld, value=float("nan")):
+    """x in rows of ld elements, all around it `value`."""
+    rows, cols = x.shape
+    buf = gpu.full((rows + 2, ld), value, dtype=gpu.float16, device="cuda")
+    view = buf[1:rows + 1, :cols]
+    view.copy_(to_dev(x))
+    return view
+
+
+EVERY = [None, tg.EXPERT_GENERIC, tg.EXPERT_32, tg.EXPERT_64, tg.EXPERT_128, tg.EXPERT_256, tg.EXPERT_TILES]
+
+
+@pytest.mark.parametrize("poison", [False, True], ids=["product", "poisoned"])
+@pytest.mark.parametrize("cfg", EVERY, ids=lambda c: f"cfg{c}")
+@pytest.mark.parametrize("form", ["nt", "nn"])
+def test_nothing_past_an_operands_end_is_multiplied(gpu, form, cfg, poison):
+    """NaN behind every row's end, before the first row and behind the last, and in the rows of no expert:
+    one that either operand let in would show, as the other's zeros do not hide it."""
+    library = tg.debugfill_lib() if poison else None
+    rng = np.random.default_rng(7)
+    counts = [33, 0, 129, 300, 1]
+    offsets, rows = groups(counts, 6)
+    E = len(counts)
+    for N, K in ((8, 8), (40, 64), (136, 72), (264, 200), (520, 40)) + (((37, 61), (130, 3)) if cfg in (None, tg.EXPERT_GENERIC) else ()):
+        a = small_ints(rng, rows, K).astype(np.float64)
+        b = small_ints(rng, E, N, K) if form == "nt" else small_ints(rng, E, K, N)
+        want, _ = ref.products(a, b, offsets, form == "nt", np.full((rows, N), 7.0))
+        a[offsets[-1]:] = np.nan
+        pad = 8 if K % 8 == 0 and N % 8 == 0 else 3
+        r, c = b.shape[1:]
+        buf = gpu.full((E, r + 2, c + pad), float("nan"), dtype=gpu.float16, device="cuda")
+        bv = buf[:, 1:r + 1, :c]
+        bv.copy_(to_dev(b))
+        out = gpu.full((rows, N), 7.0, dtype=gpu.float16, device="cuda")
+        tg.expert_gemm_f16(padded(gpu, a.astype(np.float16), K + pad), bv, to_dev(offsets), out, trans_b=form == "nt", cfg=cfg,
+                           library=library)
+        assert np.array_equal(out.cpu().numpy(), ref.to_half(want)), (N, K)
+
+
+@pytest.mark.parametrize("poison", [False, True], ids=["product", "poisoned"])
+@pytest.mark.parametrize("cfg", [c for c in EVERY if c not in ROWS_ONLY], ids=lambda c: f"cfg{c}")
+def test_a_nan_stays_in_its_expert_of_the_weights_form(gpu, cfg, poison):
+    """Every other expert's rows NaN in one operand or both, and all around the operands: the experts between
+    are exact, and the others' results NaN."""
+    library = tg.debugfill_lib() if poison else None
+    rng = np.random.default_rng(8)
+    counts = [5, 33, 0, 64, 7, 129, 300, 20, 63, 31]
+    offsets, rows = groups(counts, 6)
+    E = len(counts)
+    for M, N in ((8, 8), (40, 264), (136, 520), (392, 72)) + (((37, 61),) if cfg in (None, tg.EXPERT_GENERIC) else ()):
+        a, b = small_ints(rng, rows, M), small_ints(rng, rows, N)
+        want = ref.to_half(ref.products_tn(a, b, offsets))
+        pad = 8 if M % 8 == 0 and N % 8 == 0 else 3
+        for dirty in ("a", "b", "both"):
+            av, bv = padded(gpu, a, M + pad), padded(gpu, b, N + pad)
+            for e in range(0, E, 2):
+                lo, hi = int(offsets[e]), int(offsets[e + 1])
+                if dirty != "b":
+                    av[lo:hi] = float("nan")
+                if dirty != "a":
+                    bv[lo:hi] = float("nan")
+            av[int(offsets[-1]):], bv[int(offsets[-1]):] = float("nan"), float("nan")
+            got = tg.expert_gemm_f16_tn(av, bv, to_dev(offsets), cfg=cfg, library=library).cpu().numpy()
+            assert np.array_equal(got[1::2], want[1::2]), (M, N, dirty)
+            for e in range(0, E, 2):
+                assert np.isnan(got[e]).all() if counts[e] else (got[e] == 0).all()
