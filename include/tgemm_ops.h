@@ -196,7 +196,8 @@ TGEMM_API int expert_sort(int64_t tokens, int64_t k, int64_t experts, const void
  * Rows out to their places: XS[place[t, j], :] = X[t, :] for every slot (X tokens x H, XS rows x H,
  * binary16). A place outside [0, rows) is skipped, two slots with one place leave one of their rows.
  * With offsets (experts + 1 int32, as expert_sort writes them) the rows of XS behind
- * offsets[experts] are set to zero; with NULL they are left as they were.
+ * offsets[experts] are set to zero; with NULL they are left as they were, as are rows before
+ * offsets[experts] that no slot has.
  */
 TGEMM_API int expert_gather_f16(int64_t tokens, int64_t k, int64_t rows, int64_t H, const void* X, int64_t ldx,
                                 const void* place, void* XS, int64_t ldxs, const void* offsets, int64_t experts,
@@ -215,7 +216,8 @@ TGEMM_API int expert_combine_f16(int64_t tokens, int64_t k, int64_t rows, int64_
 /*
  * Its gradient: dY[place[t, j], :] = weights[t, j] * dOUT[t, :] and dweights[t, j] = <dOUT[t, :],
  * Y[place[t, j], :]> (of w_dtype; 0 for a slot of no place), either NULL where it is not wanted (Y is
- * read for dweights only). Rows of dY of no slot as for expert_gather_f16.
+ * read for dweights only). Rows of dY behind offsets[experts] as for expert_gather_f16; rows before it
+ * that no slot has are left as they were.
  */
 TGEMM_API int expert_combine_f16_backward(int64_t tokens, int64_t k, int64_t rows, int64_t H, const void* dOUT,
                                           int64_t lddo, const void* Y, int64_t ldy, const void* place,

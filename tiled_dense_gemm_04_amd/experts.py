@@ -43,7 +43,10 @@ SIGNATURES = {
 
 class ExpertOrder(NamedTuple):
     """Where the slots of (T, k) ids go: ``offsets`` (experts + 1), ``order`` (T k: the slot of each
-    sorted row, -1 behind the last) and ``place`` (T, k: each slot's row, -1 for none), int32."""
+    sorted row, -1 behind the last) and ``place`` (T, k: each slot's row, -1 for none), int32. The autograd
+    functions take it as ``expert_sort`` wrote it, where each of the offsets[-1] rows in use has its slot: rows
+    that lost theirs to a change of ``place`` are not written, and a gradient is summed over them. To leave
+    slots out, give them an id of no expert before sorting."""
     offsets: "torch.Tensor"  # noqa: F821
     order: "torch.Tensor"    # noqa: F821
     place: "torch.Tensor"    # noqa: F821
@@ -294,8 +297,8 @@ def autograd_functions():
             return dx, None, None, None
 
     class ExpertCombineFunction(torch.autograd.Function):
-        """(y, weights or None, *plan) -> the tokens' weighted sums; gradients of the rows (zero for rows
-        of no slot) and of the weights."""
+        """(y, weights or None, *plan) -> the tokens' weighted sums; gradients of the rows (zero behind the
+        last one in use) and of the weights (zero for a slot of no expert)."""
 
         @staticmethod
         def forward(ctx, y, weights, offsets, order, place):
