@@ -1,8 +1,9 @@
-// Calls an entry point of the expert layer with the host code of its kernels' file linked in, and
-// the HIP runtime replaced by one that records launches: no GPU, no HIP runtime library. Prints the
-// return code, then a line per launch: the kernel, its workgroups, and the count of `main` workgroups
-// that kernels of rows take as their second argument.
+// Calls an entry point of the expert layer or the norm with the host code of its kernels' file linked
+// in, and the HIP runtime replaced by one that records launches: no GPU, no HIP runtime library. Prints
+// a line per launch, the kernel, its workgroups, and the count of `main` workgroups that the expert layer's
+// kernels take as their second argument, then the return code.
 //   driver gather TOKENS K ROWS H X PLACE XS OFFSETS EXPERTS      (pointers as numbers; never read)
+//   driver norm ROWS K RESIDUAL_DTYPE(-1: none) Y Q
 //   driver rows FIRST ROWS N          (no entry point: the rows that a zeroing workgroup goes over, one a line)
 //   driver k_tiles K BK               (no entry point: the k-tiles of a product, and k values in the last)
 //   driver combine_grad TOKENS K ROWS H DOUT Y PLACE DY OFFSETS EXPERTS
@@ -54,7 +55,9 @@ hipError_t __hipPopCallConfiguration(dim3* grid, dim3* block, size_t* lds, hipSt
   return hipSuccess;
 }
 hipError_t hipLaunchKernel(const void* f, dim3 grid, dim3, void** args, size_t, hipStream_t) {
-  std::printf("%s %u %u\n", kernels()[f].c_str(), grid.x, *static_cast<const uint32_t*>(args[1]));
+  const std::string& name = kernels()[f];
+  const bool of_rows = name.find("expert_") != std::string::npos;
+  std::printf("%s %u %u\n", name.c_str(), grid.x, of_rows ? *static_cast<const uint32_t*>(args[1]) : 0u);
   return hipSuccess;
 }
 hipError_t hipGetLastError() { return hipSuccess; }
@@ -79,6 +82,14 @@ int main(int argc, char** argv) {
     rc = expert_combine_f16_backward(number(argv[2]), number(argv[3]), number(argv[4]), H, pointer(argv[6]), ld, pointer(argv[7]),
                                      ld, pointer(argv[8]), nullptr, TGEMM_DTYPE_F32, pointer(argv[9]), ld, nullptr,
                                      pointer(argv[10]), number(argv[11]), nullptr);
+  } else if (argc == 7 && !std::strcmp(argv[1], "norm")) {
+    const int64_t K = number(argv[3]);
+    const int dtype = (int)number(argv[4]);
+    void* const some = reinterpret_cast<void*>(256);
+    void* const residual = dtype < 0 ? nullptr : some;
+    void* const q = pointer(argv[6]);
+    rc = rmsnorm_f16(number(argv[2]), K, some, K, residual, K, dtype, some, TGEMM_DTYPE_F16, 1e-6f, residual, K, pointer(argv[5]), K,
+                     q, K, static_cast<float*>(q), nullptr);
   } else if (argc == 5 && !std::strcmp(argv[1], "rows")) {
     tgemm::every_nth_row(number(argv[2]), number(argv[3]), number(argv[4]), [](int64_t r) { std::printf("row %lld 0\n", (long long)r); });
   } else if (argc == 4 && !std::strcmp(argv[1], "k_tiles")) {

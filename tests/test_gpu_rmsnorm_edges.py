@@ -5,6 +5,7 @@ import pytest
 
 import norm_reference as ref
 from gpu_util import to_dev, torch_cuda
+from test_gpu_rmsnorm import check_codes, check_y
 
 import tiled_dense_gemm_04_amd as tg
 
@@ -108,3 +109,25 @@ def test_gradient_of_many_rows(gpu, R, K, turns, at_once, residual):
     xhat = h[-1].astype(np.float64) / np.sqrt((h[-1].astype(np.float64) ** 2).mean() + EPS)
     assert (np.abs(dy[-1] * xhat) > size * 2.0 ** -16 + (0.0 if w.dtype == np.float32 else 1.0) * np.abs(dw) * ref.HALF16).any()
     assert all(gpu.equal(a, b) for a, b in zip(got, grads()))  # sums in a fixed order
+
+
+@pytest.mark.parametrize("residual", [np.float16, np.float32], ids=lambda r: r.__name__)
+@pytest.mark.parametrize("rows", [2047, 2048])
+def test_rows_of_six_waves(gpu, rows, residual):
+    """Both sides of the choice of six waves a row: every row end, strided and in place, y and codes."""
+    for K in (2559, *range(2560, 2569), 3000, 3064, 3071, 3073):
+        rng = np.random.default_rng(K)
+        x = rng.standard_normal((rows, K), dtype=np.float32).astype(np.float16)
+        r = (3 * rng.standard_normal((rows, K), dtype=np.float32)).astype(residual)
+        w = (1 + 0.2 * rng.standard_normal(K)).astype(np.float32 if K % 2 else np.float16)
+        h = ref.stored(x, r)
+        xd, wd = to_dev(x), to_dev(w)
+        wide = gpu.full((rows, K + 5), 7.0, dtype=to_dev(r).dtype, device="cuda")
+        wide[:, 3:K + 3] = to_dev(r)
+        out = gpu.full((rows, K + 3), 5.0, dtype=gpu.float16, device="cuda")
+        q, s, coded = tg.rmsnorm_fp8_block(xd, wd, wide[:, 3:K + 3], eps=EPS)
+        tg.rmsnorm(xd, wd, wide[:, 3:K + 3], eps=EPS, out=out[:, 1:K + 1], residual_out=wide[:, 3:K + 3])
+        check_y(out[:, 1:K + 1], h, w)
+        check_codes(q, s, h, w)
+        assert np.array_equal(wide[:, 3:K + 3].cpu().numpy(), h) and np.array_equal(coded.cpu().numpy(), h), K
+        assert (wide[:, :3] == 7).all() and (wide[:, K + 3:] == 7).all() and (out[:, 0] == 5).all() and (out[:, K + 1:] == 5).all()

@@ -1,5 +1,5 @@
-"""What the expert layer's entry points launch, on the CPU: the host code of the kernels' file and of
-its entry points, linked with a HIP runtime that only records launches (tests/host_launch/)."""
+"""What the expert layer's and the norm's entry points launch, on the CPU: the host code of the kernels'
+files and of the entry points, linked with a HIP runtime that only records launches (tests/host_launch/)."""
 import os
 import subprocess
 
@@ -22,11 +22,12 @@ def driver(tmp_path_factory):
         pytest.skip(str(e))
     out = str(tmp_path_factory.mktemp("host_launch"))
     include = ["-I" + os.path.join(ROOT, "include"), "-I" + CSRC]
-    kernels = os.path.join(out, "expert.o")
-    for cmd in ([hipcc, "--offload-arch=" + libbuild.ARCH, "--offload-host-only", "-std=c++17", "-O1", *include, "-c",
-                 os.path.join(CSRC, "tgemm_expert.hip"), "-o", kernels],
+    kernels = [os.path.join(out, name + ".o") for name in ("tgemm_expert", "tgemm_norm")]
+    for cmd in (*([hipcc, "--offload-arch=" + libbuild.ARCH, "--offload-host-only", "-std=c++17", "-O1", *include, "-c",
+                   os.path.join(CSRC, os.path.basename(o)[:-1] + "hip"), "-o", o] for o in kernels),
                 ["/opt/rocm/llvm/bin/clang++", "-std=c++17", "-O1", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", *include,
-                 os.path.join(CSRC, "tgemm_expert_api.cpp"), os.path.join(HERE, "driver.cpp"), kernels,
+                 os.path.join(CSRC, "tgemm_expert_api.cpp"), os.path.join(CSRC, "tgemm_norm_api.cpp"),
+                 os.path.join(HERE, "driver.cpp"), *kernels,
                  "-Wl,--unresolved-symbols=ignore-all",  # (the device code's image, whose name is the compiler's)
                  "-o", os.path.join(out, "driver")]):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -78,3 +79,21 @@ def test_k_tiles_of_the_longest_sums(driver):
         for BK in (32, 64):
             nk = -(-K // BK)
             assert driver("k_tiles", K, BK)[1] == [("k_tiles", nk, K - (nk - 1) * BK if nk else 0)]
+
+
+def test_waves_of_the_norm(driver):
+    """Six waves a row only for the widths, rows and outputs for which they measured faster."""
+    def threads(rows, K, dtype, y, q):
+        rc, launches = driver("norm", rows, K, dtype, y, q)
+        assert rc == tg.TGEMM_OK and len(launches) == 1
+        return int(launches[0][0].split("rmsnorm_rowsILi")[1].split("E")[0])
+
+    for K in (2560, 2561, 3000, 384 * 8):
+        for rows in (2048, 4095, 1 << 23):
+            assert threads(rows, K, 1, P, 0) == 384 and threads(rows, K, 1, 0, P) == 384 and threads(rows, K, 0, P, 0) == 384
+            assert threads(rows, K, 0, 0, P) == 256 and threads(rows, K, 0, P, P) == 256
+            assert threads(rows, K, -1, P, 0) == 256 and threads(rows, K, -1, 0, P) == 256
+        for rows in (1, 2047, (1 << 23) + 1):
+            assert threads(rows, K, 1, P, 0) == 256 and threads(rows, K, 0, P, 0) == 256
+    for K in (2559, 384 * 8 + 1, 2049, 4096):
+        assert threads(4095, K, 1, P, 0) == 256

@@ -301,9 +301,19 @@ hipError_t launch_rows(const NormArgs& g, hipStream_t s) {
 template <int RES>
 hipError_t launch_forward(const NormArgs& g, hipStream_t s) {
 #define TGEMM_NORM_LAUNCH(TPR, CH) (launch_rows<TPR, CH, RES>(g, s))
-  // (six waves of one chunk: 4095 x 3000 with a float32 residual 31.7 us in four waves of two, so 29.2; 16384 x
-  // 3000 116 and 110; but 16384 x 2049 with a binary16 one 59 and 68. The runtime takes fewer than 2^32 threads.)
-  if (g.K >= 2560 && g.K <= 384 * 8 && g.R <= (1 << 23)) return launch_rows<384, 1, RES>(g, s);
+  // Six waves of one chunk (a row's threads all busy, but a third fewer rows in flight) instead of four waves of two,
+  // where a residual is written beside y. Rows of 2560, 2816 and 3064 values, four and six waves, us:
+  //   float32 residual      4095 rows 28.4 27.5, 31.1 29.5, 34.8 32.5;  16384 92.9 90.2, 103.5 99.4, 117.4 110.7
+  //   and codes             4095      26.9 26.6, 29.8 28.5, 32.5 31.2;  16384 86.7 85.3, 95.9 93.6, 109.4 105.0
+  //   binary16 residual     4095      15.9 15.0, 18.3 18.1, 21.1 21.0;  16384 62.7 60.5, 69.3 66.5, 77.1 73.1
+  //   and codes (not taken) 4095      16.8 16.2, 18.3 17.6, 19.8 19.9;  16384 59.0 64.0, 63.2 67.6, 70.2 70.8
+  //   none (not taken)      4095      10.3 11.0, 10.9 11.5, 11.4 11.9;  16384 36.0 42.9, 38.4 45.8, 42.3 47.2
+  // 2100 rows with a float32 residual 17.7 17.4, 19.0 18.5, 21.2 20.2, but 1800 15.0 15.4, 16.0 16.3, 17.9 18.0, and
+  // 16384 x 2304 with a binary16 one 57.8 57.8. (The runtime takes fewer than 2^32 threads.)
+  if constexpr (RES != kResNone) {
+    if ((RES == kResF32 || g.Q == nullptr) && g.K >= 2560 && g.K <= 384 * 8 && g.R >= 2048 && g.R <= (1 << 23))
+      return launch_rows<384, 1, RES>(g, s);
+  }
   TGEMM_NORM_SHAPES(TGEMM_NORM_LAUNCH, g.K)
 #undef TGEMM_NORM_LAUNCH
 }
