@@ -837,8 +837,8 @@ from . import norm  # noqa: E402
 from .norm import NORM_MAX_K, rmsnorm, rmsnorm_fp8_block  # noqa: E402,F401
 from . import experts  # noqa: E402
 from .experts import (EXPERT_32, EXPERT_64, EXPERT_128, EXPERT_256, EXPERT_GENERIC, EXPERT_TILES, MAX_EXPERTS,  # noqa: E402,F401
-                      MAX_SLOTS, ExpertOrder,                      expert_combine, expert_gather, expert_gemm_f16, expert_gemm_f16_tn, expert_gemm_select_config,
-                      expert_sort)
+                      MAX_SLOTS, ExpertOrder, expert_combine, expert_gather, expert_gemm_f16, expert_gemm_f16_tn,
+                      expert_gemm_select_config, expert_sort)
 
 OPS_SIGNATURES = {**mxfp4.SIGNATURES, **newton_schulz.SIGNATURES, **norm.SIGNATURES, **experts.SIGNATURES}
 # Every symbol include/tgemm_ops.h declares.
