@@ -257,8 +257,9 @@ __global__ __launch_bounds__(kSortThreads) void expert_sort_place(ExpertSortArgs
 // ------------------------------------------------------------------------------------
 // Rows. A thread holds eight columns of a token: reads them once and writes them to every place of
 // the token (gather), or sums the token's rows there in float32, choice by choice (combine). Bound
-// by memory: 16384 tokens, 4 choices, 4096 columns (671 MB) gathered in 105 us (6.4 TB/s), combined in 139
-// (4.8: a token's rows lie far apart; two tokens a thread are slower); 4095 x 8 x 2048 (151 MB) 27 and 29.
+// by memory: 16384 tokens, 4 choices, 4096 columns (671 MB) gathered in 107 us after other work and 118 to 122
+// in a loop (5.5 to 6.3 TB/s), combined in 144 and 122 to 125 (4.7 to 5.5; a token's rows lie far apart, and two
+// tokens a thread are slower); 4095 x 8 x 2048 (151 MB) 27 and 29.
 // The workgroups past `main` zero the rows behind the last one in use.
 __device__ __forceinline__ int rows_in_use(const ExpertRowsArgs& g) {
   const int n = g.offsets[g.experts];
@@ -332,8 +333,8 @@ __global__ __launch_bounds__(256) void expert_combine(ExpertRowsArgs g) {
 }
 
 // A wave per slot: its row of dY is written and its product with Y's summed in one pass (a token's
-// slots are neighbouring waves, which share dout's row in the caches): 16384 x 4 x 4096 (1.2 GB) in 222 us,
-// 5.4 TB/s.
+// slots are neighbouring waves, which share dout's row in the caches): 16384 x 4 x 4096 (1.2 GB) in 223 us after
+// other work and 234 to 257 in a loop, 4.7 to 5.4 TB/s.
 __global__ __launch_bounds__(256) void expert_combine_grad(ExpertRowsArgs g, uint32_t main) {
   const uint32_t cpr = ((uint32_t)g.H + 7) / 8;
   if (blockIdx.x >= main) return zero_rest_rows(g, (int)(blockIdx.x - main), cpr);

@@ -9,8 +9,8 @@
 // past the last tile leave at once (or zero the rows behind the last group). Offsets are clamped to [0,
 // rows]: no value of theirs leads outside the operands.
 // What bounds them: the binary16 MFMAs at their power limit and the rounds of tiles (uneven experts, 16384
-// rows on 16 of them, 4096 x 2048: rows' form 281 us with B N x K and 266 with K x N, weights' form 284, of
-// 275 GFLOP; one expert 264, the dense kernel of this library 271); with few rows an expert, reading the
+// rows on 16 of them, 4096 x 2048: rows' form 281 to 304 us with B N x K, by the box, and 266 with K x N, weights'
+// form 281 to 284, of 275 GFLOP; one expert 264, the dense kernel of this library 271); with few rows an expert, reading the
 // weights (64 rows on 64 experts of 2048 x 4096, about 36 of them met: 109 us, 5.5 TB/s).
 #include "tgemm_expert.h"
 #include "tgemm_pingpong.h"
@@ -430,7 +430,9 @@ __global__ __launch_bounds__(512) void expert_tiles(ExpertGemmArgs args) {
 // 170 (measured: 4 us and 0.024 a row, 4 us and 0.0072 a row); q is what makes least the tiles' time spread
 // over the compute units plus half of the longest one's. (A workgroup per tile, which the hardware
 // hands to the next free compute unit, costs 5 us more a tile: 16384 rows, 16 experts, 2048 x 1024: 99 to
-// 123 us.) More than 64 experts are taken as they come, in big tiles.
+// 123 us.) More than 64 experts, which one lane each cannot rank, are taken as they come, in big tiles: equal
+// experts lose little by it (16384 rows, 2048 x 1024: 64 of them 118 us, 65 124), uneven ones a fifth to a third
+// (134 and 161; 1024 x 512: 40 and 55), 128 of them 213 us where their bytes take 123.
 struct WeightTiles {
   uint32_t total, q;
   int expert[64];                                      // of rank r, most rows first
