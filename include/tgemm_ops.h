@@ -197,7 +197,7 @@ TGEMM_API int expert_sort(int64_t tokens, int64_t k, int64_t experts, const void
  * binary16). A place outside [0, rows) is skipped, two slots with one place leave one of their rows.
  * With offsets (experts + 1 int32, as expert_sort writes them) the rows of XS behind
  * offsets[experts] are set to zero; with NULL they are left as they were, as are rows before
- * offsets[experts] that no slot has.
+ * offsets[experts] that no slot has. With k = 0 X and place are not read and may be NULL.
  */
 TGEMM_API int expert_gather_f16(int64_t tokens, int64_t k, int64_t rows, int64_t H, const void* X, int64_t ldx,
                                 const void* place, void* XS, int64_t ldxs, const void* offsets, int64_t experts,

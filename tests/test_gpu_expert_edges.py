@@ -73,7 +73,9 @@ def test_combine_keeps_its_rows_for_the_weights_gradient_only(gpu):
     full = [y.clone().requires_grad_(), w.clone().requires_grad_()]
     out, kept = saved_by(gpu, lambda: tg.ExpertCombineFunction.apply(*full, *plan))
     assert (T * k, H) in kept
-    dy, dw = gpu.autograd.grad(out, full, dout)
+    dy, dw = gpu.autograd.grad(out, full, dout, retain_graph=True)
+    for leaf, want in zip(full, (dy, dw)):  # more kept than the one gradient reads
+        assert gpu.equal(gpu.autograd.grad(out, leaf, dout, retain_graph=True)[0], want)
     rows = y.clone().requires_grad_()
     inner = rows * 1
     out, kept = saved_by(gpu, lambda: tg.ExpertCombineFunction.apply(inner, w, *plan))
@@ -96,7 +98,9 @@ def test_products_keep_an_operand_for_the_others_gradient_only(gpu):
     both = [a.clone().requires_grad_(), b.clone().requires_grad_()]
     out, kept = saved_by(gpu, lambda: tg.ExpertGemmFunction.apply(*both, offsets))
     assert kept == sorted([(E + 1,), (rows, K), (E, N, K)])
-    da, db = gpu.autograd.grad(out, both, dc)
+    da, db = gpu.autograd.grad(out, both, dc, retain_graph=True)
+    for leaf, want in zip(both, (da, db)):
+        assert gpu.equal(gpu.autograd.grad(out, leaf, dc, retain_graph=True)[0], want)
     out, kept = saved_by(gpu, lambda: tg.ExpertGemmFunction.apply(both[0], b, offsets))
     assert kept == sorted([(E + 1,), (E, N, K)])
     assert gpu.equal(gpu.autograd.grad(out, both[0], dc)[0], da)
